@@ -11,6 +11,7 @@ or ``__graft_entry__.build()``); importing this module without it raises.
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
 
 import torch  # loads the HIP runtime the library binds to (same soname)
@@ -24,6 +25,11 @@ FP8_PAGE_KEY_BYTES = PAGE_POSITIONS * HEAD_DIM          # 8192
 FP8_PAGE_SCALE_BYTES = PAGE_POSITIONS * 4               # 256
 FP8_FUSED_PAGE_BYTES = FP8_PAGE_KEY_BYTES + FP8_PAGE_SCALE_BYTES  # 8448
 BF16_PAGE_BYTES = PAGE_POSITIONS * HEAD_DIM * 2         # 16384
+LATENT_DIM = 512
+
+IDX_NORM_OFF = 1
+IDX_ROPE_LEADING = 2
+IDX_ROPE_HALVES = 4
 
 IDX_OK = 0
 IDX_ERR_NULL = -1
@@ -42,6 +48,11 @@ _SYMBOLS = (
     "idx_paged_mqa_topk_bf16",
     "idx_store_keys_fp8",
     "idx_store_keys_bf16",
+    "idx_norm_rope",
+    "idx_norm_rope_store_fp8",
+    "idx_norm_rope_store_bf16",
+    "idx_load_slots_fp8",
+    "idx_load_slots_bf16",
     "idx_status_string",
     "idx_abi_version",
 )
@@ -91,6 +102,17 @@ def _load() -> ctypes.CDLL:
         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
         ctypes.c_int64, ctypes.c_void_p]
     lib.idx_store_keys_bf16.restype = ctypes.c_int
+    ptr, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    rotation = [i32, i32, ctypes.c_uint32, ctypes.c_float, i64]  # head_dim, rope_dim, flags, eps, row stride
+    for name, types in (
+            ("idx_norm_rope", [ptr] * 5 + [i64, i32] + rotation + [ptr]),
+            ("idx_norm_rope_store_fp8", [ptr] * 5 + [i64] + rotation + [ptr, ptr, i64, i64, i64, ptr]),
+            ("idx_norm_rope_store_bf16", [ptr] * 5 + [i64] + rotation + [ptr, i64, i64, ptr]),
+            ("idx_load_slots_fp8", [ptr] * 3 + [i64, i32, i64, i64, i64, ptr, i64, ptr]),
+            ("idx_load_slots_bf16", [ptr] * 2 + [i64, i32, i64, i64, ptr, i64, ptr])):
+        fn = getattr(lib, name)
+        fn.argtypes = types
+        fn.restype = ctypes.c_int
     lib.idx_status_string.argtypes = [ctypes.c_int]
     lib.idx_status_string.restype = ctypes.c_char_p
     lib.idx_abi_version.argtypes = []
@@ -394,10 +416,190 @@ def idx_store_keys_bf16(keys, slots, kv_pages, *, num_pages, n=None, kv_page_str
     return status
 
 
+def _device_of(named) -> torch.device | None:
+    """The one device of a call's tensors ((name, tensor or address) pairs)."""
+    dev = None
+    for name, x in named:
+        if isinstance(x, torch.Tensor):
+            if x.device.type != "cuda":
+                raise ValueError("tensors passed to the indexer library must be device tensors")
+            if dev is None:
+                dev = x.device
+            elif x.device != dev:
+                raise ValueError(f"{name} is on {x.device}, the arguments before it on {dev}")
+    return dev
+
+
+def _launch(name, dev, stream, check, *args) -> int:
+    """Calls the library with ``args`` and the stream, on the tensors' device
+    (whatever the current one is)."""
+    fn, handle = getattr(_lib, name), _stream_handle(stream, dev)
+    if dev is None or dev.index == torch.cuda.current_device():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if check and status != IDX_OK:
+        raise IdxError(status, f"{name}: {idx_status_string(status)}")
+    return status
+
+
+def _check_rows(name, x, dim, width=None) -> None:
+    """A bf16 tensor of ``dim`` dims whose rows (all dims but the first) are
+    dense; the first dim's stride is free."""
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {x.dtype}")
+    if x.dim() != dim or (width is not None and x.shape[-1] != width):
+        raise ValueError(f"{name} must have {dim} dims" + ("" if width is None else f", the last of {width}")
+                         + f", got {tuple(x.shape)}")
+    dense = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size > 1 and stride != dense:
+            raise ValueError(f"{name} must be dense behind its first dim")
+        dense *= size
+
+
+def _row_stride(x) -> int:
+    """Elements between the rows of a tensor checked by ``_check_rows``."""
+    return x.stride(0) if x.shape[0] > 1 else math.prod(x.shape[1:])
+
+
+def _rotation(x, positions, inv_freq, weight, norm, leading, halves):
+    """Checks the norm and rotation's arguments; (head_dim, rope_dim, flags)."""
+    n, head_dim = x.shape[0], x.shape[-1]
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    _check("positions", positions, torch.int64)
+    _check("inv_freq", inv_freq, torch.float32)
+    _check("weight", weight, torch.float32)
+    if positions is not None and positions.shape != (n,):
+        raise ValueError(f"positions must be [{n}], got {list(positions.shape)}")
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have one dim")
+    if weight is not None and weight.shape != (head_dim,):
+        raise ValueError(f"weight must be [{head_dim}], got {list(weight.shape)}")
+    if weight is not None and not norm:
+        raise ValueError("weight goes with the norm")
+    flags = (0 if norm else IDX_NORM_OFF) | (IDX_ROPE_LEADING if leading else 0) | (IDX_ROPE_HALVES if halves else 0)
+    return head_dim, 0 if inv_freq is None else 2 * inv_freq.shape[0], flags
+
+
+def _check_pool(kv_pages, kscale, num_pages, page_bytes, kv_page_stride, kscale_page_stride) -> None:
+    """A pool given as tensors must hold the pages (``page_bytes`` of values
+    each) that it is said to hold."""
+    if isinstance(kv_pages, torch.Tensor):
+        if not kv_pages.is_contiguous():
+            raise ValueError("kv_pages must be contiguous")
+        if num_pages > 0 and kv_pages.numel() * kv_pages.element_size() < (num_pages - 1) * kv_page_stride + page_bytes:
+            raise ValueError(f"kv_pages is shorter than {num_pages} pages of {kv_page_stride} bytes")
+    if isinstance(kscale, torch.Tensor):
+        _check("kscale", kscale, torch.float32)
+        if num_pages > 0 and kscale.numel() * 4 < (num_pages - 1) * kscale_page_stride + 4 * PAGE_POSITIONS:
+            raise ValueError(f"kscale is shorter than {num_pages} pages of {kscale_page_stride} bytes")
+
+
+def _check_slots(slots, n) -> None:
+    _check("slots", slots, torch.int64)
+    if isinstance(slots, torch.Tensor) and slots.shape != (n,):
+        raise ValueError(f"slots must be [{n}], got {list(slots.shape)}")
+
+
+def idx_norm_rope(x, positions, inv_freq, out, *, weight=None, eps=1e-6, norm=True, leading=False,
+                  halves=False, stream=None, check=True) -> int:
+    """RMS norm (times ``weight``) and rotation of the vectors of bf16 ``x``
+    [n, heads, D] (D 64, 128, 256 or 512; the first dim may be strided), head by
+    head, into bf16 ``out`` (contiguous; may be ``x``).
+
+    Token t's rotated values (the last 2*len(inv_freq) of D, or the first with
+    ``leading``; neighbours, or halves with ``halves``) turn by positions[t] *
+    inv_freq[j].  ``positions`` int64 [n] and ``inv_freq`` fp32; both None: no
+    rotation.  ``norm=False``: only the rotation.
+    """
+    _check_rows("x", x, 3)
+    _check("out", out, torch.bfloat16)
+    if out.shape != x.shape:
+        raise ValueError(f"out must be {list(x.shape)}, got {list(out.shape)}")
+    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
+    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight), ("out", out)))
+    return _launch("idx_norm_rope", dev, stream, check, _addr(x), _addr(weight), _addr(positions), _addr(inv_freq),
+                   _addr(out), x.shape[0], x.shape[1], head_dim, rope_dim, flags, eps, _row_stride(x))
+
+
+def idx_norm_rope_store_fp8(x, positions, inv_freq, slots, kv_pages, kscale, *, num_pages, weight=None,
+                            eps=1e-6, norm=True, leading=False, halves=False, kv_page_stride=None,
+                            kscale_page_stride=None, stream=None, check=True) -> int:
+    """Norm and rotation (as :func:`idx_norm_rope`) of bf16 vectors [n, D] (D 128:
+    index keys, 512: latents), quantised (scale = amax/448, e4m3fn codes) into
+    pool slots in the same pass.
+
+    ``slots`` int64 [n] (64*page + position; out of range skips the token).  The
+    strides default to the fused block of 64*D + 256 bytes; ``kscale`` is a
+    tensor or a device address (fused block: kv_pages + 64*D).
+    """
+    _check_rows("x", x, 2)
+    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
+    fused = PAGE_POSITIONS * (head_dim + 4)
+    kv_page_stride = fused if kv_page_stride is None else kv_page_stride
+    kscale_page_stride = fused if kscale_page_stride is None else kscale_page_stride
+    _check_slots(slots, x.shape[0])
+    _check_pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * head_dim, kv_page_stride, kscale_page_stride)
+    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight),
+                      ("slots", slots), ("kv_pages", kv_pages), ("kscale", kscale)))
+    return _launch("idx_norm_rope_store_fp8", dev, stream, check, _addr(x), _addr(weight), _addr(positions),
+                   _addr(inv_freq), _addr(slots), x.shape[0], head_dim, rope_dim, flags, eps, _row_stride(x),
+                   _addr(kv_pages), _addr(kscale), num_pages, kv_page_stride, kscale_page_stride)
+
+
+def idx_norm_rope_store_bf16(x, positions, inv_freq, slots, kv_pages, *, num_pages, weight=None, eps=1e-6,
+                             norm=True, leading=False, halves=False, kv_page_stride=None, stream=None,
+                             check=True) -> int:
+    """bf16 counterpart of :func:`idx_norm_rope_store_fp8`: pages of 128*D bytes."""
+    _check_rows("x", x, 2)
+    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
+    kv_page_stride = 2 * PAGE_POSITIONS * head_dim if kv_page_stride is None else kv_page_stride
+    _check_slots(slots, x.shape[0])
+    _check_pool(kv_pages, None, num_pages, 2 * PAGE_POSITIONS * head_dim, kv_page_stride, 0)
+    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight),
+                      ("slots", slots), ("kv_pages", kv_pages)))
+    return _launch("idx_norm_rope_store_bf16", dev, stream, check, _addr(x), _addr(weight), _addr(positions),
+                   _addr(inv_freq), _addr(slots), x.shape[0], head_dim, rope_dim, flags, eps, _row_stride(x),
+                   _addr(kv_pages), num_pages, kv_page_stride)
+
+
+def idx_load_slots_fp8(kv_pages, kscale, slots, out, *, num_pages, kv_page_stride=None,
+                       kscale_page_stride=None, stream=None, check=True) -> int:
+    """out[t] = bf16(code * scale) of pool slot slots[t], for bf16 ``out`` [n, D]
+    (D 128 or 512; rows may be strided).  A slot out of range leaves its row."""
+    _check_rows("out", out, 2)
+    head_dim = out.shape[1]
+    fused = PAGE_POSITIONS * (head_dim + 4)
+    kv_page_stride = fused if kv_page_stride is None else kv_page_stride
+    kscale_page_stride = fused if kscale_page_stride is None else kscale_page_stride
+    _check_slots(slots, out.shape[0])
+    _check_pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * head_dim, kv_page_stride, kscale_page_stride)
+    dev = _device_of((("out", out), ("slots", slots), ("kv_pages", kv_pages), ("kscale", kscale)))
+    return _launch("idx_load_slots_fp8", dev, stream, check, _addr(kv_pages), _addr(kscale), _addr(slots),
+                   out.shape[0], head_dim, num_pages, kv_page_stride, kscale_page_stride, _addr(out), _row_stride(out))
+
+
+def idx_load_slots_bf16(kv_pages, slots, out, *, num_pages, kv_page_stride=None, stream=None, check=True) -> int:
+    """bf16 counterpart of :func:`idx_load_slots_fp8`."""
+    _check_rows("out", out, 2)
+    head_dim = out.shape[1]
+    kv_page_stride = 2 * PAGE_POSITIONS * head_dim if kv_page_stride is None else kv_page_stride
+    _check_slots(slots, out.shape[0])
+    _check_pool(kv_pages, None, num_pages, 2 * PAGE_POSITIONS * head_dim, kv_page_stride, 0)
+    dev = _device_of((("out", out), ("slots", slots), ("kv_pages", kv_pages)))
+    return _launch("idx_load_slots_bf16", dev, stream, check, _addr(kv_pages), _addr(slots), out.shape[0], head_dim,
+                   num_pages, kv_page_stride, _addr(out), _row_stride(out))
+
+
 __all__ = [
     "idx_paged_mqa_logits_fp8", "idx_paged_mqa_logits_bf16", "idx_paged_mqa_logits_varlen_fp8",
     "idx_paged_mqa_logits_varlen_bf16", "idx_topk_logits",
     "idx_paged_mqa_topk_fp8", "idx_paged_mqa_topk_bf16", "idx_store_keys_fp8",
     "idx_store_keys_bf16", "idx_status_string",
-    "idx_abi_version", "IdxError", "LIB_PATH", "NUM_HEADS", "HEAD_DIM", "PAGE_POSITIONS",
+    "idx_norm_rope", "idx_norm_rope_store_fp8", "idx_norm_rope_store_bf16",
+    "idx_load_slots_fp8", "idx_load_slots_bf16",
+    "idx_abi_version", "IdxError", "LIB_PATH", "NUM_HEADS", "HEAD_DIM", "PAGE_POSITIONS", "LATENT_DIM",
 ]

@@ -1,0 +1,467 @@
+// norm_rope.hip -- norm, rotation, paged store and read back (gfx950 kernels
+// and C-ABI entry points declared in include/latent_cache.h).
+//
+// Every kernel gives a vector of D values to D/8 neighbouring lanes, 8 values
+// (16 bytes of bf16) each: sums and maxima over a vector are butterflies inside
+// its lanes, a wave covers 64*8/D vectors, and a vector is read once and
+// written once.  All of them move memory and compute next to nothing.
+#include "idx_device.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+struct Vectors {
+  const uint8_t* x;      // bf16
+  const float* weight;   // [D] or NULL
+  const int64_t* pos;    // [n]
+  const float* freq;     // [rope/2]
+  int64_t n;
+  int64_t x_stride;      // bytes
+  int32_t heads;
+  int32_t rope;          // rotated values
+  int32_t first;         // first rotated value
+  uint32_t flags;
+  float eps;
+};
+
+// cos and sin of position * frequency.  The product and its reduction to a
+// fraction of a turn are float64: at position 2^20 a float32 angle would
+// already be off by 0.03 rad.  The fraction, at most half a turn, is rounded to
+// float32 (2^-26 of a turn, 1e-7 rad).
+__device__ __forceinline__ f32x2 turn(int64_t position, float freq) {
+  const double turns = (double)position * (double)freq * 0.15915494309189533577;
+  const float f = (float)(turns - rint(turns));
+  float s, c;
+  sincospif(2.0f * f, &s, &c);
+  return (f32x2){c, s};
+}
+
+// cos/sin of all pairs of `tokens` tokens from t0 on, into LDS [tokens][rope/2].
+__device__ __forceinline__ void fill_turns(const Vectors& p, int64_t t0, int tokens, f32x2* table) {
+  const int pairs = p.rope >> 1;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int64_t t = t0 + i / pairs;
+    if (t < p.n) table[i] = turn(p.pos[t], p.freq[i % pairs]);
+  }
+}
+
+template <int LPV>
+__device__ __forceinline__ float vector_sum(float v) {
+#pragma unroll
+  for (int m = LPV / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+template <int LPV>
+__device__ __forceinline__ float vector_max(float v) {
+#pragma unroll
+  for (int m = LPV / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+
+// Norm and rotation of the lane's 8 values; `table` holds its token's turns,
+// `w` its 8 weights.  Called by whole waves.
+template <int LPV>
+__device__ __forceinline__ void norm_rotate(const Vectors& p, int sub, const float (&w)[8], const f32x2* table,
+                                            float (&v)[8]) {
+  if (!(p.flags & IDX_NORM_OFF)) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
+    s = vector_sum<LPV>(s);
+    const float r = 1.0f / sqrtf(s * (1.0f / (8 * LPV)) + p.eps);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = v[k] * r * w[k];
+  }
+  if (p.rope == 0) return;
+  const int at = 8 * sub - p.first;  // the lane's first value within the rotated part
+  const bool in = at >= 0 && at < p.rope;
+  if (p.flags & IDX_ROPE_HALVES) {
+    const int half = p.rope >> 1;
+    const bool low = at < half;
+    // the other value of each pair is half/8 lanes away
+    const int lane = threadIdx.x & 63, other = in ? (low ? lane + half / 8 : lane - half / 8) : lane;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float o = __shfl(v[k], other);
+      if (in) {
+        const f32x2 cs = table[(low ? at : at - half) + k];
+        v[k] = low ? v[k] * cs.x - o * cs.y : o * cs.y + v[k] * cs.x;
+      }
+    }
+  } else if (in) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x2 cs = table[(at >> 1) + k];
+      const float a = v[2 * k], b = v[2 * k + 1];
+      v[2 * k] = a * cs.x - b * cs.y;
+      v[2 * k + 1] = a * cs.y + b * cs.x;
+    }
+  }
+}
+
+template <int LPV>
+__device__ __forceinline__ void load_weight(const Vectors& p, int sub, float (&w)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) w[k] = p.weight ? p.weight[8 * sub + k] : 1.0f;
+}
+
+// Unit = one token x `STEPS` groups of kWaves * 64/LPV heads.
+template <int LPV, int STEPS>
+__global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t* out, int32_t groups) {
+  extern __shared__ f32x2 table[];
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV;
+  const int lane = threadIdx.x & 63, sub = lane % LPV;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float w[8];
+  load_weight<LPV>(p, sub, w);
+  for (int64_t unit = blockIdx.x; unit < p.n * groups; unit += gridDim.x) {
+    const int64_t t = unit / groups;
+    const int h0 = (int)(unit % groups) * (STEPS * kWaves * kVecs) + wave * kVecs + lane / LPV;
+    u32x4 raw[STEPS];
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int h = h0 + u * kWaves * kVecs;
+      raw[u] = (u32x4){0u, 0u, 0u, 0u};
+      if (h < p.heads) raw[u] = *reinterpret_cast<const u32x4*>(p.x + t * p.x_stride + ((int64_t)h * kDim + 8 * sub) * 2);
+    }
+    __syncthreads();  // the last unit's turns have been used
+    fill_turns(p, t, 1, table);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int h = h0 + u * kWaves * kVecs;
+      float v[8];
+      bf16x8_to_float(raw[u], v);
+      norm_rotate<LPV>(p, sub, w, table, v);
+      if (h < p.heads)
+        *reinterpret_cast<u32x4*>(out + ((t * p.heads + h) * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
+    }
+  }
+}
+
+// e4m3fn codes of v / scale, clamped to +-448: the quotients as the float32
+// division rounds them, from one reciprocal a vector.  q0 = v*y with y =
+// 1/scale correctly rounded, and the residual step q = q0 + (v - scale*q0)*y
+// gives the correctly rounded quotient away from underflow (Markstein's
+// correction); a scale outside [2^-60, 2^100] takes the division.  The sign
+// comes from v: a zero quotient may lose it.
+__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float scale) {
+  float q[8];
+  if (__ballot(!(scale >= 0x1p-60f && scale <= 0x1p100f)) == 0) {
+    const float y = 1.0f / scale;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float q0 = v[k] * y;
+      q[k] = fmaf(fmaf(-scale, q0, v[k]), y, q0);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] = v[k] / scale;
+  }
+  u32x2 codes;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+    uint32_t sign = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = fminf(fmaxf(q[4 * h + k], -448.0f), 448.0f);
+      sign |= (__float_as_uint(v[4 * h + k]) >> 31) << (8 * k + 7);
+    }
+    uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], (int)c, true);
+    codes[h] = (c & 0x7f7f7f7fu) | sign;
+  }
+  return codes;
+}
+
+struct Pool {
+  uint8_t* kv;
+  uint8_t* ks;
+  int64_t slots;  // 64 * pages
+  int64_t kv_stride, ks_stride;
+};
+
+// Unit = `STEPS` groups of kWaves * 64/LPV tokens.
+template <int KEY, int LPV, int STEPS>
+__global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
+  extern __shared__ f32x2 table[];
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kWaves * kVecs;
+  const int lane = threadIdx.x & 63, sub = lane % LPV;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float w[8];
+  load_weight<LPV>(p, sub, w);
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.n; t0 += (int64_t)gridDim.x * kTokens) {
+    u32x4 raw[STEPS];
+    int64_t slot[STEPS];
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int64_t t = t0 + (u * kWaves + wave) * kVecs + lane / LPV;
+      raw[u] = (u32x4){0u, 0u, 0u, 0u};
+      slot[u] = -1;
+      if (t < p.n) {
+        slot[u] = slots[t];
+        raw[u] = *reinterpret_cast<const u32x4*>(p.x + t * p.x_stride + 16 * sub);
+      }
+    }
+    __syncthreads();
+    fill_turns(p, t0, kTokens, table);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      float v[8];
+      bf16x8_to_float(raw[u], v);
+      norm_rotate<LPV>(p, sub, w, table + ((u * kWaves + wave) * kVecs + lane / LPV) * (p.rope >> 1), v);
+      const bool ok = slot[u] >= 0 && slot[u] < pool.slots;
+      const int64_t page = ok ? slot[u] / kPage : 0, i = ok ? slot[u] % kPage : 0;
+      if constexpr (KEY == kBf16) {
+        if (ok) *reinterpret_cast<u32x4*>(pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
+      } else {
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+        m = vector_max<LPV>(m);
+        const float scale = m > 0.0f ? m / 448.0f : 1.0f;
+        const u32x2 codes = quantise(v, scale);
+        if (ok) {
+          *reinterpret_cast<u32x2*>(pool.kv + page * pool.kv_stride + i * kDim + 8 * sub) = codes;
+          if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;
+        }
+      }
+    }
+  }
+}
+
+// Unit = `STEPS` groups of kWaves * 64/LPV slots.
+template <int KEY, int LPV, int STEPS>
+__global__ __launch_bounds__(kThreads) void load_slots_kernel(Pool pool, const int64_t* slots, int64_t n,
+                                                              uint8_t* out, int64_t out_stride) {
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kWaves * kVecs;
+  const int lane = threadIdx.x & 63, sub = lane % LPV, wave = threadIdx.x >> 6;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < n; t0 += (int64_t)gridDim.x * kTokens) {
+    int64_t slot[STEPS];
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      const int64_t t = t0 + (u * kWaves + wave) * kVecs + lane / LPV;
+      slot[u] = t < n ? slots[t] : -1;
+      if (slot[u] >= pool.slots) slot[u] = -1;
+    }
+    u32x4 raw[STEPS];
+    float scale[STEPS];
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      raw[u] = (u32x4){0u, 0u, 0u, 0u};
+      scale[u] = 0.0f;
+      if (slot[u] < 0) continue;
+      const int64_t page = slot[u] / kPage, i = slot[u] % kPage;
+      if constexpr (KEY == kBf16) {
+        raw[u] = *reinterpret_cast<const u32x4*>(pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2);
+      } else {
+        const u32x2 c = *reinterpret_cast<const u32x2*>(pool.kv + page * pool.kv_stride + i * kDim + 8 * sub);
+        raw[u].x = c.x;
+        raw[u].y = c.y;
+        scale[u] = *reinterpret_cast<const float*>(pool.ks + page * pool.ks_stride + 4 * i);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < STEPS; ++u) {
+      if (slot[u] < 0) continue;
+      const int64_t t = t0 + (u * kWaves + wave) * kVecs + lane / LPV;
+      u32x4 r = raw[u];
+      if constexpr (KEY == kFp8) {
+        float v[8];
+        bf16x8_to_float(__builtin_bit_cast(u32x4, fp8x8_to_bf16x8(raw[u].x, raw[u].y)), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= scale[u];
+        r = float_to_bf16x8(v);
+      }
+      *reinterpret_cast<u32x4*>(out + t * out_stride + 16 * sub) = r;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+constexpr int64_t kMaxGrid = (int64_t)1 << 20;  // larger problems loop (grid-stride)
+
+inline dim3 grid_of(int64_t units) { return dim3((uint32_t)(units < kMaxGrid ? units : kMaxGrid)); }
+
+// The checks that the norm and rotation's arguments share; `pointers`: there
+// is something to do, so the pointers are looked at.
+int validate_vectors(const void* x, const float* norm_weight, const int64_t* positions, const float* inv_freq,
+                     int64_t n, int32_t num_heads, int32_t head_dim, int32_t rope_dim, uint32_t flags, float eps,
+                     int64_t x_row_stride) {
+  if (rope_dim < 0 || rope_dim > head_dim || rope_dim % 16 != 0 ||
+      (flags & ~(IDX_NORM_OFF | IDX_ROPE_LEADING | IDX_ROPE_HALVES)) != 0)
+    return IDX_ERR_UNSUPPORTED;
+  if (n < 0 || num_heads < 0 || n > ((int64_t)1 << 40) || !(eps >= 0.0f) || !(eps < INFINITY) ||
+      x_row_stride < (int64_t)num_heads * head_dim || x_row_stride > ((int64_t)1 << 32))
+    return IDX_ERR_SHAPE;
+  if (n == 0 || num_heads == 0) return IDX_OK;
+  if (!x || (rope_dim > 0 && (!positions || !inv_freq)) || ((flags & IDX_NORM_OFF) && norm_weight)) return IDX_ERR_NULL;
+  if (!aligned(x, 16) || x_row_stride % 8 != 0 || !aligned(norm_weight, 16) || !aligned(positions, 8) ||
+      !aligned(inv_freq, 4))
+    return IDX_ERR_ALIGN;
+  return IDX_OK;
+}
+
+Vectors vectors_of(const void* x, const float* norm_weight, const int64_t* positions, const float* inv_freq,
+                   int64_t n, int32_t num_heads, int32_t head_dim, int32_t rope_dim, uint32_t flags, float eps,
+                   int64_t x_row_stride) {
+  Vectors p;
+  p.x = static_cast<const uint8_t*>(x);
+  p.weight = norm_weight;
+  p.pos = positions;
+  p.freq = inv_freq;
+  p.n = n;
+  p.x_stride = 2 * x_row_stride;
+  p.heads = num_heads;
+  p.rope = rope_dim;
+  p.first = (flags & IDX_ROPE_LEADING) ? 0 : head_dim - rope_dim;
+  p.flags = flags;
+  p.eps = eps;
+  return p;
+}
+
+template <int LPV>
+void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
+  constexpr int kOne = kWaves * (64 / LPV);  // heads of one step
+  const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2);
+  const int32_t groups = (p.heads + 4 * kOne - 1) / (4 * kOne);
+  if (p.n * groups >= 4 * device_cu_count()) {
+    norm_rope_kernel<LPV, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, static_cast<uint8_t*>(out), groups);
+  } else {
+    const int32_t single = (p.heads + kOne - 1) / kOne;
+    norm_rope_kernel<LPV, 1><<<grid_of(p.n * single), dim3(kThreads), lds, stream>>>(p, static_cast<uint8_t*>(out), single);
+  }
+}
+
+template <int KEY, int LPV>
+void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipStream_t stream) {
+  constexpr int kOne = kWaves * (64 / LPV);
+  const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kOne;
+  if (p.n >= (int64_t)4 * kOne * 2 * device_cu_count())
+    norm_rope_store_kernel<KEY, LPV, 4><<<grid_of((p.n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 4 * lds, stream>>>(
+        p, pool, slots);
+  else
+    norm_rope_store_kernel<KEY, LPV, 1><<<grid_of((p.n + kOne - 1) / kOne), dim3(kThreads), lds, stream>>>(p, pool, slots);
+}
+
+template <int KEY>
+int norm_rope_store(const void* x, const float* norm_weight, const int64_t* positions, const float* inv_freq,
+                    const int64_t* slots, int64_t n, int32_t head_dim, int32_t rope_dim, uint32_t flags, float eps,
+                    int64_t x_row_stride, void* kv_pages, float* kscale, int64_t num_pages, int64_t kv_page_stride,
+                    int64_t kscale_page_stride, hipStream_t stream) {
+  if (head_dim != IDX_HEAD_DIM && head_dim != kLatent) return IDX_ERR_UNSUPPORTED;
+  int st = validate_vectors(x, norm_weight, positions, inv_freq, n, 1, head_dim, rope_dim, flags, eps, x_row_stride);
+  if (st != IDX_OK) return st;
+  st = validate_pool(KEY, head_dim, num_pages, kv_page_stride, kscale_page_stride);
+  if (st != IDX_OK || n == 0) return st;
+  if (!slots) return IDX_ERR_NULL;
+  st = validate_pool_pointers(KEY, kv_pages, kscale, kv_page_stride, kscale_page_stride);
+  if (st != IDX_OK) return st;
+  if (!aligned(slots, 8)) return IDX_ERR_ALIGN;
+  const Vectors p = vectors_of(x, norm_weight, positions, inv_freq, n, 1, head_dim, rope_dim, flags, eps, x_row_stride);
+  const Pool pool = {static_cast<uint8_t*>(kv_pages), reinterpret_cast<uint8_t*>(kscale), num_pages * kPage,
+                     kv_page_stride, kscale_page_stride};
+  (void)hipGetLastError();  // start from a clean error state
+  if (head_dim == kLatent) launch_store<KEY, kLatent / 8>(p, pool, slots, stream);
+  else launch_store<KEY, IDX_HEAD_DIM / 8>(p, pool, slots, stream);
+  return launch_status();
+}
+
+template <int KEY, int LPV>
+void launch_load(const Pool& pool, const int64_t* slots, int64_t n, void* out, int64_t out_row_stride,
+                 hipStream_t stream) {
+  constexpr int kOne = kWaves * (64 / LPV);
+  uint8_t* o = static_cast<uint8_t*>(out);
+  if (n >= (int64_t)4 * kOne * 2 * device_cu_count())
+    load_slots_kernel<KEY, LPV, 4><<<grid_of((n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 0, stream>>>(
+        pool, slots, n, o, 2 * out_row_stride);
+  else
+    load_slots_kernel<KEY, LPV, 1><<<grid_of((n + kOne - 1) / kOne), dim3(kThreads), 0, stream>>>(pool, slots, n, o,
+                                                                                                 2 * out_row_stride);
+}
+
+template <int KEY>
+int load_slots(const void* kv_pages, const float* kscale, const int64_t* slots, int64_t n, int32_t head_dim,
+               int64_t num_pages, int64_t kv_page_stride, int64_t kscale_page_stride, void* out,
+               int64_t out_row_stride, hipStream_t stream) {
+  if (head_dim != IDX_HEAD_DIM && head_dim != kLatent) return IDX_ERR_UNSUPPORTED;
+  if (n < 0 || n > ((int64_t)1 << 40) || out_row_stride < head_dim || out_row_stride > ((int64_t)1 << 32))
+    return IDX_ERR_SHAPE;
+  int st = validate_pool(KEY, head_dim, num_pages, kv_page_stride, kscale_page_stride);
+  if (st != IDX_OK || n == 0) return st;
+  if (!slots || !out) return IDX_ERR_NULL;
+  st = validate_pool_pointers(KEY, kv_pages, kscale, kv_page_stride, kscale_page_stride);
+  if (st != IDX_OK) return st;
+  if (!aligned(slots, 8) || !aligned(out, 16) || out_row_stride % 8 != 0) return IDX_ERR_ALIGN;
+  const Pool pool = {static_cast<uint8_t*>(const_cast<void*>(kv_pages)),
+                     reinterpret_cast<uint8_t*>(const_cast<float*>(kscale)), num_pages * kPage, kv_page_stride,
+                     kscale_page_stride};
+  (void)hipGetLastError();
+  if (head_dim == kLatent) launch_load<KEY, kLatent / 8>(pool, slots, n, out, out_row_stride, stream);
+  else launch_load<KEY, IDX_HEAD_DIM / 8>(pool, slots, n, out, out_row_stride, stream);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int idx_norm_rope(const void* x, const float* norm_weight, const int64_t* positions, const float* inv_freq,
+                  void* out, int64_t n, int32_t num_heads, int32_t head_dim, int32_t rope_dim, uint32_t flags,
+                  float eps, int64_t x_row_stride, hipStream_t stream) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) return IDX_ERR_UNSUPPORTED;
+  const int st = validate_vectors(x, norm_weight, positions, inv_freq, n, num_heads, head_dim, rope_dim, flags, eps,
+                                  x_row_stride);
+  if (st != IDX_OK || n == 0 || num_heads == 0) return st;
+  if (!out) return IDX_ERR_NULL;
+  if (!aligned(out, 16)) return IDX_ERR_ALIGN;
+  const Vectors p = vectors_of(x, norm_weight, positions, inv_freq, n, num_heads, head_dim, rope_dim, flags, eps,
+                               x_row_stride);
+  (void)hipGetLastError();
+  switch (head_dim) {
+    case 64: launch_norm_rope<8>(p, out, stream); break;
+    case 128: launch_norm_rope<16>(p, out, stream); break;
+    case 256: launch_norm_rope<32>(p, out, stream); break;
+    default: launch_norm_rope<64>(p, out, stream); break;
+  }
+  return launch_status();
+}
+
+int idx_norm_rope_store_fp8(const void* x, const float* norm_weight, const int64_t* positions,
+                            const float* inv_freq, const int64_t* slots, int64_t n, int32_t head_dim,
+                            int32_t rope_dim, uint32_t flags, float eps, int64_t x_row_stride, void* kv_pages,
+                            float* kscale, int64_t num_pages, int64_t kv_page_stride, int64_t kscale_page_stride,
+                            hipStream_t stream) {
+  return norm_rope_store<kFp8>(x, norm_weight, positions, inv_freq, slots, n, head_dim, rope_dim, flags, eps,
+                               x_row_stride, kv_pages, kscale, num_pages, kv_page_stride, kscale_page_stride, stream);
+}
+
+int idx_norm_rope_store_bf16(const void* x, const float* norm_weight, const int64_t* positions,
+                             const float* inv_freq, const int64_t* slots, int64_t n, int32_t head_dim,
+                             int32_t rope_dim, uint32_t flags, float eps, int64_t x_row_stride, void* kv_pages,
+                             int64_t num_pages, int64_t kv_page_stride, hipStream_t stream) {
+  return norm_rope_store<kBf16>(x, norm_weight, positions, inv_freq, slots, n, head_dim, rope_dim, flags, eps,
+                                x_row_stride, kv_pages, nullptr, num_pages, kv_page_stride, 0, stream);
+}
+
+int idx_load_slots_fp8(const void* kv_pages, const float* kscale, const int64_t* slots, int64_t n, int32_t head_dim,
+                       int64_t num_pages, int64_t kv_page_stride, int64_t kscale_page_stride, void* out,
+                       int64_t out_row_stride, hipStream_t stream) {
+  return load_slots<kFp8>(kv_pages, kscale, slots, n, head_dim, num_pages, kv_page_stride, kscale_page_stride, out,
+                          out_row_stride, stream);
+}
+
+int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, int32_t head_dim, int64_t num_pages,
+                        int64_t kv_page_stride, void* out, int64_t out_row_stride, hipStream_t stream) {
+  return load_slots<kBf16>(kv_pages, nullptr, slots, n, head_dim, num_pages, kv_page_stride, 0, out, out_row_stride,
+                           stream);
+}
+
+}  // extern "C"

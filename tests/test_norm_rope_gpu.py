@@ -1,0 +1,274 @@
+"""Norm, rotation, paged store and read back on the GPU against float64."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from latent_reference import PAGE, assert_near_bf16, assert_near_fp8, e4m3_values, f64, inv_freq, norm_rope, vectors
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+@pytest.mark.parametrize("n,heads,dim,rope,opts", [
+    (1, 1, 128, 64, {}),
+    (1, 64, 128, 64, {"halves": True}),
+    (3, 5, 64, 64, {}),
+    (7, 13, 256, 32, {"leading": True}),
+    (5, 64, 512, 64, {}),
+    (33, 17, 512, 512, {"halves": True}),
+    (64, 64, 128, 96, {"halves": True, "leading": True}),
+    (130, 65, 128, 16, {"weight": False}),
+    (9, 3, 512, 0, {}),
+    (9, 130, 512, 48, {"norm": False, "halves": True}),
+    (700, 40, 512, 64, {}),
+    (2000, 70, 128, 128, {}),
+])
+@pytest.mark.parametrize("strided", [False, True])
+def test_norm_rope(lib, n, heads, dim, rope, opts, strided):
+    rng = np.random.default_rng(n * heads + dim)
+    opts = dict(opts)
+    weight = torch.from_numpy(1 + rng.standard_normal(dim).astype(np.float32) * 0.3)
+    if not opts.get("norm", True) or opts.pop("weight", None) is False:
+        weight = None
+    x = vectors(rng, (n, heads, dim))
+    freq = inv_freq(rope // 2) if rope else None
+    positions = torch.from_numpy(rng.integers(-5, 1 << 20, n)) if rope else None
+    if n > 4 and rope:
+        positions[1:4] = torch.tensor([0, 1, (1 << 31) + 12345])
+    y, size = norm_rope(x, positions, freq, weight, eps=1e-5, **opts)
+    xd = x.cuda()
+    if strided:
+        wide = torch.full((n, heads * dim + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+        wide[:, :heads * dim] = xd.reshape(n, -1)
+        xd = wide[:, :heads * dim].unflatten(1, (heads, dim))
+    out = torch.empty((n, heads, dim), dtype=torch.bfloat16, device="cuda")
+    lib.idx_norm_rope(xd, dev(positions), dev(freq), out, weight=dev(weight), eps=1e-5, **opts)
+    assert_near_bf16(out, y, size)
+    if not strided:  # in place
+        lib.idx_norm_rope(xd, dev(positions), dev(freq), xd, weight=dev(weight), eps=1e-5, **opts)
+        assert torch.equal(xd.view(torch.int16), out.view(torch.int16))
+
+
+def test_norm_rope_turns_back(lib):
+    """A rotation with negated frequencies undoes one: off by two roundings to
+    bf16 of the pair and both float32 parts."""
+    rng = np.random.default_rng(5)
+    x = vectors(rng, (50, 8, 128)).cuda()
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, 50)).cuda()
+    freq = inv_freq(32).cuda()
+    there, back = torch.empty_like(x), torch.empty_like(x)
+    lib.idx_norm_rope(x, positions, freq, there, norm=False)
+    lib.idx_norm_rope(there, positions, -freq, back, norm=False)
+    a = f64(x)
+    size = np.abs(a)
+    size[..., 64:] = np.repeat(np.abs(a[..., 64::2]) + np.abs(a[..., 65::2]), 2, -1)
+    # each of the pair's two values is within 2^-8 of itself after the first
+    # rounding; the turn back passes their sum on, and rounds again
+    assert (np.abs(f64(back) - a) <= size * (2 * 2.0 ** -8 + 2.0 ** -15) * 1.01 + 2.0 ** -130).all()
+
+
+def pool_of(rng, pages, dim, fp8, layout):
+    """(kv tensor, kscale or None, kv stride, kscale stride) of canary bytes."""
+    if not fp8:
+        stride = 2 * PAGE * dim + (32 if layout == "padded" else 0)
+        return torch.from_numpy(rng.integers(0, 256, pages * stride, dtype=np.uint8)), None, stride, 0
+    if layout == "fused":
+        stride = PAGE * (dim + 4)
+        return torch.from_numpy(rng.integers(0, 256, pages * stride, dtype=np.uint8)), None, stride, stride
+    stride, ks = PAGE * dim + (48 if layout == "padded" else 0), 256 + (12 if layout == "padded" else 0)
+    scales = torch.from_numpy(rng.random(pages * ks // 4 + 8).astype(np.float32))
+    return torch.from_numpy(rng.integers(0, 256, pages * stride, dtype=np.uint8)), scales, stride, ks
+
+
+def split_pool(kv, scales, pages, dim, fp8, stride, ks):
+    """Values and scales by slot, and a copy of all bytes with the slots cleared."""
+    kv = kv.cpu().numpy()
+    width = dim if fp8 else 2 * dim
+    rows = np.stack([kv[g * stride + i * width: g * stride + (i + 1) * width] for g in range(pages) for i in range(PAGE)])
+    if not fp8:
+        return rows.view(np.uint16), None
+    src = kv.view(np.uint8) if scales is None else scales.cpu().numpy().view(np.uint8)
+    at = PAGE * dim if scales is None else 0
+    s = np.concatenate([src[at + g * ks: at + g * ks + 256].view(np.float32) for g in range(pages)])
+    return rows, s
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("n,dim,rope,layout,opts", [
+    (1, 128, 64, "fused", {"halves": True}),
+    (1, 512, 64, "fused", {}),
+    (3, 512, 0, "split", {}),
+    (65, 128, 32, "padded", {"leading": True}),
+    (1000, 512, 64, "fused", {}),
+    (777, 512, 512, "padded", {"halves": True}),
+    (700, 128, 128, "split", {"norm": False}),
+    (9000, 512, 64, "fused", {}),
+    (33000, 128, 64, "split", {"halves": True}),
+])
+def test_norm_rope_store_and_load(lib, fp8, n, dim, rope, layout, opts):
+    """The stored slots hold the quantised vectors, every other byte of the pool
+    is left as it was, and the read back gives their values."""
+    rng = np.random.default_rng(n + dim)
+    pages = n // PAGE + 3
+    weight = None if not opts.get("norm", True) else torch.from_numpy(1 + rng.standard_normal(dim).astype(np.float32) * 0.3)
+    x = vectors(rng, (n, dim))
+    freq = inv_freq(rope // 2) if rope else None
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, n)) if rope else None
+    slots = rng.permutation(pages * PAGE)[:n].astype(np.int64)
+    if n > 10:
+        slots[rng.random(n) < 0.05] = -1
+        slots[rng.random(n) < 0.02] = pages * PAGE + rng.integers(0, 100)
+        slots[4], slots[5] = np.iinfo(np.int64).max, np.iinfo(np.int64).min
+    kept = (slots >= 0) & (slots < pages * PAGE)
+    kv, scales, stride, ks = pool_of(rng, pages, dim, fp8, layout)
+    kvd, sd, xd, slotd = kv.cuda(), dev(scales), x.cuda(), torch.from_numpy(slots).cuda()
+    kscale = sd if sd is not None else kvd.data_ptr() + PAGE * dim
+    common = dict(num_pages=pages, kv_page_stride=stride)
+    if fp8:
+        lib.idx_norm_rope_store_fp8(xd, dev(positions), dev(freq), slotd, kvd, kscale, weight=dev(weight),
+                                    kscale_page_stride=ks, **common, **opts)
+    else:
+        lib.idx_norm_rope_store_bf16(xd, dev(positions), dev(freq), slotd, kvd, weight=dev(weight), **common, **opts)
+    y, size = norm_rope(x, positions, freq, weight, **opts)
+    got, got_s = split_pool(kvd, sd, pages, dim, fp8, stride, ks)
+    if fp8:
+        assert_near_fp8(got[slots[kept]], got_s[slots[kept]], y[kept], size[kept])
+    else:
+        bits = torch.from_numpy(got[slots[kept]].view(np.int16)).view(torch.bfloat16)
+        assert_near_bf16(bits, y[kept], size[kept])
+    # put the old bytes back into the stored slots: nothing else has changed
+    back = kvd.cpu().numpy().copy()
+    width = dim if fp8 else 2 * dim
+    for s in slots[kept]:
+        g, i = divmod(int(s), PAGE)
+        a = g * stride + i * width
+        back[a: a + width] = kv.numpy()[a: a + width]
+        if fp8 and scales is None:
+            a = g * ks + PAGE * dim + 4 * i
+            back[a: a + 4] = kv.numpy()[a: a + 4]
+    assert np.array_equal(back, kv.numpy())
+    if scales is not None:
+        other = np.ones(len(scales), bool)
+        for s in slots[kept]:
+            other[int(s) // PAGE * ks // 4 + int(s) % PAGE] = False
+        assert np.array_equal(sd.cpu().numpy()[other], scales.numpy()[other])
+    # read back, in another order, a slot twice, rows of skipped slots left
+    take = np.concatenate([slots, slots[:3]])
+    take = take[rng.permutation(len(take))]
+    wide = torch.full((len(take), dim + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :dim]
+    if fp8:
+        lib.idx_load_slots_fp8(kvd, kscale, torch.from_numpy(take).cuda(), out, kscale_page_stride=ks, **common)
+    else:
+        lib.idx_load_slots_bf16(kvd, torch.from_numpy(take).cuda(), out, **common)
+    ok = (take >= 0) & (take < pages * PAGE)
+    w = wide.float().cpu().numpy()
+    assert (w[:, dim:] == 3.0).all() and (w[~ok] == 3.0).all()
+    if fp8:
+        want = e4m3_values()[got[take[ok]]] * got_s[take[ok], None].astype(np.float64)
+        # a float32 product, rounded to bf16
+        assert (np.abs(w[ok][:, :dim] - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -23) + 2.0 ** -134).all()
+    else:
+        assert np.array_equal(out.cpu().view(torch.int16).numpy()[ok].view(np.uint16), got[take[ok]])
+
+
+@pytest.mark.parametrize("n", [1, 1000, 5000])
+def test_plain_store_gives_the_key_stores_bytes(lib, n):
+    """Without norm and rotation the 128-value store writes what
+    idx_store_keys_fp8 and the oracle's quantiser write, over all magnitudes."""
+    rng = np.random.default_rng(n)
+    k = rng.standard_normal((n, 128)).astype(np.float32) * np.float32(10.0) ** rng.integers(-30, 30, (n, 1)).astype(np.float32)
+    k[rng.random(n) < 0.03] = 0.0
+    k[rng.random((n, 128)) < 0.01] = -0.0
+    x = torch.from_numpy(k).to(torch.bfloat16)
+    pages = n // PAGE + 1
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n]).cuda()
+    a = torch.zeros(pages * 8448, dtype=torch.uint8, device="cuda")
+    b = torch.zeros_like(a)
+    lib.idx_norm_rope_store_fp8(x.cuda(), None, None, slots, a, a.data_ptr() + 8192, norm=False, num_pages=pages)
+    lib.idx_store_keys_fp8(x.cuda(), slots, b, b.data_ptr() + 8192, num_pages=pages)
+    assert torch.equal(a, b)
+    codes, scales = oracle.quantize_keys_fp8(x.view(torch.int16).numpy().view(np.uint16))
+    got, got_s = split_pool(a, None, pages, 128, True, 8448, 8448)
+    assert np.array_equal(got[slots.cpu().numpy()], codes) and np.array_equal(got_s[slots.cpu().numpy()], scales)
+
+
+def test_plain_latent_store_is_the_float32_recipe(lib):
+    """512 values: codes and scales are those of the recipe in float32, bit for
+    bit (no norm, no rotation: no other rounding comes before)."""
+    rng = np.random.default_rng(8)
+    n, pages = 3000, 60
+    x = (torch.from_numpy(rng.standard_normal((n, 512)) * 10.0 ** rng.integers(-30, 30, (n, 1)))).to(torch.bfloat16)
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n])
+    kv = torch.zeros((pages, PAGE, 512), dtype=torch.uint8, device="cuda")
+    ks = torch.zeros((pages, PAGE), device="cuda")
+    lib.idx_norm_rope_store_fp8(x.cuda(), None, None, slots.cuda(), kv, ks, norm=False, num_pages=pages,
+                                kv_page_stride=PAGE * 512, kscale_page_stride=256)
+    scale = x.float().abs().amax(-1) / 448
+    codes = (x.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(ks.cpu().view(-1)[slots], scale)
+    assert torch.equal(kv.cpu().view(-1, 512)[slots], codes)
+
+
+def test_far_pages(lib):
+    """Slots whose bytes lie past 4 GiB of the pool."""
+    pages = 140000  # 4.6 GB
+    kv = torch.empty(pages * 33024, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(3)
+    x = vectors(rng, (40, 512))
+    slots = torch.from_numpy(pages * PAGE - 1 - rng.permutation(4000)[:40])
+    lib.idx_norm_rope_store_fp8(x.cuda(), None, None, slots.cuda(), kv, kv.data_ptr() + 32768, num_pages=pages)
+    out = torch.zeros((40, 512), dtype=torch.bfloat16, device="cuda")
+    lib.idx_load_slots_fp8(kv, kv.data_ptr() + 32768, slots.cuda(), out, num_pages=pages)
+    y, size = norm_rope(x, None, None)
+    scale = np.abs(y).max(-1, keepdims=True) / 448
+    # e4m3's half step, the bf16 rounding of the product, the float32 part
+    tol = np.maximum(np.abs(y) * 2.0 ** -4, scale * 2.0 ** -10) * 1.01 + np.abs(y) * 2.0 ** -7
+    assert (np.abs(f64(out) - y) <= tol).all()
+
+
+def test_other_stream_and_graph(lib):
+    """Calls follow the stream that they are given; a captured store and load
+    replay on what their buffers hold then."""
+    rng = np.random.default_rng(6)
+    n, pages = 300, 8
+    x = vectors(rng, (n, 512)).cuda()
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, n)).cuda()
+    freq = inv_freq(32).cuda()
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n]).cuda()
+    kv = torch.zeros(pages * 33024, dtype=torch.uint8, device="cuda")
+    out = torch.zeros((n, 512), dtype=torch.bfloat16, device="cuda")
+
+    def both(stream=None):
+        lib.idx_norm_rope_store_fp8(x, positions, freq, slots, kv, kv.data_ptr() + 32768, num_pages=pages, stream=stream)
+        lib.idx_load_slots_fp8(kv, kv.data_ptr() + 32768, slots, out, num_pages=pages, stream=stream)
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    both(side)
+    side.synchronize()
+    want = out.clone()
+    both()
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for k in range(3):
+        x.copy_(vectors(np.random.default_rng(70 + k), (n, 512)))
+        positions.add_(1000)
+        kv.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        kv.zero_()
+        out.zero_()
+        both()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
