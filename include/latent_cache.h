@@ -119,6 +119,77 @@ int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, i
                         int64_t num_pages, int64_t kv_page_stride, void* out, int64_t out_row_stride,
                         hipStream_t stream);
 
+/*
+ * Attention over the paged latents.  Row b is one query token of num_heads
+ * heads; S_b are the positions it attends to; position p = 64*j + i has the
+ * latent c_p (code * scale, or its bf16 values) of slot i of page
+ * page_table_b[j], key and value of every head:
+ *
+ *   L_b      = clamp(seqlens[b], 0, table_width * 64)
+ *   S_b      = the entries p, 0 <= p < L_b, among the first min(k, L_b) of
+ *              topk_idx[b] -- what idx_topk_logits leaves; other entries are
+ *              skipped, one that is there twice counts twice --
+ *              or every p < L_b if k is -1
+ *   x_hp     = scale * <q[b][h], c_p>
+ *   z_h      = sum_{p in S_b} exp(x_hp) (+ exp(sinks[h]))
+ *   out[b][h] = sum_{p in S_b} exp(x_hp) c_p / z_h          lse[b][h] = ln z_h
+ *
+ * A row with nothing in S_b and no sink gets out 0 and lse -inf.  Two results
+ * over disjoint sets of positions (a sink in one of them at most) join as
+ * (out1 e^lse1 + out2 e^lse2) / (e^lse1 + e^lse2).  Slots that no position of
+ * S_b names are not read, whatever they hold.  A position of S_b whose page id
+ * lies outside [0, num_pages), or whose row's table index lies outside
+ * [0, num_tables), is not read either: it makes its row's out and lse NaN.
+ * Scores, sums and outputs are float32 until the one rounding of out; the
+ * probability of a position is rounded to bf16 for its product with c_p.
+ *
+ *   q          bf16 [rows][num_heads][512], contiguous, 16-byte aligned.
+ *   kv_pages, kscale, num_pages, kv_page_stride, kscale_page_stride
+ *              the pool of 512-value pages: kv_page_stride >= 32768 bytes
+ *              (bf16: 65536), the rest as in idx_paged_mqa_logits_fp8.
+ *   page_table int32, 4-byte aligned: row b's table (table_width entries) at
+ *              page_table + t*page_table_row_stride with t = b, or
+ *              t = row_table[b] where row_table is not NULL.  A stride of 0
+ *              gives every row one table.
+ *   row_table  int32 [rows] or NULL, 4-byte aligned; num_tables >= 0 is read
+ *              with it only.
+ *   topk_idx   int32 [rows][k], 4-byte aligned; NULL if k is -1 (it may be if k
+ *              is 0).
+ *   seqlens    int32 [rows], 4-byte aligned.
+ *   sinks      fp32 [num_heads], 4-byte aligned, or NULL.
+ *   out        bf16 [rows][num_heads][512], 16-byte aligned.
+ *   lse        fp32 [rows][num_heads], 4-byte aligned, or NULL.
+ *   rows, num_heads   >= 0; 0 returns IDX_OK with no launch.
+ *   num_heads  at most 128.    head_dim must be 512.
+ *   table_width >= 0, at most 16,777,216 (page_table may be NULL if it is 0).
+ *   k >= -1.   scale finite.
+ *   workspace  idx_latent_attention_workspace(rows, num_heads, table_width, k)
+ *              bytes on the call's device, 16-byte aligned; NULL where that is 0.  It holds nothing between calls,
+ *              but calls that may run at the same time (captured ones
+ *              included) need one each.
+ */
+int idx_latent_attention_fp8(const void* q, const void* kv_pages, const float* kscale,
+                             const int32_t* page_table, const int32_t* row_table, int32_t num_tables,
+                             const int32_t* topk_idx, const int32_t* seqlens, const float* sinks,
+                             void* out, float* lse, int32_t rows, int32_t num_heads, int32_t head_dim,
+                             int32_t table_width, int64_t num_pages, int64_t kv_page_stride,
+                             int64_t kscale_page_stride, int64_t page_table_row_stride, int32_t k,
+                             float scale, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream);
+
+/* bf16 counterpart (no scales). */
+int idx_latent_attention_bf16(const void* q, const void* kv_pages, const int32_t* page_table,
+                              const int32_t* row_table, int32_t num_tables, const int32_t* topk_idx,
+                              const int32_t* seqlens, const float* sinks, void* out, float* lse,
+                              int32_t rows, int32_t num_heads, int32_t head_dim, int32_t table_width,
+                              int64_t num_pages, int64_t kv_page_stride,
+                              int64_t page_table_row_stride, int32_t k, float scale, void* workspace,
+                              int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that a call of these sizes needs on the current device (0:
+ * none; -1: sizes out of range). */
+int64_t idx_latent_attention_workspace(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k);
+
 #ifdef __cplusplus
 }
 #endif

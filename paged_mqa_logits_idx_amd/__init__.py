@@ -53,6 +53,9 @@ _SYMBOLS = (
     "idx_norm_rope_store_bf16",
     "idx_load_slots_fp8",
     "idx_load_slots_bf16",
+    "idx_latent_attention_fp8",
+    "idx_latent_attention_bf16",
+    "idx_latent_attention_workspace",
     "idx_status_string",
     "idx_abi_version",
 )
@@ -109,10 +112,16 @@ def _load() -> ctypes.CDLL:
             ("idx_norm_rope_store_fp8", [ptr] * 5 + [i64] + rotation + [ptr, ptr, i64, i64, i64, ptr]),
             ("idx_norm_rope_store_bf16", [ptr] * 5 + [i64] + rotation + [ptr, i64, i64, ptr]),
             ("idx_load_slots_fp8", [ptr] * 3 + [i64, i32, i64, i64, i64, ptr, i64, ptr]),
-            ("idx_load_slots_bf16", [ptr] * 2 + [i64, i32, i64, i64, ptr, i64, ptr])):
+            ("idx_load_slots_bf16", [ptr] * 2 + [i64, i32, i64, i64, ptr, i64, ptr]),
+            ("idx_latent_attention_fp8", [ptr] * 5 + [i32] + [ptr] * 5 + [i32] * 4 + [i64] * 4
+             + [i32, ctypes.c_float, ptr, i64, ptr]),
+            ("idx_latent_attention_bf16", [ptr] * 4 + [i32] + [ptr] * 5 + [i32] * 4 + [i64] * 3
+             + [i32, ctypes.c_float, ptr, i64, ptr])):
         fn = getattr(lib, name)
         fn.argtypes = types
         fn.restype = ctypes.c_int
+    lib.idx_latent_attention_workspace.argtypes = [i32] * 4
+    lib.idx_latent_attention_workspace.restype = i64
     lib.idx_status_string.argtypes = [ctypes.c_int]
     lib.idx_status_string.restype = ctypes.c_char_p
     lib.idx_abi_version.argtypes = []
@@ -594,6 +603,103 @@ def idx_load_slots_bf16(kv_pages, slots, out, *, num_pages, kv_page_stride=None,
                    num_pages, kv_page_stride, _addr(out), _row_stride(out))
 
 
+def idx_latent_attention_workspace(rows, num_heads, table_width, k=None) -> int:
+    """Bytes of workspace that a latent attention call of these sizes needs on
+    the current device (``k`` None: no selection)."""
+    return int(_lib.idx_latent_attention_workspace(rows, num_heads, table_width, -1 if k is None else k))
+
+
+def _latent_workspace(rows, heads, width, k, dev, stream) -> torch.Tensor | None:
+    """A workspace from torch's allocator, on the call's device and stream."""
+    if dev is None:
+        return None
+    with torch.cuda.device(dev):
+        need = idx_latent_attention_workspace(rows, heads, width, k)
+        if need <= 0:
+            return None
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+        if not isinstance(stream, torch.cuda.Stream):
+            raise ValueError("a call on a raw stream handle needs its own workspace")
+        with torch.cuda.stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
+def _latent_attention(name, q, kv_pages, kscale, page_table, topk_idx, seqlens, out, lse, scale, num_pages, sinks,
+                      row_table, workspace, strides, page_table_row_stride, stream, check):
+    """``kscale`` and ``strides`` are tuples: those of the pool's key type."""
+    _check("q", q, torch.bfloat16)
+    _check("out", out, torch.bfloat16)
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError(f"q and out must be [rows, heads, {LATENT_DIM}], got {list(q.shape)} and {list(out.shape)}")
+    rows, heads, head_dim = q.shape
+    _check("page_table", page_table, torch.int32, dense_rows=True)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have two dims")
+    tables, width = page_table.shape
+    for what, x, dtype, shape in (("seqlens", seqlens, torch.int32, (rows,)), ("sinks", sinks, torch.float32, (heads,)),
+                                  ("lse", lse, torch.float32, (rows, heads)), ("row_table", row_table, torch.int32, (rows,))):
+        if x is not None:
+            _check(what, x, dtype)
+            if x.shape != shape:
+                raise ValueError(f"{what} must be {list(shape)}, got {list(x.shape)}")
+    k = None
+    if topk_idx is not None:
+        _check("topk_idx", topk_idx, torch.int32)
+        if topk_idx.dim() != 2 or topk_idx.shape[0] != rows:
+            raise ValueError(f"topk_idx must be [{rows}, k], got {list(topk_idx.shape)}")
+        k = topk_idx.shape[1]
+    if page_table_row_stride is None:
+        shared = tables == 1 and row_table is None
+        page_table_row_stride = 0 if shared else page_table.stride(0)
+        if not shared and row_table is None and tables < rows:
+            raise ValueError(f"page_table holds {tables} tables for {rows} rows")
+    _check_pool(kv_pages, kscale[0] if kscale else None, num_pages,
+                PAGE_POSITIONS * LATENT_DIM * (1 if kscale else 2), strides[0], strides[-1])
+    dev = _device_of((("q", q), ("kv_pages", kv_pages), ("kscale", kscale[0] if kscale else None),
+                      ("page_table", page_table), ("topk_idx", topk_idx), ("seqlens", seqlens), ("out", out),
+                      ("lse", lse), ("sinks", sinks), ("row_table", row_table), ("workspace", workspace)))
+    if workspace is None:
+        workspace = _latent_workspace(rows, heads, width, k, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _launch(name, dev, stream, check, _addr(q), _addr(kv_pages), *[_addr(x) for x in kscale], _addr(page_table),
+                   _addr(row_table), 0 if row_table is None else tables, _addr(topk_idx), _addr(seqlens), _addr(sinks),
+                   _addr(out), _addr(lse), rows, heads, head_dim, width, num_pages, *strides, page_table_row_stride,
+                   -1 if k is None else k, scale, _addr(workspace), nbytes)
+
+
+def idx_latent_attention_fp8(q, kv_pages, kscale, page_table, topk_idx, seqlens, out, lse=None, *, scale, num_pages,
+                             sinks=None, row_table=None, workspace=None,
+                             kv_page_stride=PAGE_POSITIONS * (LATENT_DIM + 4),
+                             kscale_page_stride=PAGE_POSITIONS * (LATENT_DIM + 4), page_table_row_stride=None,
+                             stream=None, check=True) -> int:
+    """Attention of bf16 ``q`` [rows, heads, 512] to the fp8 latents of the positions
+    in ``topk_idx`` (int32 [rows, k], as the top-k leaves it; None: every position
+    below ``seqlens``), which are key and value of all heads; into ``out`` (as
+    ``q``) and, if given, ``lse`` fp32 [rows, heads].
+
+    ``page_table`` int32 [tables, width]: one for all rows, one per row, or row b's
+    at ``row_table[b]``.  ``sinks`` fp32 [heads] join the softmax's denominator.
+    ``workspace``: a tensor of :func:`idx_latent_attention_workspace` bytes, of this
+    call's own while it runs; None takes one from torch's allocator.
+    """
+    return _latent_attention("idx_latent_attention_fp8", q, kv_pages, (kscale,), page_table, topk_idx, seqlens, out,
+                             lse, scale, num_pages, sinks, row_table, workspace, (kv_page_stride, kscale_page_stride),
+                             page_table_row_stride, stream, check)
+
+
+def idx_latent_attention_bf16(q, kv_pages, page_table, topk_idx, seqlens, out, lse=None, *, scale, num_pages,
+                              sinks=None, row_table=None, workspace=None,
+                              kv_page_stride=2 * PAGE_POSITIONS * LATENT_DIM, page_table_row_stride=None, stream=None,
+                              check=True) -> int:
+    """bf16 counterpart of :func:`idx_latent_attention_fp8`."""
+    return _latent_attention("idx_latent_attention_bf16", q, kv_pages, (), page_table, topk_idx, seqlens, out, lse,
+                             scale, num_pages, sinks, row_table, workspace, (kv_page_stride,), page_table_row_stride,
+                             stream, check)
+
+
 __all__ = [
     "idx_paged_mqa_logits_fp8", "idx_paged_mqa_logits_bf16", "idx_paged_mqa_logits_varlen_fp8",
     "idx_paged_mqa_logits_varlen_bf16", "idx_topk_logits",
@@ -601,5 +707,6 @@ __all__ = [
     "idx_store_keys_bf16", "idx_status_string",
     "idx_norm_rope", "idx_norm_rope_store_fp8", "idx_norm_rope_store_bf16",
     "idx_load_slots_fp8", "idx_load_slots_bf16",
+    "idx_latent_attention_fp8", "idx_latent_attention_bf16", "idx_latent_attention_workspace",
     "idx_abi_version", "IdxError", "LIB_PATH", "NUM_HEADS", "HEAD_DIM", "PAGE_POSITIONS", "LATENT_DIM",
 ]

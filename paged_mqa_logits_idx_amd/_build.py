@@ -10,7 +10,7 @@ from pathlib import Path
 
 PKG_DIR = Path(__file__).resolve().parent
 REPO_DIR = PKG_DIR.parent
-SOURCES = [PKG_DIR / "csrc" / name for name in ("paged_mqa_logits.hip", "norm_rope.hip")]
+SOURCES = [PKG_DIR / "csrc" / name for name in ("paged_mqa_logits.hip", "norm_rope.hip", "latent_attention.hip")]
 LIB_PATH = PKG_DIR / "libidx_paged_mqa.so"
 STREAM_SOURCES = [PKG_DIR / "csrc" / "read_stream.hip"]
 STREAM_LIB_PATH = PKG_DIR / "libidx_read_stream.so"

@@ -91,3 +91,86 @@ def vectors(rng: np.random.Generator, shape, spread: float = 1.0) -> torch.Tenso
     if len(x) > 2:
         x[2] = 0.0
     return torch.from_numpy(x).to(torch.bfloat16)
+
+
+def latent_values(kv: torch.Tensor, scales, fp8: bool) -> np.ndarray:
+    """The latents [pages, 64, 512] that a pool (uint8 codes and float32 scales,
+    or bf16) stands for."""
+    if not fp8:
+        return f64(kv).reshape(-1, PAGE, LATENT)
+    return e4m3_values()[kv.cpu().numpy().reshape(-1, PAGE, LATENT)] * f64(scales).reshape(-1, PAGE, 1)
+
+
+def attention(q, latents, tables, lengths, scale, selected=None, sinks=None):
+    """(out, lse, tolerances): row b of q [rows, heads, 512] over the positions
+    selected[b] (None: all) below lengths[b], whose pages tables[b] (None: the
+    row has no valid table) names.
+
+    The tolerances follow the library's roundings.  Scores: products of bf16
+    values summed in float32, 512 of them and the scales: |error| <= 516 2^-24
+    sum_d |q_d c_d| scale = E.  Probabilities: exp passes E on, and is itself,
+    with its argument's rounding, within 2^-20; rounded to bf16 (2^-8 of the
+    value at most) for the products, which are summed in float32 over n
+    positions.  With A = sum_p p |c_p| / z
+      |out error| <= A (2^-8 + 2 E + 2^-19 + n 2^-24) + 2^-8 |out|
+      |lse error| <= E + 2^-20 + n 2^-24 + |lse| 2^-22
+    The probabilities' roundings are independent from position to position, so
+    the error's norm over the 512 values is also far below that sum: at most
+    2^-8 sqrt(sum_p p^2 |c_p|^2) / z were all of them at their largest and
+    orthogonal; twice that (and the rest as above, over the norms) is `norm`.
+    """
+    q = f64(q)
+    rows, heads, _ = q.shape
+    out, lse = np.zeros((rows, heads, LATENT)), np.full((rows, heads), -np.inf)
+    tol, tol_lse, norm = np.zeros_like(out), np.zeros_like(lse), np.zeros_like(lse)
+    pages = latents.shape[0]
+    for b in range(rows):
+        L = int(lengths[b])
+        at = np.arange(L) if selected is None else np.asarray(selected[b][: min(len(selected[b]), max(L, 0))], dtype=np.int64)
+        at = at[(at >= 0) & (at < L)]
+        page = np.full(len(at), -1) if tables[b] is None else np.asarray(tables[b])[at // PAGE]
+        if ((page < 0) | (page >= pages)).any():
+            out[b], lse[b] = np.nan, np.nan
+            continue
+        c = latents[page, at % PAGE]
+        x = scale * (q[b] @ c.T)
+        E = 516 * 2.0 ** -24 * abs(scale) * (np.abs(q[b]) @ np.abs(c).T).max(-1, initial=0.0)
+        s = x if sinks is None else np.concatenate([x, f64(sinks)[:, None]], 1)
+        if s.shape[1] == 0:
+            continue
+        top = s.max(-1, keepdims=True)
+        top = np.where(np.isneginf(top), 0.0, top)
+        e = np.exp(s - top)
+        z = e.sum(-1, keepdims=True)
+        p = np.divide(e, z, where=z > 0, out=np.zeros_like(e))[:, : len(at)]
+        with np.errstate(divide="ignore"):
+            lse[b] = (top + np.log(z))[:, 0]
+        out[b] = p @ c
+        n, A = len(at), p @ np.abs(c)
+        other = (2 * E + 2.0 ** -19 + n * 2.0 ** -24)[:, None]
+        tol[b] = A * (2.0 ** -8 + other) + 2.0 ** -8 * np.abs(out[b]) + 2.0 ** -126
+        tol_lse[b] = E + 2.0 ** -20 + n * 2.0 ** -24 + np.where(np.isinf(lse[b]), 0, np.abs(lse[b])) * 2.0 ** -22
+        spread = np.sqrt((p * p) @ (c * c).sum(-1))
+        norm[b] = (2 * 2.0 ** -8 * spread + other[:, 0] * np.linalg.norm(A, axis=-1)
+                   + 2.0 ** -8 * np.linalg.norm(out[b], axis=-1) + 2.0 ** -120)
+    return out, lse, (tol, tol_lse, norm)
+
+
+def assert_attention(got, got_lse, want) -> None:
+    out, lse, (tol, tol_lse, norm) = want
+    got = f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(out)), "NaN rows differ"
+    live = ~np.isnan(out)
+    d = np.abs(got - out)
+    bad = live & (d > tol)
+    assert not bad.any(), f"{bad.sum()} values off, worst {d[bad].max():.3e} at {np.argwhere(bad)[:3].tolist()}"
+    rows = live[..., 0]
+    far = np.linalg.norm(np.where(live, got - out, 0.0), axis=-1)
+    assert (far <= norm)[rows].all(), f"norm of the error {far[rows].max():.3e}, ratio {(far / norm)[rows].max():.2f}"
+    if got_lse is None:
+        return
+    got_lse = f64(got_lse)
+    assert np.array_equal(np.isnan(got_lse), np.isnan(lse)) and np.array_equal(np.isneginf(got_lse), np.isneginf(lse))
+    fin = np.isfinite(lse)
+    d = np.abs(np.where(fin, got_lse, 0) - np.where(fin, lse, 0))
+    assert (d <= tol_lse).all(), f"lse off by {d.max():.3e}"

@@ -155,3 +155,72 @@ def test_binding_refuses():
         b.idx_load_slots_fp8(kv, 4, slots, x, num_pages=1)
     with pytest.raises(ValueError, match="kv_pages must be contiguous"):
         b.idx_load_slots_bf16(kv[::2], slots, v, num_pages=0)
+
+
+ATT8_ORDER = "q kv ks pt rt nt idx sl sinks out lse rows heads dim width pages kvs kss pts k scale ws wb stream"
+ATT16_ORDER = "q kv pt rt nt idx sl sinks out lse rows heads dim width pages kvs pts k scale ws wb stream"
+ATT = dict(q=16, kv=16, ks=4, pt=4, rt=None, nt=0, idx=4, sl=4, sinks=None, out=16, lse=4, rows=1, heads=64, dim=512, width=1,
+           pages=1, kvs=65536, kss=33024, pts=1, k=8, scale=0.5, ws=None, wb=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dim=576), UNSUPPORTED), (dict(heads=129), UNSUPPORTED),
+    (dict(rows=-1), SHAPE), (dict(heads=-1), SHAPE), (dict(width=-1), SHAPE), (dict(width=(1 << 24) + 1), SHAPE), (dict(k=-2), SHAPE),
+    (dict(pages=-1), SHAPE), (dict(kvs=32000), SHAPE), (dict(pts=-1), SHAPE), (dict(nt=-1), SHAPE),
+    (dict(scale=float("nan")), SHAPE), (dict(scale=float("-inf")), SHAPE), (dict(wb=-1), SHAPE),
+    (dict(rows=0, q=None, out=None), OK), (dict(heads=0, q=None, out=None), OK),
+    (dict(q=None), NULL), (dict(kv=None), NULL), (dict(pt=None), NULL), (dict(sl=None), NULL), (dict(out=None), NULL),
+    (dict(idx=None), NULL), (dict(k=-1), NULL),           # a list without its length, a length without its list
+    (dict(q=8), ALIGN), (dict(kv=8), ALIGN), (dict(pt=2), ALIGN), (dict(rt=2), ALIGN), (dict(idx=2), ALIGN), (dict(sl=2), ALIGN),
+    (dict(sinks=2), ALIGN), (dict(out=8), ALIGN), (dict(lse=2), ALIGN), (dict(ws=8), ALIGN), (dict(kvs=65544), ALIGN),
+    (dict(k=4096, width=64), NULL),                       # splits its rows: a workspace is needed
+    (dict(k=4096, width=64, ws=16, wb=1000), SHAPE),      # too small a one
+    (dict(idx=None, k=-1, width=4097), NULL),
+])
+def test_attention_validation(raw, kw, status):
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, **kw) == status
+    assert call(raw, "idx_latent_attention_bf16", ATT16_ORDER, ATT, **kw) == status
+
+
+def test_attention_fp8_scales(raw):
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, ks=None) == NULL
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, kss=252) == SHAPE
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, ks=6) == ALIGN
+
+
+def test_attention_workspace_sizes():
+    import paged_mqa_logits_idx_amd as b
+
+    assert b.idx_latent_attention_workspace(0, 64, 32, 2048) == 0
+    assert b.idx_latent_attention_workspace(4096, 64, 88, 2048) == 0       # rows enough to fill the device
+    assert b.idx_latent_attention_workspace(1, 64, 512, 2048) > 0
+    assert b.idx_latent_attention_workspace(1, 64, 512) >= b.idx_latent_attention_workspace(1, 64, 512, 2048)
+    assert b.idx_latent_attention_workspace(1, 64, 512, 16) == 0           # one tile
+    for bad in [(-1, 64, 32, 1), (1, 129, 32, 1), (1, 64, -1, 1), (1, 64, (1 << 24) + 1, 1)]:
+        assert b.idx_latent_attention_workspace(*bad) == -1
+
+
+def test_attention_binding_refuses():
+    import paged_mqa_logits_idx_amd as b
+
+    q = torch.zeros(3, 8, 512, dtype=torch.bfloat16)
+    kv = torch.zeros((2, 33024), dtype=torch.uint8)
+    table, sl = torch.zeros((3, 2), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    idx = torch.zeros((3, 4), dtype=torch.int32)
+    for match, args, kw in [
+        ("q must be torch.bfloat16", (q.float(), kv, 4, table, idx, sl, q), {}),
+        ("q and out must be", (q, kv, 4, table, idx, sl, q[:2]), {}),
+        ("page_table must be torch.int32", (q, kv, 4, table.long(), idx, sl, q), {}),
+        ("page_table must have two dims", (q, kv, 4, table[0], idx, sl, q), {}),
+        ("holds 2 tables for 3 rows", (q, kv, 4, table[:2], idx, sl, q), {}),
+        ("topk_idx must be", (q, kv, 4, table, idx[:2], sl, q), {}),
+        ("topk_idx must be contiguous", (q, kv, 4, table, idx.t().contiguous().t(), sl, q), {}),
+        ("seqlens must be", (q, kv, 4, table, idx, sl[:2], q), {}),
+        ("lse must be", (q, kv, 4, table, idx, sl, q, torch.zeros(3, 9)), {}),
+        ("sinks must be", (q, kv, 4, table, idx, sl, q), dict(sinks=torch.zeros(9))),
+        ("row_table must be", (q, kv, 4, table, idx, sl, q), dict(row_table=sl[:1])),
+        ("kv_pages is shorter", (q, kv, 4, table, idx, sl, q), dict(num_pages=3)),
+        ("must be device tensors", (q, kv, 4, table, idx, sl, q), {}),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            b.idx_latent_attention_fp8(*args, scale=1.0, **{"num_pages": 2, **kw})
