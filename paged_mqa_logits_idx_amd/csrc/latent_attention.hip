@@ -91,11 +91,6 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float max_over_g(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
-}
-
 // Where chunk c (16 bytes) of position r stands within the position's LDS row:
 // rows of a multiple of 256 bytes would put one chunk of all positions into
 // the same banks.  16 positions spread over 16 chunks, 8 consecutive ones over
@@ -119,25 +114,25 @@ __device__ __forceinline__ Closing close_sum(float m, float z, float sink) {
   return c;
 }
 
-// Tile shapes: 32 KiB of latents either way, and as many waves as it takes for
-// each to hold its part of the queries and of the outputs in registers.
+// A unit's tile: 64 positions x 64 heads, four 32 x 32 blocks of scores.  Eight
+// waves, two on each SIMD: the two waves of a block take 256 of the 512 values
+// each and add their halves up through LDS (so a wave keeps 64 registers of
+// queries and 64 of outputs, and has as many again to read LDS ahead of the
+// matrix units).
 template <int KEY>
 struct Shape {
-  static constexpr int kTile = KEY == kFp8 ? 64 : 32;                     // positions of a tile
-  static constexpr int kRowBytes = KEY == kFp8 ? kLatent : 2 * kLatent;   // of a position
-  static constexpr int kWaves = 8, HT = 64;
+  static constexpr int kTile = 64, HT = 64;
+  static constexpr int kWaves = 8, kThreads = 64 * kWaves;
+  static constexpr int kRowBytes = KEY == kFp8 ? kLatent : 2 * kLatent;  // of a position
   static constexpr int kChunks = kRowBytes / 16;    // of a position
-  static constexpr int NB = HT / 16;                // head blocks
-  static constexpr int PB = kTile / 16;             // position blocks
-  static constexpr int HG = kWaves / PB;            // head groups: a wave scores one position block x one group
-  static constexpr int NQ = NB / HG;                // head blocks of a group
+  static constexpr int kBuffers = KEY == kFp8 ? 4 : 2;
   static constexpr int kDims = kLatent / kWaves;    // values of a wave's outputs
-  static constexpr int MB = kDims / 16;
+  static constexpr int MB = kDims / 32, NB = HT / 32;
   static constexpr int kGather = kTile / kWaves;    // positions that a wave gathers
   static constexpr int kPerDma = 64 / kChunks;      // positions of one DMA
-  static constexpr int kDmaOps = kGather / kPerDma + (KEY == kFp8 ? 1 : 0);  // of a wave and tile, scales included
-  static constexpr int kBuffers = 4;
-  static constexpr int kRing = 2048 / kTile;        // tiles whose positions are resolved ahead
+  static constexpr int kDmas = kGather / kPerDma;
+  static constexpr int kDmaOps = kDmas + (KEY == kFp8 ? 1 : 0);  // of a wave and tile, scales included
+  static constexpr int kRing = 16;                  // tiles whose positions are resolved ahead
 };
 
 template <int KEY>
@@ -146,9 +141,13 @@ struct AttendShared {
   uint8_t tile[S::kBuffers][S::kTile * S::kRowBytes];
   float scale[S::kBuffers][S::kTile];   // e4m3 scales of the tiles' positions
   uint32_t ref[S::kRing][S::kTile];     // slots of the positions (64 * page + i), or kMasked, kBad
-  __bf16 p[2][S::HT * S::kTile];        // [head][position], 16-byte chunks swizzled by head
-  float mx[S::HT][S::PB];               // maxima of the tile's position blocks
-  float sum[S::PB][S::HT];
+  bf16x8 p[4][S::HT][2];                // probabilities, by 16 positions and head, in operand order
+  f32x4 part[4][2][2][64];              // halves of scores on their way: by block, wave and lane
+  uint32_t special[S::kRing];           // whether a tile has a position that is masked or bad
+  uint32_t over[4];                     // whether a tile's scores exceed the references, by tile % 4
+  float mx[S::HT][4];                   // maxima of the tile's blocks of 16 positions
+  float by[S::HT];                      // factors of a moved reference; at the end the references
+  float sum[4][S::HT];
 };
 
 constexpr uint32_t kMasked = 0xffffffffu;  // no position
@@ -156,14 +155,15 @@ constexpr uint32_t kBad = 0xfffffffeu;     // its page id lies outside the pool
 constexpr int64_t kMaxPages = (int64_t)1 << 25;  // 64 * page + i stays below kBad (and 2^25 pages are a TiB)
 
 template <int KEY>
-__global__ __launch_bounds__(512, 2) void latent_attention_kernel(Attend a) {
+__global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kernel(Attend a) {
   using S = Shape<KEY>;
-  constexpr int kTile = S::kTile, kRowBytes = S::kRowBytes, NB = S::NB, NQ = S::NQ, MB = S::MB, PB = S::PB;
+  constexpr int kTile = S::kTile, kRowBytes = S::kRowBytes, NB = S::NB, MB = S::MB;
   __shared__ __attribute__((aligned(16))) AttendShared<KEY> sh;
 
-  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int pb = wave % PB, hg = wave / PB;
+  const int pb = wave & 1, hg = wave >> 1 & 1;  // the wave's block of scores: positions 32*pb, heads 32*hg
+  const int kh = wave >> 2;                     // and its half of the values, 256*kh
 
   // Units of one row and split (its head blocks read the same latents) follow
   // each other on one XCD; the last rows, the longest of a causal batch, start
@@ -184,30 +184,28 @@ __global__ __launch_bounds__(512, 2) void latent_attention_kernel(Attend a) {
   const int32_t* tab = a.pt + (int64_t)(a.rt ? (table_ok ? table : 0) : b) * a.pt_stride;
   const int32_t* idx = a.k >= 0 ? a.idx + (int64_t)b * a.k : nullptr;
 
-  f32x4 acc[MB][NB];
+  f32x16 acc[MB][NB];  // values kDims*wave + 32*mb + 8*(i/4) + 4*half + i%4 of heads 32*nb + n
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  float m[NB], sum[NQ];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) m[nb] = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < NQ; ++u) sum[u] = 0.0f;
+    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = (f32x16)(0.0f);
+  // Of head 32*hg + n: reference (0 before the first), what a logit may exceed
+  // it by (anything does before the first), sum of probabilities.
+  float m = 0.0f, most = -INFINITY, sum = 0.0f;
 
   if (mine > 0) {
-    // Slots of the positions of the unit's tiles [j0, j0 + n), `many` a thread
-    // at once.
-    auto resolve = [&](int32_t j0, int32_t n, auto many) {
+    // Slots of the positions of the unit's tiles [j0, j0 + count), `many` a
+    // thread at once.
+    auto resolve = [&](int32_t j0, int32_t ntiles, auto many) {
       constexpr int kMany = decltype(many)::value;
 #pragma unroll 1
-      for (int32_t i0 = threadIdx.x; i0 < n * kTile; i0 += kMany * 512) {
+      for (int32_t i0 = threadIdx.x; i0 < ntiles * kTile; i0 += kMany * S::kThreads) {
         int32_t p[kMany], page[kMany];
 #pragma unroll
         for (int e = 0; e < kMany; ++e) {
-          const int32_t i = i0 + e * 512, t = (split + (j0 + i / kTile) * a.splits) * kTile + i % kTile;
+          const int32_t i = i0 + e * S::kThreads, t = (split + (j0 + i / kTile) * a.splits) * kTile + i % kTile;
           p[e] = -1;
-          if (i < n * kTile && t < count) p[e] = idx ? idx[t] : t;
+          if (i < ntiles * kTile && t < count) p[e] = idx ? idx[t] : t;
         }
 #pragma unroll
         for (int e = 0; e < kMany; ++e) {
@@ -216,250 +214,439 @@ __global__ __launch_bounds__(512, 2) void latent_attention_kernel(Attend a) {
         }
 #pragma unroll
         for (int e = 0; e < kMany; ++e) {
-          const int32_t i = i0 + e * 512;
+          const int32_t i = i0 + e * S::kThreads;
           uint32_t r = kMasked;
           if (p[e] >= 0 && p[e] < L)
             r = page[e] >= 0 && (uint32_t)page[e] < a.pages_lim ? (uint32_t)page[e] * kPage + p[e] % kPage : kBad;
-          if (i < n * kTile) sh.ref[(j0 + i / kTile) % S::kRing][i % kTile] = r;
+          if (i < ntiles * kTile) {  // (a wave's 64 positions are one tile)
+            const int32_t j = (j0 + i / kTile) % S::kRing;
+            sh.ref[j][i % kTile] = r;
+            const uint64_t odd = __ballot(r >= kBad);
+            if (lane == 0) sh.special[j] = odd != 0;
+          }
         }
       }
     };
     const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[0][0];
     const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[0][0];
-    // Tile j into its buffer; every wave issues kDmaOps operations.
+    // Tile j into its buffer (zeros, past the last); every wave issues kDmaOps
+    // operations.  Lane l computes the address of the wave's position
+    // l % kGather.
     auto gather = [&](int32_t j) {
-      int lane = threadIdx.x & 63; asm volatile("" : "+v"(lane)); 
       const int buf = j % S::kBuffers;
-      const uint32_t* ref = sh.ref[j % S::kRing];
+      const uint32_t slot = j < mine ? sh.ref[j % S::kRing][S::kGather * wave + lane % S::kGather] : kMasked;
+      const bool ok = slot < kBad;
+      const uint32_t page = slot / kPage, i = slot % kPage;
+      const uint8_t* src = a.kv + (uint64_t)page * (uint64_t)a.kv_stride + i * kRowBytes;
+      src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
+      const uint32_t lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
 #pragma unroll
       for (int d = 0; d < S::kGather / S::kPerDma; ++d) {
-        const int first = S::kGather * wave + d * S::kPerDma, r = first + lane / S::kChunks;
-        const uint32_t slot = ref[r];
-        const uint8_t* src = slot < kBad ? a.kv + (int64_t)(slot / kPage) * a.kv_stride + (slot % kPage) * kRowBytes
-                                         : reinterpret_cast<const uint8_t*>(kZeroLatent);
-        dma16(src + 16 * swizzle(lane % S::kChunks, r), lds_tile + (uint32_t)((buf * kTile + first) * kRowBytes));
+        const int first = d * S::kPerDma, r = first + lane / S::kChunks;
+        const uintptr_t base = ((uintptr_t)__shfl(hi, r) << 32) | __shfl(lo, r);
+        dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
+              lds_tile + (uint32_t)((buf * kTile + S::kGather * wave + first) * kRowBytes));
       }
       if constexpr (KEY == kFp8) {
-        const uint32_t slot = ref[S::kGather * wave + lane % S::kGather];
-        const uint8_t* src = slot < kBad ? a.ks + (int64_t)(slot / kPage) * a.ks_stride + 4 * (slot % kPage)
-                                         : reinterpret_cast<const uint8_t*>(kZeroLatent);
-        if (lane < S::kGather) dma4(src, lds_scale + (uint32_t)((buf * kTile + S::kGather * wave) * 4));
+        const uint8_t* from = a.ks + (uint64_t)page * (uint64_t)a.ks_stride + 4 * i;
+        from = ok ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
+        if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((buf * kTile + S::kGather * wave) * 4));
       }
     };
 
-    // Queries: by DMA into the tile buffers, rows of 1 KiB as they stand in
-    // memory, while the first slots are resolved; from there to registers as
-    // the B operand.  Lane (n, g) holds head n's values 16*(4s' + g) + 8u .. +8
-    // of step s = 2s' + u (e4m3: two steps share a 16-byte chunk of codes), or
-    // 8*(4s + g) .. +8 (bf16).  Heads past the last are zero.  (Loading the
-    // fragments from memory took 16 bytes of 64 lines an instruction: 7 us a
-    // unit instead of 2.)
+    // Queries: by DMA into the last 64 KiB of the tile buffers, rows of 1 KiB
+    // as they stand in memory, while the first slots are resolved; from there to
+    // registers as the B operand (loading the fragments from memory took 16
+    // bytes of 64 lines an instruction: 7 us a unit instead of 2).  Lane (n,
+    // half) holds head n's values of step s: 16*(2*(s/2) + half) + 8*(s%2) .. +8
+    // (e4m3: two steps share a 16-byte chunk of codes) or 8*(2*s + half) .. +8
+    // (bf16).  Heads past the last are zero.
+    constexpr uint32_t kQueryAt = sizeof(sh.tile) - S::HT * 2 * kLatent;
 #pragma unroll
     for (int e = 0; e < S::HT / S::kWaves; ++e) {
       const int h = S::kWaves * e + wave;
       const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent)
                                             : reinterpret_cast<const uint8_t*>(kZeroLatent);
-      dma16(src + 16 * swizzle(lane, h), lds_tile + (uint32_t)(h * 2 * kLatent));
+      dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
     }
-    resolve(0, min(mine, S::kRing), std::integral_constant<int, 4>{});
+    if (threadIdx.x < 4) sh.over[threadIdx.x] = 0;
+    resolve(0, min(mine, S::kRing), std::integral_constant<int, 2>{});
     wait_vm<0>();
     barrier();
-    bf16x8 q[NQ][16];
+    constexpr int kEarly = S::kBuffers - S::HT * 2 * kLatent / (kTile * kRowBytes);  // tiles beside the queries
 #pragma unroll
-    for (int u = 0; u < NQ; ++u) {
-      const int h = 16 * (hg * NQ + u) + n;
+    for (int32_t j = 0; j < kEarly; ++j) gather(j);
+    bf16x8 q[16];
 #pragma unroll
-      for (int s = 0; s < 16; ++s) {
-        const int c = KEY == kFp8 ? 2 * (4 * (s >> 1) + g) + (s & 1) : 4 * s + g;
-        q[u][s] = *reinterpret_cast<const bf16x8*>(&sh.tile[0][0] + h * 2 * kLatent + 16 * swizzle(c, h));
-      }
+    for (int s = 0; s < 16; ++s) {
+      const int h = 32 * hg + n, c = 32 * kh + (KEY == kFp8 ? 2 * (2 * (s >> 1) + half) + (s & 1) : 2 * s + half);
+      q[s] = *reinterpret_cast<const bf16x8*>(&sh.tile[0][0] + kQueryAt + h * 2 * kLatent + 16 * swizzle(c, h));
     }
     barrier();
-    for (int32_t j = 0; j < min(mine, 3); ++j) gather(j);
 
-    f32x4 x[NQ];  // scores of the wave's positions 16*pb + 4*g + e and heads 16*(hg*NQ + u) + n
-    auto score = [&](int32_t j) {
-      int lane = threadIdx.x & 63; asm volatile("" : "+v"(lane)); const int n = lane & 15, g = lane >> 4; 
-      const uint8_t* rows = sh.tile[j % S::kBuffers];
+    // The rows of scores of a wave's products: the position that its lane reads
+    // as A operand is row n, but for kh 1 row n ^ 16, so that products 0..7 are
+    // those of the 16 positions 32*pb + 16*kh that the wave goes on with
+    // (8*(i/4) + 4*half + i%4 of them) and products 8..15 its partner's.
+    const int kr = 32 * pb + (n ^ 16 * kh);
+    auto read_k = [&](const uint8_t* rows, int t) {  // fp8: values 16 of step pair t; bf16: 8 of step t
+      return *reinterpret_cast<const u32x4*>(rows + kr * kRowBytes + 16 * swizzle((KEY == kFp8 ? 16 : 32) * kh + 2 * t + half, kr));
+    };
+    auto send = [&](const f32x16& x) {
 #pragma unroll
-      for (int u = 0; u < NQ; ++u) x[u] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      const int r = 16 * pb + n;
+      for (int k = 0; k < 2; ++k)
+        sh.part[wave & 3][kh ^ 1][k][lane] = (f32x4){x[8 + 4 * k], x[9 + 4 * k], x[10 + 4 * k], x[11 + 4 * k]};
+    };
+    float x[8];  // products of the wave's 16 positions and head 32*hg + n
+    auto receive = [&](const f32x16& mine_) {
 #pragma unroll
-      for (int s = 0; s < 16; s += KEY == kFp8 ? 2 : 1) {
-        if constexpr (KEY == kFp8) {
-          const u32x4 c = *reinterpret_cast<const u32x4*>(rows + r * kRowBytes + 16 * swizzle(4 * (s >> 1) + g, r));
-          const bf16x8 c0 = fp8x8_to_bf16x8(c.x, c.y), c1 = fp8x8_to_bf16x8(c.z, c.w);
+      for (int k = 0; k < 2; ++k) {
+        const f32x4 v = sh.part[wave & 3][kh][k][lane];
 #pragma unroll
-          for (int u = 0; u < NQ; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c0, q[u][s], x[u], 0, 0, 0);
-#pragma unroll
-          for (int u = 0; u < NQ; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c1, q[u][s + 1], x[u], 0, 0, 0);
-        } else {
-          const bf16x8 c = *reinterpret_cast<const bf16x8*>(rows + r * kRowBytes + 16 * swizzle(4 * s + g, r));
-#pragma unroll
-          for (int u = 0; u < NQ; ++u) x[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, q[u][s], x[u], 0, 0, 0);
-        }
-      }
-      const u32x4 ref = *reinterpret_cast<const u32x4*>(&sh.ref[j % S::kRing][16 * pb + 4 * g]);
-      f32x4 by = {a.scale2, a.scale2, a.scale2, a.scale2};
-      if constexpr (KEY == kFp8) by *= *reinterpret_cast<const f32x4*>(&sh.scale[j % S::kBuffers][16 * pb + 4 * g]);
-#pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = x[u][e] * by[e];
-          if (ref[e] >= kBad) v = ref[e] == kBad ? __builtin_nanf("") : -INFINITY;
-          x[u][e] = v;
-          top = fmaxf(top, v);
-        }
-        top = max_over_g(top);
-        if (g == 0) sh.mx[16 * (hg * NQ + u) + n][pb] = top;
+        for (int e = 0; e < 4; ++e) x[4 * k + e] = mine_[4 * k + e] + v[e];
       }
     };
-
-    // The references that the tile's maxima leave, and its probabilities.  Sums
-    // take them unrounded; times the latent's scale, as bf16, they go to LDS.
+    auto score = [&](int32_t j) -> f32x16 {
+      const uint8_t* rows = sh.tile[j % S::kBuffers];
+      f32x16 half0 = (f32x16)(0.0f);
+#pragma unroll
+      for (int s = 0; s < 16; s += 2) {
+        bf16x8 c0, c1;
+        if constexpr (KEY == kFp8) {
+          const u32x4 c = read_k(rows, s / 2);
+          c0 = fp8x8_to_bf16x8(c.x, c.y), c1 = fp8x8_to_bf16x8(c.z, c.w);
+        } else {
+          c0 = __builtin_bit_cast(bf16x8, read_k(rows, s)), c1 = __builtin_bit_cast(bf16x8, read_k(rows, s + 1));
+        }
+        half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[s], half0, 0, 0, 0);
+        half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[s + 1], half0, 0, 0, 0);
+      }
+      send(half0);
+      return half0;
+    };
+    const int own = 32 * pb + 16 * kh + 4 * half;  // the lane's positions: own + 8*k .. +4
+    auto read_ks = [&](int32_t j, int k) -> f32x4 {
+      if constexpr (KEY == kFp8) return *reinterpret_cast<const f32x4*>(&sh.scale[j % S::kBuffers][own + 8 * k]);
+      return (f32x4){1.f, 1.f, 1.f, 1.f};
+    };
+    float part;  // the sum of the lane's probabilities
+    // Base-2 logits of tile j less a reference, masks applied.
+    auto logits = [&](int32_t j, float ref, float (&t)[8]) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f32x4 ks = read_ks(j, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[4 * k + e] = fmaf(x[4 * k + e], a.scale2 * ks[e], -ref);
+      }
+      if (uniform(sh.special[j % S::kRing]) != 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const u32x4 slot = *reinterpret_cast<const u32x4*>(&sh.ref[j % S::kRing][own + 8 * k]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            t[4 * k + e] = slot[e] == kBad ? __builtin_nanf("") : t[4 * k + e];
+            t[4 * k + e] = slot[e] == kMasked ? -INFINITY : t[4 * k + e];
+          }
+        }
+      }
+    };
+    auto max_of = [&](const float (&t)[8]) {
+      return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+    };
+    // Probabilities: their sum unrounded; times the latents' scales, as bf16, to
+    // LDS, where a lane's 8 positions are 8 k-values of the B operand of one step
+    // of 16 positions.
+    auto weigh = [&](int32_t j, const float (&t)[8]) {
+      bf16x8 w;
+      part = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f32x4 ks = read_ks(j, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(t[4 * k + e]);
+          part += p;
+          w[4 * k + e] = (__bf16)(p * ks[e]);
+        }
+      }
+      sh.p[2 * pb + kh][32 * hg + n][half] = w;
+    };
+    // Tile j's probabilities by the reference as it is, and whether it will do:
+    // a logit more than kLazy over it, or the head's first, and it will not.
     auto probabilities = [&](int32_t j) {
-      float by[NB];  // what the sums so far are to be multiplied with
-      bool moved = false;
+      float t[8];
+      logits(j, m, t);
+      if (__ballot(max_of(t) > most) != 0) sh.over[j & 3] = 1;
+      weigh(j, t);
+    };
+    // The heads' references anew from tile j's maxima, the sums so far to match,
+    // and the tile's probabilities again.
+    auto refer = [&](int32_t j) {
+      float t[8];
+      logits(j, 0.0f, t);
+      float top = max_of(t);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const int h = 32 * hg + n;
+      if (half == 0) sh.mx[h][2 * pb + kh] = top;
+      barrier();
+      const f32x4 all = *reinterpret_cast<const f32x4*>(sh.mx[h]);
+      top = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
+      const bool moves = top - m > most;
+      const float f = moves ? (most == kLazy ? __builtin_amdgcn_exp2f(m - top) : 0.0f) : 1.0f;
+      if (moves) m = top, most = kLazy;
+      sum *= f;
+      if (pb == 0 && kh == 0 && half == 0) sh.by[h] = f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] -= m;
+      weigh(j, t);
+      barrier();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        float top = sh.mx[16 * nb + n][0];
+        const float by = sh.by[32 * nb + n];
 #pragma unroll
-        for (int k = 1; k < PB; ++k) top = fmaxf(top, sh.mx[16 * nb + n][k]);
-        const float to = top > m[nb] + kLazy ? top : m[nb];
-        by[nb] = to == m[nb] ? 1.0f : __builtin_amdgcn_exp2f(m[nb] - to);
-        moved |= to != m[nb];
-        m[nb] = to;
-      }
-      f32x4 ks = {1.f, 1.f, 1.f, 1.f};
-      if constexpr (KEY == kFp8) ks = *reinterpret_cast<const f32x4*>(&sh.scale[j % S::kBuffers][16 * pb + 4 * g]);
-#pragma unroll
-      for (int u = 0; u < NQ; ++u) {
-        float ref = m[u], f = by[u];
-#pragma unroll
-        for (int nb = NQ; nb < NB; nb += NQ) {
-          ref = hg * NQ == nb ? m[nb + u] : ref;
-          f = hg * NQ == nb ? by[nb + u] : f;
-        }
-        if (ref == -INFINITY) ref = 0.0f;  // nothing live yet: the exponentials are 0
-        float part = 0.0f;
-        bf16x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = __builtin_amdgcn_exp2f(x[u][e] - ref);
-          part += p;
-          w[e] = (__bf16)(p * ks[e]);
-        }
-        sum[u] = sum[u] * f + part;
-        const int h = 16 * (hg * NQ + u) + n, c = 2 * pb + (g >> 1);
-        *reinterpret_cast<bf16x4*>(&sh.p[j & 1][h * kTile + 8 * (c ^ (h & (kTile / 8 - 1))) + 4 * (g & 1)]) = w;
-      }
-      if (__ballot(moved) != 0) {
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb) acc[mb][nb] *= by[nb];
+        for (int mb = 0; mb < MB; ++mb) acc[mb][nb] *= by;
       }
     };
+    auto settle = [&](int32_t j) {
+      if (j == 0 || uniform(sh.over[j & 3]) != 0) refer(j);
+      sum += part;
+    };
+
+    // A operand of the outputs: 32 values 32*mb of the wave's, over step s of 16
+    // positions (slots as the probabilities': 8*(k/4) + 4*half + k%4).
+    const int lane16 = lane & 15, g = lane >> 4;
+    struct Codes {
+      v2i lo, hi;  // fp8: lo only
+    };
+    auto read_v = [&](const uint8_t* rows, int s, int mb) -> Codes {
+      Codes t;
+      if constexpr (KEY == kFp8) {
+        // 16 lanes read 8 positions x 16 values: lanes 2k, 2k+1 the 16 codes of
+        // position k, lane i gets value i of the 8 positions
+        const int k = lane16 >> 1, r = 16 * s + 8 * (k >> 2) + 4 * half + (k & 3), c = 2 * (MB * wave + mb) + (g & 1);
+        t.lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) v2i*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (lane & 1)));
+      } else {
+        // 16 lanes read 4 positions x 16 values: lanes 4k .. 4k+3 the 32 bytes of
+        // position k
+        v4s u[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * s + 8 * e + 4 * half + (lane16 >> 2);
+          const int c = 4 * (MB * wave + mb) + 2 * (g & 1) + (lane16 >> 1 & 1);
+          u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) v4s*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (lane & 1)));
+        }
+        t.lo = __builtin_bit_cast(v2i, u[0]), t.hi = __builtin_bit_cast(v2i, u[1]);
+      }
+      return t;
+    };
+    auto widen = [&](const Codes& t) -> bf16x8 {
+      if constexpr (KEY == kFp8) return fp8x8_to_bf16x8((uint32_t)t.lo.x, (uint32_t)t.lo.y);
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(t.lo, t.hi, 0, 1, 2, 3));
+    };
+    auto read_w = [&](int s, int nb) { return sh.p[s][32 * nb + n][half]; };
     auto accumulate = [&](int32_t j) {
-      int lane = threadIdx.x & 63; asm volatile("" : "+v"(lane)); const int n = lane & 15, g = lane >> 4; 
       const uint8_t* rows = sh.tile[j % S::kBuffers];
 #pragma unroll
-      for (int s = 0; s < kTile / 32; ++s) {
+      for (int s = 0; s < 4; ++s) {
         bf16x8 w[NB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int h = 16 * nb + n;
-          w[nb] = *reinterpret_cast<const bf16x8*>(&sh.p[j & 1][h * kTile + 8 * ((4 * s + g) ^ (h & (kTile / 8 - 1)))]);
-        }
+        for (int nb = 0; nb < NB; ++nb) w[nb] = read_w(s, nb);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          bf16x8 v;
-          if constexpr (KEY == kFp8) {
-            // 16 lanes read 8 positions x 16 values: lanes 2j, 2j+1 the 16
-            // codes of position j, lane n gets value n of the 8 positions
-            const int r = 32 * s + 8 * g + (n >> 1), c = MB * wave + mb;
-            const v2i t = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (__attribute__((address_space(3))) v2i*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (n & 1)));
-            v = fp8x8_to_bf16x8((uint32_t)t.x, (uint32_t)t.y);
-          } else {
-            // 16 lanes read 4 positions x 16 values: lanes 4j .. 4j+3 the 32
-            // bytes of position j
-            v4s t[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int r = 32 * s + 8 * g + 4 * k + (n >> 2), c = 2 * (MB * wave + mb) + (n >> 1 & 1);
-              t[k] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) v4s*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (n & 1)));
-            }
-            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(t[0], t[1], 0, 1, 2, 3, 4, 5, 6, 7));
-          }
+          const bf16x8 v = widen(read_v(rows, s, mb));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
-            acc[mb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[nb], acc[mb][nb], 0, 0, 0);
+            acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[nb], acc[mb][nb], 0, 0, 0);
         }
       }
     };
 
-    // A tile has arrived when at most the operations of the tiles issued after
-    // it are outstanding (they complete in order).
-    // While tile j + 1 is scored, tiles j + 2 and j + 3 are on their way; tile
-    // j's latents are added up before its successor's probabilities are taken.
-    for (int32_t j = -1; j < mine; ++j) {
-      const bool more = j + 1 < mine;
-      if (more) {
-        if (j + 3 < mine && j < 0) wait_vm<2 * S::kDmaOps>();
-        else if (j + 2 < mine) wait_vm<S::kDmaOps>();
-        else wait_vm<0>();
+    // score(j + 1), probabilities(j + 1), accumulate(j) and gather(j + 3) in one
+    // instruction stream, as if no position of tile j + 1 were masked (a tile
+    // that has some takes its probabilities again).  The first half alternates
+    // the 16 products of the scores with 8 of the outputs' and comes with the
+    // LDS reads for several products later, the conversion of the next products'
+    // codes, and a piece of the gather; the second half has the other 8 products
+    // of the outputs and the probabilities.
+    [[maybe_unused]] auto phase = [&](int32_t j) {
+      constexpr int kAhead = 3, kDmas = S::kDmas;
+      const uint8_t* kt = sh.tile[(j + 1) % S::kBuffers];
+      const uint8_t* vt = sh.tile[j % S::kBuffers];
+      u32x4 kk[kAhead];
+      Codes vv[2];
+      bf16x8 w[NB], w2[2][NB];
+      kk[0] = read_k(kt, 0);
+      vv[0] = read_v(vt, 0, 0);
+      w[0] = read_w(0, 0);
+      w[1] = read_w(0, 1);
+      kk[1] = read_k(kt, 1);
+      vv[1] = read_v(vt, 0, 1);
+      kk[2] = read_k(kt, 2);
+      uint32_t slot = sh.ref[(j + 3) % S::kRing][S::kGather * wave + lane % S::kGather];
+      slot = j + 3 < mine ? slot : kMasked;
+      const int gbuf = (j + 3) % S::kBuffers;
+      uint32_t lo = 0, hi = 0, alo[2], ahi[2];
+      f32x16 sc = (f32x16)(0.0f);
+      bf16x8 c0 = fp8x8_to_bf16x8(kk[0].x, kk[0].y), c1 = fp8x8_to_bf16x8(kk[0].z, kk[0].w), v = widen(vv[0]);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        const int i = t / 2;  // of the outputs' 8 pairs of products: step i / MB, values i % MB
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[2 * t], sc, 0, 0, 0);
+        acc[i % MB][t & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[t & 1], acc[i % MB][t & 1], 0, 0, 0);
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[2 * t + 1], sc, 0, 0, 0);
+        if (t + 1 < 8) {
+          const u32x4 c = kk[(t + 1) % kAhead];
+          c0 = fp8x8_to_bf16x8(c.x, c.y), c1 = fp8x8_to_bf16x8(c.z, c.w);
+        }
+        if (t + kAhead < 8) kk[t % kAhead] = read_k(kt, t + kAhead);
+        if (t & 1) {
+          v = widen(vv[(i + 1) & 1]);
+          vv[i & 1] = read_v(vt, (i + 2) / MB, (i + 2) % MB);
+          if (i % MB == MB - 1 && i < 3) w[0] = read_w(1, 0), w[1] = read_w(1, 1);
+        }
+        if (t >= 6) w2[t - 6][0] = read_w(t - 4, 0), w2[t - 6][1] = read_w(t - 4, 1);
+        if (t == 0) {
+          const bool ok = slot < kBad;
+          const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
+          src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
+          lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
+        }
+        // a DMA a step, its shuffles a step ahead
+        if (t >= 1 && t < 1 + kDmas) {
+          const int d = t - 1, r = d * S::kPerDma + lane / S::kChunks;
+          alo[d & 1] = __shfl(lo, r), ahi[d & 1] = __shfl(hi, r);
+        }
+        if (t >= 2 && t < 2 + kDmas) {
+          const int d = t - 2, first = d * S::kPerDma, r = first + lane / S::kChunks;
+          const uintptr_t base = ((uintptr_t)ahi[d & 1] << 32) | alo[d & 1];
+          dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
+                lds_tile + (uint32_t)((gbuf * kTile + S::kGather * wave + first) * kRowBytes));
+        }
+        if (t == 2 + kDmas) {
+          const uint8_t* from = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
+          from = slot < kBad ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
+          if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((gbuf * kTile + S::kGather * wave) * 4));
+        }
       }
-      barrier();  // tile j + 1 and tile j's probabilities are there; every wave is done with tile j - 1
-      if (j >= 0 && j + 3 < mine) {
-        gather(j + 3);
-        // half of the ring anew, past the tiles whose slots are still read
-        constexpr int kHalf = S::kRing / 2;
-        if (j - 1 >= kHalf && (j - 1) % kHalf == 0 && j - 1 + kHalf < mine)
-          resolve(j - 1 + kHalf, min(kHalf, mine - (j - 1 + kHalf)), std::integral_constant<int, 1>{});
+      __builtin_amdgcn_sched_barrier(0);
+      send(sc);
+      barrier();  // the halves are there; tile j's probabilities have been read
+      receive(sc);
+      float top = -INFINITY;
+      part = 0.0f;
+      bf16x8 out;
+      const f32x4 ks[2] = {read_ks(j + 1, 0), read_ks(j + 1, 1)};
+      auto element = [&](int e) {
+        const float by = ks[e / 4][e % 4], t = fmaf(x[e], a.scale2 * by, -m);
+        top = fmaxf(top, t);
+        const float p = __builtin_amdgcn_exp2f(t);
+        part += p;
+        out[e] = (__bf16)(p * by);
+      };
+#pragma unroll
+      for (int i = 4; i < 8; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        acc[i % MB][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w2[i / MB - 2][0], acc[i % MB][0], 0, 0, 0);
+        acc[i % MB][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w2[i / MB - 2][1], acc[i % MB][1], 0, 0, 0);
+        if (i + 1 < 8) v = widen(vv[(i + 1) & 1]);
+        if (i + 2 < 8) vv[i & 1] = read_v(vt, (i + 2) / MB, (i + 2) % MB);
+        element(2 * (i - 4));
+        element(2 * (i - 4) + 1);
       }
-      if (more) score(j + 1);
+      sh.p[2 * pb + kh][32 * hg + n][half] = out;
+      __builtin_amdgcn_sched_barrier(0);
+      if (__ballot(top > most) != 0) sh.over[(j + 1) & 3] = 1;
+    };
+    // Half of the ring anew, past the tiles whose slots are still read (from
+    // next - 4 on); `next` is the tile gathered last.
+    auto refill = [&](int32_t next) {
+      constexpr int kHalf = S::kRing / 2;
+      const int32_t done = next - 4;
+      if (done >= kHalf && done % kHalf == 0 && done + kHalf < mine)
+        resolve(done + kHalf, min(kHalf, mine - (done + kHalf)), std::integral_constant<int, 1>{});
+    };
+
+    if constexpr (KEY == kFp8) {
+      // A phase scores tile j + 1 and adds up tile j's latents, while tiles j + 2
+      // and j + 3 are on their way; one barrier a phase.  A tile has arrived when
+      // at most the operations of the tiles issued after it are outstanding
+      // (they complete in order).
+      gather(2);
+      wait_vm<2 * S::kDmaOps>();
       barrier();
-      if (j >= 0) accumulate(j);
-      if (more) probabilities(j + 1);
+      const f32x16 first = score(0);
+      barrier();
+      receive(first);
+      probabilities(0);
+      for (int32_t j = 0; j + 1 < mine; ++j) {
+        wait_vm<S::kDmaOps>();
+        barrier();  // tile j + 1 and tile j's probabilities are there; every wave is done with tile j - 1
+        settle(j);
+        if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;  // (read a phase ago, used again two phases on)
+        phase(j);
+        if (uniform(sh.special[(j + 1) % S::kRing]) != 0) probabilities(j + 1);
+        refill(j + 3);
+      }
+      wait_vm<0>();
+      barrier();
+      settle(mine - 1);
+      accumulate(mine - 1);
+    } else {
+      // Two buffers: a tile is scored and added up while the next is on its way.
+      if (kEarly < 1) gather(0);
+      for (int32_t j = 0; j < mine; ++j) {
+        wait_vm<0>();
+        barrier();  // tile j is there; every wave is done with tile j - 1
+        if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;
+        gather(j + 1);
+        refill(j + 1);
+        const f32x16 half0 = score(j);
+        barrier();
+        receive(half0);
+        probabilities(j);
+        barrier();
+        settle(j);
+        accumulate(j);
+      }
+      wait_vm<0>();
     }
     barrier();
   }
 
   // Sums over the position blocks, and the outputs of all waves as rows of
   // float32 in the tile buffers, so that they leave in whole lines.
-#pragma unroll
-  for (int u = 0; u < NQ; ++u) {
-    float s = sum[u];
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (g == 0) sh.sum[pb][16 * (hg * NQ + u) + n] = s;
+  {
+    const float s = sum + __shfl_xor(sum, 32);
+    if (half == 0) sh.sum[2 * pb + kh][32 * hg + n] = s;
+    if (half == 0 && pb == 0 && kh == 0) sh.by[32 * hg + n] = most == kLazy ? m : -INFINITY;
   }
   barrier();
   uint8_t* rows = &sh.tile[0][0];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int h = 16 * nb + n;
-    float z = sh.sum[0][h];
-#pragma unroll
-    for (int k = 1; k < PB; ++k) z += sh.sum[k][h];
-    float by = 1.0f, half = 1.0f;
+    const int h = 32 * nb + n;
+    const float z = (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]), ref = sh.by[h];
+    float by = 1.0f, root = 1.0f;
     if (a.splits > 1) {
       const int64_t ph = ((int64_t)b * a.splits + split) * a.heads + h0 + h;
       float* ml = a.part + (int64_t)a.rows * a.splits * a.heads * kLatent + 2 * ph;
-      if (h0 + h < a.heads && wave == 0 && g == 0) *reinterpret_cast<f32x2*>(ml) = (f32x2){m[nb], z};
+      if (h0 + h < a.heads && wave == 0 && half == 0) *reinterpret_cast<f32x2*>(ml) = (f32x2){ref, z};
     } else {
-      const Closing c = close_sum(m[nb], z, a.sinks && h0 + h < a.heads ? a.sinks[h0 + h] * kLog2e : -INFINITY);
-      if (a.lse && h0 + h < a.heads && wave == 0 && g == 0) a.lse[(int64_t)b * a.heads + h0 + h] = c.lse;
-      by = c.by, half = c.half;
+      const Closing c = close_sum(ref, z, a.sinks && h0 + h < a.heads ? a.sinks[h0 + h] * kLog2e : -INFINITY);
+      if (a.lse && h0 + h < a.heads && wave == 0 && half == 0) a.lse[(int64_t)b * a.heads + h0 + h] = c.lse;
+      by = c.by, root = c.half;
     }
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-      *reinterpret_cast<f32x4*>(rows + h * 4 * kLatent + 16 * swizzle((S::kDims * wave + 16 * mb) / 4 + g, h)) =
-          acc[mb][nb] * by * half * half;
+    for (int mb = 0; mb < MB; ++mb) {
+      const f32x16 o = acc[mb][nb] * by * root * root;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<f32x4*>(rows + h * 4 * kLatent + 16 * swizzle((S::kDims * wave + 32 * mb + 8 * k) / 4 + half, h)) =
+            (f32x4){o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]};
+    }
   }
   barrier();
   if (a.splits > 1 && mine == 0) return;  // a split with nothing in it leaves m and l only
@@ -533,7 +720,7 @@ constexpr int kHeadTile = 64;
 constexpr int kTile = 64;  // positions that a split has at least two of
 constexpr int32_t kMaxWidth = 1 << 24;
 
-// Splits of a row's positions: enough units for two workgroups a CU, at least
+// Splits of a row's positions: enough units for a workgroup a CU, at least
 // two tiles each.  From the scalar arguments alone (the lengths are on the
 // device).
 int splits_of(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
@@ -541,7 +728,7 @@ int splits_of(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
                                 : (int64_t)table_width * kPage;
   const int64_t tiles = (most + kTile - 1) / kTile;
   const int64_t units = (int64_t)rows * ((num_heads + kHeadTile - 1) / kHeadTile);
-  int64_t s = 2 * device_cu_count() / (units > 0 ? units : 1);
+  int64_t s = device_cu_count() / (units > 0 ? units : 1);
   if (s > tiles / 2) s = tiles / 2;
   if (s > kMaxSplits) s = kMaxSplits;
   return s < 1 ? 1 : (int)s;
@@ -607,7 +794,7 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   const int64_t groups = ((int64_t)rows * a.splits + 7) / 8 * a.head_blocks;
   if (groups > (int64_t)1 << 28) return IDX_ERR_SHAPE;
   (void)hipGetLastError();  // start from a clean error state
-  latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(512), 0, stream>>>(a);
+  latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(Shape<KEY>::kThreads), 0, stream>>>(a);
   if (a.splits > 1)
     latent_combine_kernel<<<dim3((uint32_t)(((int64_t)rows * num_heads + 3) / 4)), dim3(256), 0, stream>>>(a);
   return launch_status();
