@@ -425,92 +425,108 @@ def idx_store_keys_bf16(keys, slots, kv_pages, *, num_pages, n=None, kv_page_str
     return status
 
 
-def _device_of(named) -> torch.device | None:
-    """The one device of a call's tensors ((name, tensor or address) pairs)."""
-    dev = None
-    for name, x in named:
-        if isinstance(x, torch.Tensor):
-            if x.device.type != "cuda":
-                raise ValueError("tensors passed to the indexer library must be device tensors")
-            if dev is None:
-                dev = x.device
-            elif x.device != dev:
-                raise ValueError(f"{name} is on {x.device}, the arguments before it on {dev}")
-    return dev
+# --- the latent cache's operators (include/latent_cache.h).  Their arguments are
+# tensors; a call on a few tokens takes the GPU a few microseconds, so the checks
+# below stay short: dtype, shape, layout and device of each, once.
+
+# (the public current_stream builds an object, which takes half as long as a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _launch(name, dev, stream, check, *args) -> int:
-    """Calls the library with ``args`` and the stream, on the tensors' device
-    (whatever the current one is)."""
-    fn, handle = getattr(_lib, name), _stream_handle(stream, dev)
-    if dev is None or dev.index == torch.cuda.current_device():
+def _elsewhere(name, x, dev) -> ValueError:
+    return ValueError(f"{name} is on {x.device}, the arguments before it on " + ("cpu" if dev < 0 else f"cuda:{dev}"))
+
+
+def _dense(name, x, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of this type and shape on device ``dev``."""
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(x.shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if x.get_device() != dev:
+        raise _elsewhere(name, x, dev)
+    return x.data_ptr()
+
+
+def _rows(name, x, dims) -> int:
+    """Elements between the rows (first dim) of a bf16 tensor of ``dims`` dims
+    whose rows are dense."""
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {x.dtype}")
+    shape = x.shape
+    if len(shape) != dims:
+        raise ValueError(f"{name} must have {dims} dims, got {list(shape)}")
+    if x.is_contiguous():
+        return math.prod(shape[1:])
+    dense = 1
+    for size, step in zip(reversed(shape[1:]), reversed(x.stride()[1:])):
+        if size > 1 and step != dense:
+            raise ValueError(f"{name} must be dense behind its first dim")
+        dense *= size
+    return x.stride(0) if shape[0] > 1 else dense
+
+
+def _launch(fn, dev, stream, check, *args) -> int:
+    """Calls the library on the tensors' device, whatever the current one is."""
+    if dev < 0:
+        raise ValueError("tensors passed to the indexer library must be device tensors")
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream, dev)
+    if dev == torch.cuda.current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, handle)
     if check and status != IDX_OK:
-        raise IdxError(status, f"{name}: {idx_status_string(status)}")
+        raise IdxError(status, f"{fn.__name__}: {idx_status_string(status)}")
     return status
 
 
-def _check_rows(name, x, dim, width=None) -> None:
-    """A bf16 tensor of ``dim`` dims whose rows (all dims but the first) are
-    dense; the first dim's stride is free."""
-    if x.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {x.dtype}")
-    if x.dim() != dim or (width is not None and x.shape[-1] != width):
-        raise ValueError(f"{name} must have {dim} dims" + ("" if width is None else f", the last of {width}")
-                         + f", got {tuple(x.shape)}")
-    dense = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if size > 1 and stride != dense:
-            raise ValueError(f"{name} must be dense behind its first dim")
-        dense *= size
-
-
-def _row_stride(x) -> int:
-    """Elements between the rows of a tensor checked by ``_check_rows``."""
-    return x.stride(0) if x.shape[0] > 1 else math.prod(x.shape[1:])
-
-
-def _rotation(x, positions, inv_freq, weight, norm, leading, halves):
-    """Checks the norm and rotation's arguments; (head_dim, rope_dim, flags)."""
-    n, head_dim = x.shape[0], x.shape[-1]
+def _rotation(x, dev, positions, inv_freq, weight, norm, leading, halves):
+    """The norm and rotation's arguments: addresses of weight, positions and
+    inv_freq, rope_dim and flags."""
+    shape = x.shape
+    flags = (0 if norm else IDX_NORM_OFF) | (IDX_ROPE_LEADING if leading else 0) | (IDX_ROPE_HALVES if halves else 0)
+    w = p = f = None
+    rope = 0
+    if weight is not None:
+        if not norm:
+            raise ValueError("weight goes with the norm")
+        w = _dense("weight", weight, torch.float32, shape[-1:], dev)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    _check("positions", positions, torch.int64)
-    _check("inv_freq", inv_freq, torch.float32)
-    _check("weight", weight, torch.float32)
-    if positions is not None and positions.shape != (n,):
-        raise ValueError(f"positions must be [{n}], got {list(positions.shape)}")
-    if inv_freq is not None and inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have one dim")
-    if weight is not None and weight.shape != (head_dim,):
-        raise ValueError(f"weight must be [{head_dim}], got {list(weight.shape)}")
-    if weight is not None and not norm:
-        raise ValueError("weight goes with the norm")
-    flags = (0 if norm else IDX_NORM_OFF) | (IDX_ROPE_LEADING if leading else 0) | (IDX_ROPE_HALVES if halves else 0)
-    return head_dim, 0 if inv_freq is None else 2 * inv_freq.shape[0], flags
+    if positions is not None:
+        p = _dense("positions", positions, torch.int64, shape[:1], dev)
+        rope = 2 * inv_freq.numel()
+        f = _dense("inv_freq", inv_freq, torch.float32, (rope // 2,), dev)
+    return w, p, f, rope, flags
 
 
-def _check_pool(kv_pages, kscale, num_pages, page_bytes, kv_page_stride, kscale_page_stride) -> None:
-    """A pool given as tensors must hold the pages (``page_bytes`` of values
-    each) that it is said to hold."""
+def _pool(kv_pages, kscale, num_pages, page_bytes, kv_page_stride, kscale_page_stride, dev):
+    """Addresses of a pool and its scales, which as tensors must hold the pages
+    (``page_bytes`` of values each) that they are said to hold."""
+    kv, ks = kv_pages, kscale
     if isinstance(kv_pages, torch.Tensor):
         if not kv_pages.is_contiguous():
             raise ValueError("kv_pages must be contiguous")
-        if num_pages > 0 and kv_pages.numel() * kv_pages.element_size() < (num_pages - 1) * kv_page_stride + page_bytes:
+        if num_pages > 0 and kv_pages.nbytes < (num_pages - 1) * kv_page_stride + page_bytes:
             raise ValueError(f"kv_pages is shorter than {num_pages} pages of {kv_page_stride} bytes")
+        if kv_pages.get_device() != dev:
+            raise _elsewhere("kv_pages", kv_pages, dev)
+        kv = kv_pages.data_ptr()
     if isinstance(kscale, torch.Tensor):
-        _check("kscale", kscale, torch.float32)
-        if num_pages > 0 and kscale.numel() * 4 < (num_pages - 1) * kscale_page_stride + 4 * PAGE_POSITIONS:
+        if kscale.dtype is not torch.float32:
+            raise ValueError(f"kscale must be torch.float32, got {kscale.dtype}")
+        if not kscale.is_contiguous():
+            raise ValueError("kscale must be contiguous")
+        if num_pages > 0 and kscale.nbytes < (num_pages - 1) * kscale_page_stride + 4 * PAGE_POSITIONS:
             raise ValueError(f"kscale is shorter than {num_pages} pages of {kscale_page_stride} bytes")
-
-
-def _check_slots(slots, n) -> None:
-    _check("slots", slots, torch.int64)
-    if isinstance(slots, torch.Tensor) and slots.shape != (n,):
-        raise ValueError(f"slots must be [{n}], got {list(slots.shape)}")
+        if kscale.get_device() != dev:
+            raise _elsewhere("kscale", kscale, dev)
+        ks = kscale.data_ptr()
+    return kv, ks
 
 
 def idx_norm_rope(x, positions, inv_freq, out, *, weight=None, eps=1e-6, norm=True, leading=False,
@@ -524,14 +540,12 @@ def idx_norm_rope(x, positions, inv_freq, out, *, weight=None, eps=1e-6, norm=Tr
     inv_freq[j].  ``positions`` int64 [n] and ``inv_freq`` fp32; both None: no
     rotation.  ``norm=False``: only the rotation.
     """
-    _check_rows("x", x, 3)
-    _check("out", out, torch.bfloat16)
-    if out.shape != x.shape:
-        raise ValueError(f"out must be {list(x.shape)}, got {list(out.shape)}")
-    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
-    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight), ("out", out)))
-    return _launch("idx_norm_rope", dev, stream, check, _addr(x), _addr(weight), _addr(positions), _addr(inv_freq),
-                   _addr(out), x.shape[0], x.shape[1], head_dim, rope_dim, flags, eps, _row_stride(x))
+    stride, dev = _rows("x", x, 3), x.get_device()
+    n, heads, dim = x.shape
+    to = _dense("out", out, torch.bfloat16, x.shape, dev)
+    w, p, f, rope, flags = _rotation(x, dev, positions, inv_freq, weight, norm, leading, halves)
+    return _launch(_lib.idx_norm_rope, dev, stream, check, x.data_ptr(), w, p, f, to, n, heads, dim, rope, flags, eps,
+                   stride)
 
 
 def idx_norm_rope_store_fp8(x, positions, inv_freq, slots, kv_pages, kscale, *, num_pages, weight=None,
@@ -545,129 +559,134 @@ def idx_norm_rope_store_fp8(x, positions, inv_freq, slots, kv_pages, kscale, *, 
     strides default to the fused block of 64*D + 256 bytes; ``kscale`` is a
     tensor or a device address (fused block: kv_pages + 64*D).
     """
-    _check_rows("x", x, 2)
-    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
-    fused = PAGE_POSITIONS * (head_dim + 4)
+    stride, dev = _rows("x", x, 2), x.get_device()
+    n, dim = x.shape
+    fused = PAGE_POSITIONS * (dim + 4)
     kv_page_stride = fused if kv_page_stride is None else kv_page_stride
     kscale_page_stride = fused if kscale_page_stride is None else kscale_page_stride
-    _check_slots(slots, x.shape[0])
-    _check_pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * head_dim, kv_page_stride, kscale_page_stride)
-    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight),
-                      ("slots", slots), ("kv_pages", kv_pages), ("kscale", kscale)))
-    return _launch("idx_norm_rope_store_fp8", dev, stream, check, _addr(x), _addr(weight), _addr(positions),
-                   _addr(inv_freq), _addr(slots), x.shape[0], head_dim, rope_dim, flags, eps, _row_stride(x),
-                   _addr(kv_pages), _addr(kscale), num_pages, kv_page_stride, kscale_page_stride)
+    w, p, f, rope, flags = _rotation(x, dev, positions, inv_freq, weight, norm, leading, halves)
+    at = _dense("slots", slots, torch.int64, (n,), dev)
+    kv, ks = _pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * dim, kv_page_stride, kscale_page_stride, dev)
+    return _launch(_lib.idx_norm_rope_store_fp8, dev, stream, check, x.data_ptr(), w, p, f, at, n, dim, rope, flags, eps,
+                   stride, kv, ks, num_pages, kv_page_stride, kscale_page_stride)
 
 
 def idx_norm_rope_store_bf16(x, positions, inv_freq, slots, kv_pages, *, num_pages, weight=None, eps=1e-6,
                              norm=True, leading=False, halves=False, kv_page_stride=None, stream=None,
                              check=True) -> int:
     """bf16 counterpart of :func:`idx_norm_rope_store_fp8`: pages of 128*D bytes."""
-    _check_rows("x", x, 2)
-    head_dim, rope_dim, flags = _rotation(x, positions, inv_freq, weight, norm, leading, halves)
-    kv_page_stride = 2 * PAGE_POSITIONS * head_dim if kv_page_stride is None else kv_page_stride
-    _check_slots(slots, x.shape[0])
-    _check_pool(kv_pages, None, num_pages, 2 * PAGE_POSITIONS * head_dim, kv_page_stride, 0)
-    dev = _device_of((("x", x), ("positions", positions), ("inv_freq", inv_freq), ("weight", weight),
-                      ("slots", slots), ("kv_pages", kv_pages)))
-    return _launch("idx_norm_rope_store_bf16", dev, stream, check, _addr(x), _addr(weight), _addr(positions),
-                   _addr(inv_freq), _addr(slots), x.shape[0], head_dim, rope_dim, flags, eps, _row_stride(x),
-                   _addr(kv_pages), num_pages, kv_page_stride)
+    stride, dev = _rows("x", x, 2), x.get_device()
+    n, dim = x.shape
+    page = 2 * PAGE_POSITIONS * dim
+    kv_page_stride = page if kv_page_stride is None else kv_page_stride
+    w, p, f, rope, flags = _rotation(x, dev, positions, inv_freq, weight, norm, leading, halves)
+    at = _dense("slots", slots, torch.int64, (n,), dev)
+    kv, _ = _pool(kv_pages, None, num_pages, page, kv_page_stride, 0, dev)
+    return _launch(_lib.idx_norm_rope_store_bf16, dev, stream, check, x.data_ptr(), w, p, f, at, n, dim, rope, flags, eps,
+                   stride, kv, num_pages, kv_page_stride)
 
 
 def idx_load_slots_fp8(kv_pages, kscale, slots, out, *, num_pages, kv_page_stride=None,
                        kscale_page_stride=None, stream=None, check=True) -> int:
     """out[t] = bf16(code * scale) of pool slot slots[t], for bf16 ``out`` [n, D]
     (D 128 or 512; rows may be strided).  A slot out of range leaves its row."""
-    _check_rows("out", out, 2)
-    head_dim = out.shape[1]
-    fused = PAGE_POSITIONS * (head_dim + 4)
+    stride, dev = _rows("out", out, 2), out.get_device()
+    n, dim = out.shape
+    fused = PAGE_POSITIONS * (dim + 4)
     kv_page_stride = fused if kv_page_stride is None else kv_page_stride
     kscale_page_stride = fused if kscale_page_stride is None else kscale_page_stride
-    _check_slots(slots, out.shape[0])
-    _check_pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * head_dim, kv_page_stride, kscale_page_stride)
-    dev = _device_of((("out", out), ("slots", slots), ("kv_pages", kv_pages), ("kscale", kscale)))
-    return _launch("idx_load_slots_fp8", dev, stream, check, _addr(kv_pages), _addr(kscale), _addr(slots),
-                   out.shape[0], head_dim, num_pages, kv_page_stride, kscale_page_stride, _addr(out), _row_stride(out))
+    at = _dense("slots", slots, torch.int64, (n,), dev)
+    kv, ks = _pool(kv_pages, kscale, num_pages, PAGE_POSITIONS * dim, kv_page_stride, kscale_page_stride, dev)
+    return _launch(_lib.idx_load_slots_fp8, dev, stream, check, kv, ks, at, n, dim, num_pages, kv_page_stride,
+                   kscale_page_stride, out.data_ptr(), stride)
 
 
 def idx_load_slots_bf16(kv_pages, slots, out, *, num_pages, kv_page_stride=None, stream=None, check=True) -> int:
     """bf16 counterpart of :func:`idx_load_slots_fp8`."""
-    _check_rows("out", out, 2)
-    head_dim = out.shape[1]
-    kv_page_stride = 2 * PAGE_POSITIONS * head_dim if kv_page_stride is None else kv_page_stride
-    _check_slots(slots, out.shape[0])
-    _check_pool(kv_pages, None, num_pages, 2 * PAGE_POSITIONS * head_dim, kv_page_stride, 0)
-    dev = _device_of((("out", out), ("slots", slots), ("kv_pages", kv_pages)))
-    return _launch("idx_load_slots_bf16", dev, stream, check, _addr(kv_pages), _addr(slots), out.shape[0], head_dim,
-                   num_pages, kv_page_stride, _addr(out), _row_stride(out))
+    stride, dev = _rows("out", out, 2), out.get_device()
+    n, dim = out.shape
+    page = 2 * PAGE_POSITIONS * dim
+    kv_page_stride = page if kv_page_stride is None else kv_page_stride
+    at = _dense("slots", slots, torch.int64, (n,), dev)
+    kv, _ = _pool(kv_pages, None, num_pages, page, kv_page_stride, 0, dev)
+    return _launch(_lib.idx_load_slots_bf16, dev, stream, check, kv, at, n, dim, num_pages, kv_page_stride,
+                   out.data_ptr(), stride)
 
 
 def idx_latent_attention_workspace(rows, num_heads, table_width, k=None) -> int:
     """Bytes of workspace that a latent attention call of these sizes needs on
     the current device (``k`` None: no selection)."""
-    return int(_lib.idx_latent_attention_workspace(rows, num_heads, table_width, -1 if k is None else k))
+    return _lib.idx_latent_attention_workspace(rows, num_heads, table_width, -1 if k is None else k)
 
 
 def _latent_workspace(rows, heads, width, k, dev, stream) -> torch.Tensor | None:
     """A workspace from torch's allocator, on the call's device and stream."""
-    if dev is None:
+    if dev < 0:
         return None
-    with torch.cuda.device(dev):
-        need = idx_latent_attention_workspace(rows, heads, width, k)
-        if need <= 0:
-            return None
-        if stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=dev)
-        if not isinstance(stream, torch.cuda.Stream):
-            raise ValueError("a call on a raw stream handle needs its own workspace")
-        with torch.cuda.stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=dev)
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _latent_workspace(rows, heads, width, k, dev, stream)
+    need = idx_latent_attention_workspace(rows, heads, width, k)
+    if need <= 0:
+        return None
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+    if not isinstance(stream, torch.cuda.Stream):
+        raise ValueError("a call on a raw stream handle needs its own workspace")
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
 
 
-def _latent_attention(name, q, kv_pages, kscale, page_table, topk_idx, seqlens, out, lse, scale, num_pages, sinks,
+def _latent_attention(fn, q, kv_pages, kscale, page_table, topk_idx, seqlens, out, lse, scale, num_pages, sinks,
                       row_table, workspace, strides, page_table_row_stride, stream, check):
     """``kscale`` and ``strides`` are tuples: those of the pool's key type."""
-    _check("q", q, torch.bfloat16)
-    _check("out", out, torch.bfloat16)
-    if q.dim() != 3 or out.shape != q.shape:
-        raise ValueError(f"q and out must be [rows, heads, {LATENT_DIM}], got {list(q.shape)} and {list(out.shape)}")
-    rows, heads, head_dim = q.shape
-    _check("page_table", page_table, torch.int32, dense_rows=True)
+    dev, shape = q.get_device(), q.shape
+    if len(shape) != 3 or out.shape != shape:
+        raise ValueError(f"q and out must be [rows, heads, {LATENT_DIM}], got {list(shape)} and {list(out.shape)}")
+    rows, heads, dim = shape
+    from_q = _dense("q", q, torch.bfloat16, shape, dev)
+    to = _dense("out", out, torch.bfloat16, shape, dev)
+    if page_table.dtype is not torch.int32:
+        raise ValueError(f"page_table must be torch.int32, got {page_table.dtype}")
     if page_table.dim() != 2:
         raise ValueError("page_table must have two dims")
     tables, width = page_table.shape
-    for what, x, dtype, shape in (("seqlens", seqlens, torch.int32, (rows,)), ("sinks", sinks, torch.float32, (heads,)),
-                                  ("lse", lse, torch.float32, (rows, heads)), ("row_table", row_table, torch.int32, (rows,))):
-        if x is not None:
-            _check(what, x, dtype)
-            if x.shape != shape:
-                raise ValueError(f"{what} must be {list(shape)}, got {list(x.shape)}")
-    k = None
+    step, unit = page_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("page_table must be unit-stride along its last dim")
+    if page_table.get_device() != dev:
+        raise _elsewhere("page_table", page_table, dev)
+    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
+    idx = sink = log = which = None
+    k = -1
     if topk_idx is not None:
-        _check("topk_idx", topk_idx, torch.int32)
         if topk_idx.dim() != 2 or topk_idx.shape[0] != rows:
             raise ValueError(f"topk_idx must be [{rows}, k], got {list(topk_idx.shape)}")
         k = topk_idx.shape[1]
+        idx = _dense("topk_idx", topk_idx, torch.int32, (rows, k), dev)
+    if sinks is not None:
+        sink = _dense("sinks", sinks, torch.float32, (heads,), dev)
+    if lse is not None:
+        log = _dense("lse", lse, torch.float32, (rows, heads), dev)
+    if row_table is not None:
+        which = _dense("row_table", row_table, torch.int32, (rows,), dev)
     if page_table_row_stride is None:
         shared = tables == 1 and row_table is None
-        page_table_row_stride = 0 if shared else page_table.stride(0)
+        page_table_row_stride = 0 if shared else step
         if not shared and row_table is None and tables < rows:
             raise ValueError(f"page_table holds {tables} tables for {rows} rows")
-    _check_pool(kv_pages, kscale[0] if kscale else None, num_pages,
-                PAGE_POSITIONS * LATENT_DIM * (1 if kscale else 2), strides[0], strides[-1])
-    dev = _device_of((("q", q), ("kv_pages", kv_pages), ("kscale", kscale[0] if kscale else None),
-                      ("page_table", page_table), ("topk_idx", topk_idx), ("seqlens", seqlens), ("out", out),
-                      ("lse", lse), ("sinks", sinks), ("row_table", row_table), ("workspace", workspace)))
+    kv, *ks = _pool(kv_pages, kscale[0] if kscale else None, num_pages,
+                    PAGE_POSITIONS * LATENT_DIM * (1 if kscale else 2), strides[0], strides[-1], dev)
     if workspace is None:
-        workspace = _latent_workspace(rows, heads, width, k, dev, stream)
+        workspace = _latent_workspace(rows, heads, width, None if k < 0 else k, dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return _launch(name, dev, stream, check, _addr(q), _addr(kv_pages), *[_addr(x) for x in kscale], _addr(page_table),
-                   _addr(row_table), 0 if row_table is None else tables, _addr(topk_idx), _addr(seqlens), _addr(sinks),
-                   _addr(out), _addr(lse), rows, heads, head_dim, width, num_pages, *strides, page_table_row_stride,
-                   -1 if k is None else k, scale, _addr(workspace), nbytes)
+    elif workspace.get_device() != dev:
+        raise _elsewhere("workspace", workspace, dev)
+    space, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    return _launch(fn, dev, stream, check, from_q, kv, *(ks if kscale else ()), page_table.data_ptr(), which,
+                   0 if which is None else tables, idx, lengths, sink, to, log, rows, heads, dim, width, num_pages,
+                   *strides, page_table_row_stride, k, scale, space, nbytes)
 
 
 def idx_latent_attention_fp8(q, kv_pages, kscale, page_table, topk_idx, seqlens, out, lse=None, *, scale, num_pages,
@@ -685,7 +704,7 @@ def idx_latent_attention_fp8(q, kv_pages, kscale, page_table, topk_idx, seqlens,
     ``workspace``: a tensor of :func:`idx_latent_attention_workspace` bytes, of this
     call's own while it runs; None takes one from torch's allocator.
     """
-    return _latent_attention("idx_latent_attention_fp8", q, kv_pages, (kscale,), page_table, topk_idx, seqlens, out,
+    return _latent_attention(_lib.idx_latent_attention_fp8, q, kv_pages, (kscale,), page_table, topk_idx, seqlens, out,
                              lse, scale, num_pages, sinks, row_table, workspace, (kv_page_stride, kscale_page_stride),
                              page_table_row_stride, stream, check)
 
@@ -695,7 +714,7 @@ def idx_latent_attention_bf16(q, kv_pages, page_table, topk_idx, seqlens, out, l
                               kv_page_stride=2 * PAGE_POSITIONS * LATENT_DIM, page_table_row_stride=None, stream=None,
                               check=True) -> int:
     """bf16 counterpart of :func:`idx_latent_attention_fp8`."""
-    return _latent_attention("idx_latent_attention_bf16", q, kv_pages, (), page_table, topk_idx, seqlens, out, lse,
+    return _latent_attention(_lib.idx_latent_attention_bf16, q, kv_pages, (), page_table, topk_idx, seqlens, out, lse,
                              scale, num_pages, sinks, row_table, workspace, (kv_page_stride,), page_table_row_stride,
                              stream, check)
 

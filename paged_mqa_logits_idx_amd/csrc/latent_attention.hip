@@ -463,102 +463,148 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
     };
 
-    // score(j + 1), probabilities(j + 1), accumulate(j) and gather(j + 3) in one
-    // instruction stream, as if no position of tile j + 1 were masked (a tile
-    // that has some takes its probabilities again).  The first half alternates
-    // the 16 products of the scores with 8 of the outputs' and comes with the
-    // LDS reads for several products later, the conversion of the next products'
-    // codes, and a piece of the gather; the second half has the other 8 products
-    // of the outputs and the probabilities.
-    [[maybe_unused]] auto phase = [&](int32_t j) {
+    // One instruction stream a tile.  Phase j scores tile j + 1, adds up tile j's
+    // latents and gathers tile j + 3, as if no position of tile j + 1 were masked
+    // (a tile that has some takes its probabilities again).  The 16 products of
+    // the scores and the 8 pairs of products of the outputs (pair i: step i / 2 of
+    // 16 positions, values i % 2) are laid out so that the matrix units have work
+    // whose operands are in registers wherever a wave would wait:
+    //   the last pairs of tile j - 1      while the first reads after the barrier
+    //   and pairs 0, 1 of tile j          are on their way,
+    //   pairs 2, 3 among the scores       with the LDS reads three steps ahead, the
+    //                                     conversion of the next codes, the gather,
+    //   pair 4                            while the halves of scores change hands,
+    //   pair 5                            among the probabilities;
+    //   pairs 6, 7                        are left to the next phase.
+    Codes late[2];        // pairs 6, 7 of the tile before: codes and probabilities
+    bf16x8 late_w[NB];
+    auto add = [&](const bf16x8& v, const bf16x8 (&w)[NB], int mb) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[nb], acc[mb][nb], 0, 0, 0);
+    };
+    auto add_late = [&]() {
+      add(widen(late[0]), late_w, 0);
+      add(widen(late[1]), late_w, 1);
+    };
+    // FIRST: tile 0 is scored, nothing added up; LAST: the other way round.
+    auto phase = [&](int32_t j, auto first, auto last) {
+      constexpr bool kScore = !decltype(last)::value, kAdd = !decltype(first)::value;
       constexpr int kAhead = 3, kDmas = S::kDmas;
       const uint8_t* kt = sh.tile[(j + 1) % S::kBuffers];
       const uint8_t* vt = sh.tile[j % S::kBuffers];
-      u32x4 kk[kAhead];
-      Codes vv[2];
-      bf16x8 w[NB], w2[2][NB];
-      kk[0] = read_k(kt, 0);
-      vv[0] = read_v(vt, 0, 0);
-      w[0] = read_w(0, 0);
-      w[1] = read_w(0, 1);
-      kk[1] = read_k(kt, 1);
-      vv[1] = read_v(vt, 0, 1);
-      kk[2] = read_k(kt, 2);
-      uint32_t slot = sh.ref[(j + 3) % S::kRing][S::kGather * wave + lane % S::kGather];
-      slot = j + 3 < mine ? slot : kMasked;
       const int gbuf = (j + 3) % S::kBuffers;
-      uint32_t lo = 0, hi = 0, alo[2], ahi[2];
+      uint32_t over = 0, slot = 0, lo = 0, hi = 0, alo[2], ahi[2];
+      u32x4 kk[kAhead];
+      bf16x8 w[2][NB], c0, c1, v;
+      Codes vv[2];
+      if constexpr (kAdd) {
+        over = sh.over[j & 3];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) w[0][nb] = read_w(0, nb);
+        vv[0] = read_v(vt, 0, 0);
+        vv[1] = read_v(vt, 0, 1);
+      }
+      if constexpr (kScore) {
+#pragma unroll
+        for (int t = 0; t < kAhead; ++t) kk[t] = read_k(kt, t);
+        if constexpr (kAdd) slot = sh.ref[(j + 3) % S::kRing][S::kGather * wave + lane % S::kGather];
+      }
+      if constexpr (kAdd) {
+        if (j > 0) add_late();
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0 || uniform(over) != 0) {
+          refer(j);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) w[0][nb] = read_w(0, nb);
+        }
+        sum += part;
+        if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;  // (read a phase ago, used again two phases on)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) w[1][nb] = read_w(1, nb);
+        add(widen(vv[0]), w[0], 0);
+        vv[0] = read_v(vt, 1, 0);
+        add(widen(vv[1]), w[0], 1);
+        vv[1] = read_v(vt, 1, 1);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) w[0][nb] = read_w(2, nb);
+      }
       f32x16 sc = (f32x16)(0.0f);
-      bf16x8 c0 = fp8x8_to_bf16x8(kk[0].x, kk[0].y), c1 = fp8x8_to_bf16x8(kk[0].z, kk[0].w), v = widen(vv[0]);
+      if constexpr (kScore) c0 = fp8x8_to_bf16x8(kk[0].x, kk[0].y), c1 = fp8x8_to_bf16x8(kk[0].z, kk[0].w);
+      if constexpr (kAdd) v = widen(vv[0]);
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         __builtin_amdgcn_sched_barrier(0);
-        const int i = t / 2;  // of the outputs' 8 pairs of products: step i / MB, values i % MB
-        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[2 * t], sc, 0, 0, 0);
-        acc[i % MB][t & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[t & 1], acc[i % MB][t & 1], 0, 0, 0);
-        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[2 * t + 1], sc, 0, 0, 0);
-        if (t + 1 < 8) {
+        const int mb = t / 4, nb = t / 2 % 2;  // pairs 2, 3: a product in every other step
+        if constexpr (kScore) sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[2 * t], sc, 0, 0, 0);
+        if (kAdd && t % 2 == 0) acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[1][nb], acc[mb][nb], 0, 0, 0);
+        if constexpr (kScore) sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[2 * t + 1], sc, 0, 0, 0);
+        if (kScore && t + 1 < 8) {
           const u32x4 c = kk[(t + 1) % kAhead];
           c0 = fp8x8_to_bf16x8(c.x, c.y), c1 = fp8x8_to_bf16x8(c.z, c.w);
         }
-        if (t + kAhead < 8) kk[t % kAhead] = read_k(kt, t + kAhead);
-        if (t & 1) {
-          v = widen(vv[(i + 1) & 1]);
-          vv[i & 1] = read_v(vt, (i + 2) / MB, (i + 2) % MB);
-          if (i % MB == MB - 1 && i < 3) w[0] = read_w(1, 0), w[1] = read_w(1, 1);
-        }
-        if (t >= 6) w2[t - 6][0] = read_w(t - 4, 0), w2[t - 6][1] = read_w(t - 4, 1);
-        if (t == 0) {
-          const bool ok = slot < kBad;
-          const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
-          src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
-          lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
-        }
-        // a DMA a step, its shuffles a step ahead
-        if (t >= 1 && t < 1 + kDmas) {
-          const int d = t - 1, r = d * S::kPerDma + lane / S::kChunks;
-          alo[d & 1] = __shfl(lo, r), ahi[d & 1] = __shfl(hi, r);
-        }
-        if (t >= 2 && t < 2 + kDmas) {
-          const int d = t - 2, first = d * S::kPerDma, r = first + lane / S::kChunks;
-          const uintptr_t base = ((uintptr_t)ahi[d & 1] << 32) | alo[d & 1];
-          dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
-                lds_tile + (uint32_t)((gbuf * kTile + S::kGather * wave + first) * kRowBytes));
-        }
-        if (t == 2 + kDmas) {
-          const uint8_t* from = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
-          from = slot < kBad ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
-          if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((gbuf * kTile + S::kGather * wave) * 4));
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      send(sc);
-      barrier();  // the halves are there; tile j's probabilities have been read
-      receive(sc);
-      float top = -INFINITY;
-      part = 0.0f;
-      bf16x8 out;
-      const f32x4 ks[2] = {read_ks(j + 1, 0), read_ks(j + 1, 1)};
-      auto element = [&](int e) {
-        const float by = ks[e / 4][e % 4], t = fmaf(x[e], a.scale2 * by, -m);
-        top = fmaxf(top, t);
-        const float p = __builtin_amdgcn_exp2f(t);
-        part += p;
-        out[e] = (__bf16)(p * by);
-      };
+        if (kScore && t + kAhead < 8) kk[t % kAhead] = read_k(kt, t + kAhead);
+        if constexpr (kAdd) {
+          if (t == 3) v = widen(vv[1]), vv[0] = read_v(vt, 2, 0);
+          if (t == 4) vv[1] = read_v(vt, 2, 1);
+          if (t == 7) {
+            v = widen(vv[0]);
 #pragma unroll
-      for (int i = 4; i < 8; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
-        acc[i % MB][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w2[i / MB - 2][0], acc[i % MB][0], 0, 0, 0);
-        acc[i % MB][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w2[i / MB - 2][1], acc[i % MB][1], 0, 0, 0);
-        if (i + 1 < 8) v = widen(vv[(i + 1) & 1]);
-        if (i + 2 < 8) vv[i & 1] = read_v(vt, (i + 2) / MB, (i + 2) % MB);
-        element(2 * (i - 4));
-        element(2 * (i - 4) + 1);
+            for (int e = 0; e < NB; ++e) late_w[e] = read_w(3, e);
+            late[0] = read_v(vt, 3, 0), late[1] = read_v(vt, 3, 1);
+          }
+        }
+        if constexpr (kScore && kAdd) {
+          if (t == 0) {
+            slot = j + 3 < mine ? slot : kMasked;
+            const bool ok = slot < kBad;
+            const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
+            src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
+            lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
+          }
+          // a DMA a step, its shuffles a step ahead
+          if (t >= 1 && t < 1 + kDmas) {
+            const int d = t - 1, r = d * S::kPerDma + lane / S::kChunks;
+            alo[d & 1] = __shfl(lo, r), ahi[d & 1] = __shfl(hi, r);
+          }
+          if (t >= 2 && t < 2 + kDmas) {
+            const int d = t - 2, first_ = d * S::kPerDma, r = first_ + lane / S::kChunks;
+            const uintptr_t base = ((uintptr_t)ahi[d & 1] << 32) | alo[d & 1];
+            dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
+                  lds_tile + (uint32_t)((gbuf * kTile + S::kGather * wave + first_) * kRowBytes));
+          }
+          if (t == 2 + kDmas) {
+            const uint8_t* from = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
+            from = slot < kBad ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
+            if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((gbuf * kTile + S::kGather * wave) * 4));
+          }
+        }
       }
-      sh.p[2 * pb + kh][32 * hg + n][half] = out;
       __builtin_amdgcn_sched_barrier(0);
-      if (__ballot(top > most) != 0) sh.over[(j + 1) & 3] = 1;
+      if constexpr (kScore) send(sc);
+      if constexpr (kAdd) add(v, w[0], 0);
+      if constexpr (kScore) {
+        barrier();  // the halves are there; tile j's probabilities have been read
+        receive(sc);
+        const f32x4 ks[2] = {read_ks(j + 1, 0), read_ks(j + 1, 1)};
+        if constexpr (kAdd) add(widen(vv[1]), w[0], 1);
+        float top = -INFINITY;
+        part = 0.0f;
+        bf16x8 out;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float by = ks[e / 4][e % 4], t = fmaf(x[e], a.scale2 * by, -m);
+          top = fmaxf(top, t);
+          const float p = __builtin_amdgcn_exp2f(t);
+          part += p;
+          out[e] = (__bf16)(p * by);
+        }
+        sh.p[2 * pb + kh][32 * hg + n][half] = out;
+        if (__ballot(top > most) != 0) sh.over[(j + 1) & 3] = 1;
+        if (uniform(sh.special[(j + 1) % S::kRing]) != 0) probabilities(j + 1);
+      } else {
+        add(widen(vv[1]), w[0], 1);
+        add_late();
+      }
     };
     // Half of the ring anew, past the tiles whose slots are still read (from
     // next - 4 on); `next` is the tile gathered last.
@@ -570,30 +616,23 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     };
 
     if constexpr (KEY == kFp8) {
-      // A phase scores tile j + 1 and adds up tile j's latents, while tiles j + 2
-      // and j + 3 are on their way; one barrier a phase.  A tile has arrived when
-      // at most the operations of the tiles issued after it are outstanding
+      // Tiles j + 2 and j + 3 are on their way during phase j.  A tile has arrived
+      // when at most the operations of the tiles issued after it are outstanding
       // (they complete in order).
       gather(2);
       wait_vm<2 * S::kDmaOps>();
       barrier();
-      const f32x16 first = score(0);
-      barrier();
-      receive(first);
-      probabilities(0);
-      for (int32_t j = 0; j + 1 < mine; ++j) {
+      phase(-1, std::true_type{}, std::false_type{});
+      int32_t j = 0;
+      for (; j + 1 < mine; ++j) {
         wait_vm<S::kDmaOps>();
         barrier();  // tile j + 1 and tile j's probabilities are there; every wave is done with tile j - 1
-        settle(j);
-        if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;  // (read a phase ago, used again two phases on)
-        phase(j);
-        if (uniform(sh.special[(j + 1) % S::kRing]) != 0) probabilities(j + 1);
+        phase(j, std::false_type{}, std::false_type{});
         refill(j + 3);
       }
       wait_vm<0>();
       barrier();
-      settle(mine - 1);
-      accumulate(mine - 1);
+      phase(j, std::false_type{}, std::true_type{});
     } else {
       // Two buffers: a tile is scored and added up while the next is on its way.
       if (kEarly < 1) gather(0);
