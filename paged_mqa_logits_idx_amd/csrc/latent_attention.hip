@@ -230,28 +230,36 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[0][0];
     const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[0][0];
     // Tile j into its buffer (zeros, past the last); every wave issues kDmaOps
-    // operations.  Lane l computes the address of the wave's position
-    // l % kGather.
-    auto gather = [&](int32_t j) {
-      const int buf = j % S::kBuffers;
-      const uint32_t slot = j < mine ? sh.ref[j % S::kRing][S::kGather * wave + lane % S::kGather] : kMasked;
+    // operations.  Lane l holds the address of the wave's position l % kGather.
+    struct Source {
+      uint32_t lo, hi;      // of the latent
+      const uint8_t* scale;
+    };
+    auto source_of = [&](int32_t j) -> Source {
+      uint32_t slot = sh.ref[j % S::kRing][S::kGather * wave + lane % S::kGather];
+      slot = j < mine ? slot : kMasked;
       const bool ok = slot < kBad;
-      const uint32_t page = slot / kPage, i = slot % kPage;
-      const uint8_t* src = a.kv + (uint64_t)page * (uint64_t)a.kv_stride + i * kRowBytes;
-      src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
-      const uint32_t lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
-#pragma unroll
-      for (int d = 0; d < S::kGather / S::kPerDma; ++d) {
-        const int first = d * S::kPerDma, r = first + lane / S::kChunks;
-        const uintptr_t base = ((uintptr_t)__shfl(hi, r) << 32) | __shfl(lo, r);
+      const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroLatent);
+      const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
+      src = ok ? src : zero;
+      Source from = {(uint32_t)(uintptr_t)src, (uint32_t)((uintptr_t)src >> 32), zero};
+      if (KEY == kFp8 && ok) from.scale = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
+      return from;
+    };
+    auto gather_part = [&](int32_t j, const Source& from, int d) {
+      const int buf = j % S::kBuffers, first = d * S::kPerDma, r = first + lane / S::kChunks;
+      if (d < S::kDmas) {
+        const uintptr_t base = ((uintptr_t)__shfl(from.hi, r) << 32) | __shfl(from.lo, r);
         dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
               lds_tile + (uint32_t)((buf * kTile + S::kGather * wave + first) * kRowBytes));
+      } else if (lane < S::kGather) {
+        dma4(from.scale, lds_scale + (uint32_t)((buf * kTile + S::kGather * wave) * 4));
       }
-      if constexpr (KEY == kFp8) {
-        const uint8_t* from = a.ks + (uint64_t)page * (uint64_t)a.ks_stride + 4 * i;
-        from = ok ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
-        if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((buf * kTile + S::kGather * wave) * 4));
-      }
+    };
+    auto gather = [&](int32_t j) {
+      const Source from = source_of(j);
+#pragma unroll
+      for (int d = 0; d < S::kDmaOps; ++d) gather_part(j, from, d);
     };
 
     // Queries: by DMA into the last 64 KiB of the tile buffers, rows of 1 KiB
@@ -469,34 +477,29 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     // the scores and the 8 pairs of products of the outputs (pair i: step i / 2 of
     // 16 positions, values i % 2) are laid out so that the matrix units have work
     // whose operands are in registers wherever a wave would wait:
-    //   the last pairs of tile j - 1      while the first reads after the barrier
-    //   and pairs 0, 1 of tile j          are on their way,
-    //   pairs 2, 3 among the scores       with the LDS reads three steps ahead, the
-    //                                     conversion of the next codes, the gather,
-    //   pair 4                            while the halves of scores change hands,
-    //   pair 5                            among the probabilities;
-    //   pairs 6, 7                        are left to the next phase.
-    Codes late[2];        // pairs 6, 7 of the tile before: codes and probabilities
-    bf16x8 late_w[NB];
+    //   pairs 0, 1       while the first codes of tile j + 1 are read,
+    //   pairs 2, 3       among the scores, with the LDS reads three steps ahead,
+    //                    the conversion of the next codes and the gather,
+    //   pairs 4 .. 7     in the time of the probabilities, before them in one of
+    //                    a SIMD's two waves and behind them in the other.
+    // The gather's five operations stand apart: the memory path takes one in
+    // about 50 cycles, and a wave whose operation has to wait issues nothing else
+    // (all in one place they held up every phase by 1500 cycles).
     auto add = [&](const bf16x8& v, const bf16x8 (&w)[NB], int mb) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[nb], acc[mb][nb], 0, 0, 0);
     };
-    auto add_late = [&]() {
-      add(widen(late[0]), late_w, 0);
-      add(widen(late[1]), late_w, 1);
-    };
     // FIRST: tile 0 is scored, nothing added up; LAST: the other way round.
     auto phase = [&](int32_t j, auto first, auto last) {
       constexpr bool kScore = !decltype(last)::value, kAdd = !decltype(first)::value;
-      constexpr int kAhead = 3, kDmas = S::kDmas;
+      constexpr int kAhead = 3;
       const uint8_t* kt = sh.tile[(j + 1) % S::kBuffers];
       const uint8_t* vt = sh.tile[j % S::kBuffers];
-      const int gbuf = (j + 3) % S::kBuffers;
-      uint32_t over = 0, slot = 0, lo = 0, hi = 0, alo[2], ahi[2];
+      uint32_t over = 0, special = 0;
       u32x4 kk[kAhead];
-      bf16x8 w[2][NB], c0, c1, v;
-      Codes vv[2];
+      bf16x8 w[4][NB], c0, c1, v;
+      Codes vv[4];
+      Source from;
       if constexpr (kAdd) {
         over = sh.over[j & 3];
 #pragma unroll
@@ -507,11 +510,9 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       if constexpr (kScore) {
 #pragma unroll
         for (int t = 0; t < kAhead; ++t) kk[t] = read_k(kt, t);
-        if constexpr (kAdd) slot = sh.ref[(j + 3) % S::kRing][S::kGather * wave + lane % S::kGather];
+        special = sh.special[(j + 1) % S::kRing];
       }
       if constexpr (kAdd) {
-        if (j > 0) add_late();
-        __builtin_amdgcn_sched_barrier(0);
         if (j == 0 || uniform(over) != 0) {
           refer(j);
 #pragma unroll
@@ -525,8 +526,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         vv[0] = read_v(vt, 1, 0);
         add(widen(vv[1]), w[0], 1);
         vv[1] = read_v(vt, 1, 1);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) w[0][nb] = read_w(2, nb);
+        if constexpr (kScore) from = source_of(j + 3);
       }
       f32x16 sc = (f32x16)(0.0f);
       if constexpr (kScore) c0 = fp8x8_to_bf16x8(kk[0].x, kk[0].y), c1 = fp8x8_to_bf16x8(kk[0].z, kk[0].w);
@@ -544,49 +544,29 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         }
         if (kScore && t + kAhead < 8) kk[t % kAhead] = read_k(kt, t + kAhead);
         if constexpr (kAdd) {
-          if (t == 3) v = widen(vv[1]), vv[0] = read_v(vt, 2, 0);
-          if (t == 4) vv[1] = read_v(vt, 2, 1);
-          if (t == 7) {
-            v = widen(vv[0]);
-#pragma unroll
-            for (int e = 0; e < NB; ++e) late_w[e] = read_w(3, e);
-            late[0] = read_v(vt, 3, 0), late[1] = read_v(vt, 3, 1);
-          }
+          if (t == 3) v = widen(vv[1]);
+          if (t >= 4) vv[t - 4] = read_v(vt, 2 + (t - 4) / MB, (t - 4) % MB);
+          if (t >= 6) w[t - 4][0] = read_w(t - 4, 0), w[t - 4][1] = read_w(t - 4, 1);
         }
         if constexpr (kScore && kAdd) {
-          if (t == 0) {
-            slot = j + 3 < mine ? slot : kMasked;
-            const bool ok = slot < kBad;
-            const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
-            src = ok ? src : reinterpret_cast<const uint8_t*>(kZeroLatent);
-            lo = (uint32_t)(uintptr_t)src, hi = (uint32_t)((uintptr_t)src >> 32);
-          }
-          // a DMA a step, its shuffles a step ahead
-          if (t >= 1 && t < 1 + kDmas) {
-            const int d = t - 1, r = d * S::kPerDma + lane / S::kChunks;
-            alo[d & 1] = __shfl(lo, r), ahi[d & 1] = __shfl(hi, r);
-          }
-          if (t >= 2 && t < 2 + kDmas) {
-            const int d = t - 2, first_ = d * S::kPerDma, r = first_ + lane / S::kChunks;
-            const uintptr_t base = ((uintptr_t)ahi[d & 1] << 32) | alo[d & 1];
-            dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
-                  lds_tile + (uint32_t)((gbuf * kTile + S::kGather * wave + first_) * kRowBytes));
-          }
-          if (t == 2 + kDmas) {
-            const uint8_t* from = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
-            from = slot < kBad ? from : reinterpret_cast<const uint8_t*>(kZeroLatent);
-            if (lane < S::kGather) dma4(from, lds_scale + (uint32_t)((gbuf * kTile + S::kGather * wave) * 4));
-          }
+          if (t == 1 || t == 4) gather_part(j + 3, from, t / 4);
+          if (t == 7) gather_part(j + 3, from, 2);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (kScore) send(sc);
-      if constexpr (kAdd) add(v, w[0], 0);
       if constexpr (kScore) {
+        send(sc);
         barrier();  // the halves are there; tile j's probabilities have been read
         receive(sc);
+      }
+      auto outputs = [&]() {
+        if constexpr (kAdd) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) add(widen(vv[i]), w[2 + i / MB], i % MB);
+        }
+      };
+      auto chances = [&]() {
         const f32x4 ks[2] = {read_ks(j + 1, 0), read_ks(j + 1, 1)};
-        if constexpr (kAdd) add(widen(vv[1]), w[0], 1);
         float top = -INFINITY;
         part = 0.0f;
         bf16x8 out;
@@ -600,11 +580,21 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         }
         sh.p[2 * pb + kh][32 * hg + n][half] = out;
         if (__ballot(top > most) != 0) sh.over[(j + 1) & 3] = 1;
-        if (uniform(sh.special[(j + 1) % S::kRing]) != 0) probabilities(j + 1);
+      };
+      if constexpr (kScore && kAdd) {
+        gather_part(j + 3, from, 3);
+        if (kh == 0) outputs();
+        __builtin_amdgcn_sched_barrier(0);
+        chances();
+        __builtin_amdgcn_sched_barrier(0);
+        if (kh != 0) outputs();
+        gather_part(j + 3, from, 4);
+      } else if constexpr (kScore) {
+        chances();
       } else {
-        add(widen(vv[1]), w[0], 1);
-        add_late();
+        outputs();
       }
+      if (kScore && uniform(special) != 0) probabilities(j + 1);
     };
     // Half of the ring anew, past the tiles whose slots are still read (from
     // next - 4 on); `next` is the tile gathered last.
