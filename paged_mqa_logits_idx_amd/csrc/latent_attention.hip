@@ -40,6 +40,9 @@ namespace {
 constexpr float kLazy = 8.0f;       // base-2 logits that the maximum may exceed its reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kHeadTile = 64;       // heads of a unit
+constexpr int kTile = 64;           // positions of a tile
+constexpr int kPartials = kHeadTile * kLatent;  // float32 outputs of a unit
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef int v2i __attribute__((ext_vector_type(2)));
@@ -60,7 +63,7 @@ struct Attend {
   const float* sinks;  // [heads] or NULL
   uint8_t* out;        // bf16 [rows][heads][512]
   float* lse;          // [rows][heads] or NULL
-  float* part;         // splits > 1: [rows][splits][heads][512], then their m and l
+  float* part;         // splits > 1: [rows][splits][head_blocks] units of outputs, then their heads' m and l
   int64_t kv_stride, ks_stride, pt_stride;
   uint32_t pages_lim;  // page ids below it are in the pool
   int32_t rows, heads, width, num_tables;
@@ -121,7 +124,7 @@ __device__ __forceinline__ Closing close_sum(float m, float z, float sink) {
 // matrix units).
 template <int KEY>
 struct Shape {
-  static constexpr int kTile = 64, HT = 64;
+  static constexpr int HT = kHeadTile;
   static constexpr int kWaves = 8, kThreads = 64 * kWaves;
   static constexpr int kRowBytes = KEY == kFp8 ? kLatent : 2 * kLatent;  // of a position
   static constexpr int kChunks = kRowBytes / 16;    // of a position
@@ -138,9 +141,9 @@ struct Shape {
 template <int KEY>
 struct AttendShared {
   using S = Shape<KEY>;
-  uint8_t tile[S::kBuffers][S::kTile * S::kRowBytes];
-  float scale[S::kBuffers][S::kTile];   // e4m3 scales of the tiles' positions
-  uint32_t ref[S::kRing][S::kTile];     // slots of the positions (64 * page + i), or kMasked, kBad
+  uint8_t tile[S::kBuffers][kTile * S::kRowBytes];
+  float scale[S::kBuffers][kTile];   // e4m3 scales of the tiles' positions
+  uint32_t ref[S::kRing][kTile];     // slots of the positions (64 * page + i), or kMasked, kBad
   bf16x8 p[4][S::HT][2];                // probabilities, by 16 positions and head, in operand order
   f32x4 part[4][2][2][64];              // halves of scores on their way: by block, wave and lane
   uint32_t special[S::kRing];           // whether a tile has a position that is masked or bad
@@ -157,7 +160,7 @@ constexpr int64_t kMaxPages = (int64_t)1 << 25;  // 64 * page + i stays below kB
 template <int KEY>
 __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kernel(Attend a) {
   using S = Shape<KEY>;
-  constexpr int kTile = S::kTile, kRowBytes = S::kRowBytes, NB = S::NB, MB = S::MB;
+  constexpr int kRowBytes = S::kRowBytes, NB = S::NB, MB = S::MB;
   __shared__ __attribute__((aligned(16))) AttendShared<KEY> sh;
 
   const int lane = threadIdx.x & 63, n = lane & 31, half = lane >> 5;
@@ -175,14 +178,50 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   const int32_t b = a.rows - 1 - (int32_t)(rs / a.splits), split = (int32_t)(rs % a.splits);
   const int32_t h0 = hb * S::HT;
 
-  const int32_t L = uniform(min(max(a.sl[b], 0), a.width * kPage));
-  const int32_t count = a.k >= 0 ? min(a.k, L) : L;
+  // What depends on nothing but the arguments goes out first: waves 0 .. 3 load
+  // the list's entries of the first kRing tiles, before the length that may cut
+  // it short is there, and waves 4 .. 7 the queries (a wave's loads complete in
+  // order: queries ahead of a page id would hold it up).
+  //
+  // Queries: by DMA into the last 64 KiB of the tile buffers, rows of 1 KiB as
+  // they stand in memory; from there to registers as the B operand (loading the
+  // fragments from memory took 16 bytes of 64 lines an instruction: 7 us a unit
+  // instead of 2).  Heads past the last are zero.
+  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[0][0];
+  const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[0][0];
+  constexpr uint32_t kQueryAt = sizeof(sh.tile) - S::HT * 2 * kLatent;
+  constexpr int kResolvers = S::kWaves / 2, kMany = S::kRing * kTile / (64 * kResolvers);
+  const int32_t whole = a.width * kPage, bound = a.k >= 0 ? min(a.k, whole) : whole;
+  const int32_t* idx = a.k >= 0 ? a.idx + (int64_t)b * a.k : nullptr;
+  auto entry = [&](int32_t j, int32_t i) -> int32_t {  // entry i of the unit's tile j, or -1
+    const int32_t t = (split + j * a.splits) * kTile + i;
+    const int32_t* list = idx;
+    // Keeps the compiler from a second copy of the loop over the bf16 tiles: 53
+    // against 60 us (16 rows of 8192 positions and 128 heads).  The e4m3 tiles'
+    // loop is 2 % faster as two copies.
+    if constexpr (KEY == kBf16) asm("" : "+s"(list));
+    return t >= bound ? -1 : list ? list[t] : t;
+  };
+  int32_t early[kMany];  // lane's entry of tiles kMany * wave ..
+  if (wave < kResolvers) {
+#pragma unroll
+    for (int e = 0; e < kMany; ++e) early[e] = entry(kMany * wave + e, lane);
+  } else {
+#pragma unroll
+    for (int e = 0; e < S::HT / (S::kWaves - kResolvers); ++e) {
+      const int h = (S::kWaves - kResolvers) * e + wave - kResolvers;
+      const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent)
+                                            : reinterpret_cast<const uint8_t*>(kZeroLatent);
+      dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
+    }
+  }
+  const int32_t L = uniform(min(max(a.sl[b], 0), whole));
+  const int32_t count = min(bound, L);
   const int32_t tiles = (count + kTile - 1) / kTile;
   const int32_t mine = tiles > split ? (tiles - split + a.splits - 1) / a.splits : 0;
   const int32_t table = a.rt ? a.rt[b] : 0;
   const bool table_ok = !a.rt || (table >= 0 && table < a.num_tables);
   const int32_t* tab = a.pt + (int64_t)(a.rt ? (table_ok ? table : 0) : b) * a.pt_stride;
-  const int32_t* idx = a.k >= 0 ? a.idx + (int64_t)b * a.k : nullptr;
 
   f32x16 acc[MB][NB];  // values kDims*wave + 32*mb + 8*(i/4) + 4*half + i%4 of heads 32*nb + n
 #pragma unroll
@@ -194,41 +233,17 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   float m = 0.0f, most = -INFINITY, sum = 0.0f;
 
   if (mine > 0) {
-    // Slots of the positions of the unit's tiles [j0, j0 + count), `many` a
-    // thread at once.
-    auto resolve = [&](int32_t j0, int32_t ntiles, auto many) {
-      constexpr int kMany = decltype(many)::value;
-#pragma unroll 1
-      for (int32_t i0 = threadIdx.x; i0 < ntiles * kTile; i0 += kMany * S::kThreads) {
-        int32_t p[kMany], page[kMany];
-#pragma unroll
-        for (int e = 0; e < kMany; ++e) {
-          const int32_t i = i0 + e * S::kThreads, t = (split + (j0 + i / kTile) * a.splits) * kTile + i % kTile;
-          p[e] = -1;
-          if (i < ntiles * kTile && t < count) p[e] = idx ? idx[t] : t;
-        }
-#pragma unroll
-        for (int e = 0; e < kMany; ++e) {
-          page[e] = -1;
-          if (p[e] >= 0 && p[e] < L && table_ok) page[e] = tab[p[e] / kPage];
-        }
-#pragma unroll
-        for (int e = 0; e < kMany; ++e) {
-          const int32_t i = i0 + e * S::kThreads;
-          uint32_t r = kMasked;
-          if (p[e] >= 0 && p[e] < L)
-            r = page[e] >= 0 && (uint32_t)page[e] < a.pages_lim ? (uint32_t)page[e] * kPage + p[e] % kPage : kBad;
-          if (i < ntiles * kTile) {  // (a wave's 64 positions are one tile)
-            const int32_t j = (j0 + i / kTile) % S::kRing;
-            sh.ref[j][i % kTile] = r;
-            const uint64_t odd = __ballot(r >= kBad);
-            if (lane == 0) sh.special[j] = odd != 0;
-          }
-        }
-      }
+    // Slots of positions: page ids of the entries, then the ring's places of
+    // tile j's, a lane each.
+    auto page_of = [&](int32_t p) -> int32_t { return (uint32_t)p < (uint32_t)whole && table_ok ? tab[p / kPage] : -1; };
+    auto keep = [&](int32_t j, int32_t p, int32_t page) {
+      uint32_t r = kMasked;
+      if ((split + j * a.splits) * kTile + lane < count && (uint32_t)p < (uint32_t)L)
+        r = (uint32_t)page < a.pages_lim ? (uint32_t)page * kPage + p % kPage : kBad;
+      sh.ref[j % S::kRing][lane] = r;
+      const uint64_t odd = __ballot(r >= kBad);
+      if (lane == 0) sh.special[j % S::kRing] = odd != 0;
     };
-    const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[0][0];
-    const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[0][0];
     // Tile j into its buffer (zeros, past the last); every wave issues kDmaOps
     // operations.  Lane l holds the address of the wave's position l % kGather.
     struct Source {
@@ -262,28 +277,23 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       for (int d = 0; d < S::kDmaOps; ++d) gather_part(j, from, d);
     };
 
-    // Queries: by DMA into the last 64 KiB of the tile buffers, rows of 1 KiB
-    // as they stand in memory, while the first slots are resolved; from there to
-    // registers as the B operand (loading the fragments from memory took 16
-    // bytes of 64 lines an instruction: 7 us a unit instead of 2).  Lane (n,
-    // half) holds head n's values of step s: 16*(2*(s/2) + half) + 8*(s%2) .. +8
-    // (e4m3: two steps share a 16-byte chunk of codes) or 8*(2*s + half) .. +8
-    // (bf16).  Heads past the last are zero.
-    constexpr uint32_t kQueryAt = sizeof(sh.tile) - S::HT * 2 * kLatent;
-#pragma unroll
-    for (int e = 0; e < S::HT / S::kWaves; ++e) {
-      const int h = S::kWaves * e + wave;
-      const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent)
-                                            : reinterpret_cast<const uint8_t*>(kZeroLatent);
-      dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
-    }
     if (threadIdx.x < 4) sh.over[threadIdx.x] = 0;
-    resolve(0, min(mine, S::kRing), std::integral_constant<int, 2>{});
-    wait_vm<0>();
+    if (wave < kResolvers) {
+      int32_t page[kMany];
+#pragma unroll
+      for (int e = 0; e < kMany; ++e) page[e] = page_of(early[e]);
+#pragma unroll
+      for (int e = 0; e < kMany; ++e) keep(kMany * wave + e, early[e], page[e]);
+    }
     barrier();
     constexpr int kEarly = S::kBuffers - S::HT * 2 * kLatent / (kTile * kRowBytes);  // tiles beside the queries
 #pragma unroll
     for (int32_t j = 0; j < kEarly; ++j) gather(j);
+    wait_vm<kEarly * S::kDmaOps>();
+    barrier();
+    // Lane (n, half) holds head n's values of step s: 16*(2*(s/2) + half) +
+    // 8*(s%2) .. +8 (e4m3: two steps share a 16-byte chunk of codes) or
+    // 8*(2*s + half) .. +8 (bf16).
     bf16x8 q[16];
 #pragma unroll
     for (int s = 0; s < 16; ++s) {
@@ -596,13 +606,16 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
       if (kScore && uniform(special) != 0) probabilities(j + 1);
     };
-    // Half of the ring anew, past the tiles whose slots are still read (from
-    // next - 4 on); `next` is the tile gathered last.
+    // Half of the ring anew, a tile a wave, past the tiles whose slots are still
+    // read (from next - 4 on); `next` is the tile gathered last.
     auto refill = [&](int32_t next) {
       constexpr int kHalf = S::kRing / 2;
+      static_assert(kHalf == S::kWaves);
       const int32_t done = next - 4;
-      if (done >= kHalf && done % kHalf == 0 && done + kHalf < mine)
-        resolve(done + kHalf, min(kHalf, mine - (done + kHalf)), std::integral_constant<int, 1>{});
+      if (done >= kHalf && done % kHalf == 0 && done + kHalf < mine) {
+        const int32_t j = done + kHalf + wave, p = entry(j, lane);
+        keep(j, p, page_of(p));
+      }
     };
 
     if constexpr (KEY == kFp8) {
@@ -625,7 +638,6 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       phase(j, std::false_type{}, std::true_type{});
     } else {
       // Two buffers: a tile is scored and added up while the next is on its way.
-      if (kEarly < 1) gather(0);
       for (int32_t j = 0; j < mine; ++j) {
         wait_vm<0>();
         barrier();  // tile j is there; every wave is done with tile j - 1
@@ -645,32 +657,48 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     barrier();
   }
 
-  // Sums over the position blocks, and the outputs of all waves as rows of
-  // float32 in the tile buffers, so that they leave in whole lines.
+  // Sums over the position blocks.
   {
     const float s = sum + __shfl_xor(sum, 32);
     if (half == 0) sh.sum[2 * pb + kh][32 * hg + n] = s;
     if (half == 0 && pb == 0 && kh == 0) sh.by[32 * hg + n] = most == kLazy ? m : -INFINITY;
   }
+  wait_vm<0>();  // (nothing in it: the queries are still on their way)
   barrier();
+  auto total = [&](int h) { return (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]); };
+  if (a.splits > 1) {
+    // The outputs as they stand in the registers; a split with nothing in it
+    // leaves references and sums only.
+    const int64_t unit = ((int64_t)b * a.splits + split) * a.head_blocks + hb;
+    if (threadIdx.x < S::HT)
+      *reinterpret_cast<f32x2*>(a.part + (int64_t)a.rows * a.splits * a.head_blocks * kPartials + 2 * (S::HT * unit + threadIdx.x)) =
+          (f32x2){sh.by[threadIdx.x], total(threadIdx.x)};
+    if (mine == 0) return;
+    f32x4* to = reinterpret_cast<f32x4*>(a.part + unit * kPartials) + lane;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      if (h0 + 32 * nb + n >= a.heads) continue;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f32x16& o = acc[mb][nb];
+          to[64 * (4 * (NB * (MB * wave + mb) + nb) + k)] = (f32x4){o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]};
+        }
+    }
+    return;
+  }
+  // The outputs of all waves as rows of float32 in the tile buffers, so that
+  // they leave in whole lines.
   uint8_t* rows = &sh.tile[0][0];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const int h = 32 * nb + n;
-    const float z = (sh.sum[0][h] + sh.sum[1][h]) + (sh.sum[2][h] + sh.sum[3][h]), ref = sh.by[h];
-    float by = 1.0f, root = 1.0f;
-    if (a.splits > 1) {
-      const int64_t ph = ((int64_t)b * a.splits + split) * a.heads + h0 + h;
-      float* ml = a.part + (int64_t)a.rows * a.splits * a.heads * kLatent + 2 * ph;
-      if (h0 + h < a.heads && wave == 0 && half == 0) *reinterpret_cast<f32x2*>(ml) = (f32x2){ref, z};
-    } else {
-      const Closing c = close_sum(ref, z, a.sinks && h0 + h < a.heads ? a.sinks[h0 + h] * kLog2e : -INFINITY);
-      if (a.lse && h0 + h < a.heads && wave == 0 && half == 0) a.lse[(int64_t)b * a.heads + h0 + h] = c.lse;
-      by = c.by, root = c.half;
-    }
+    const Closing c = close_sum(sh.by[h], total(h), a.sinks && h0 + h < a.heads ? a.sinks[h0 + h] * kLog2e : -INFINITY);
+    if (a.lse && h0 + h < a.heads && wave == 0 && half == 0) a.lse[(int64_t)b * a.heads + h0 + h] = c.lse;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-      const f32x16 o = acc[mb][nb] * by * root * root;
+      const f32x16 o = acc[mb][nb] * c.by * c.half * c.half;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         *reinterpret_cast<f32x4*>(rows + h * 4 * kLatent + 16 * swizzle((S::kDims * wave + 32 * mb + 8 * k) / 4 + half, h)) =
@@ -678,93 +706,101 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     }
   }
   barrier();
-  if (a.splits > 1 && mine == 0) return;  // a split with nothing in it leaves m and l only
   for (int h = wave; h < S::HT && h0 + h < a.heads; h += S::kWaves) {
     const f32x4 lo = *reinterpret_cast<const f32x4*>(rows + h * 4 * kLatent + 16 * swizzle(2 * lane, h));
     const f32x4 hi = *reinterpret_cast<const f32x4*>(rows + h * 4 * kLatent + 16 * swizzle(2 * lane + 1, h));
-    if (a.splits > 1) {
-      f32x4* to = reinterpret_cast<f32x4*>(a.part + (((int64_t)b * a.splits + split) * a.heads + h0 + h) * kLatent + 8 * lane);
-      to[0] = lo;
-      to[1] = hi;
-    } else {
-      const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      *reinterpret_cast<u32x4*>(a.out + (((int64_t)b * a.heads + h0 + h) * kLatent + 8 * lane) * 2) = float_to_bf16x8(o);
-    }
+    const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    *reinterpret_cast<u32x4*>(a.out + (((int64_t)b * a.heads + h0 + h) * kLatent + 8 * lane) * 2) = float_to_bf16x8(o);
   }
 }
 
-// Joins the splits of a row: one wave a head, 8 values a lane.  The order of
-// the splits is fixed, so the result does not depend on their timing.
+// Joins the splits of a row: a wave has 32 values of 8 heads, 4 a lane, which
+// are 16 bytes of a unit's outputs (8 heads of them a line).  16 splits' loads
+// are under way at once, outputs and sums together: which splits have written
+// any is known only with the sums.  The order of the splits is fixed, so the
+// result does not depend on their timing.
+template <int kBatch>
 __global__ __launch_bounds__(256) void latent_combine_kernel(Attend a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t head = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (head >= (int64_t)a.rows * a.heads) return;
-  const int64_t b = head / a.heads;
-  const int32_t h = (int32_t)(head % a.heads);
-  const float* ml = a.part + (int64_t)a.rows * a.splits * a.heads * kLatent;
-  // lane s holds split s's reference and sum (at most 64 splits)
-  f32x2 mz = {-INFINITY, 0.0f};
-  if (lane < a.splits) mz = *reinterpret_cast<const f32x2*>(ml + 2 * ((b * a.splits + lane) * a.heads + h));
-  float top = mz.x;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t groups = (uint32_t)(a.heads + 7) / 8;
+  const int64_t b = (blockIdx.x >> 2) / groups;
+  const int32_t h = 8 * (int32_t)((blockIdx.x >> 2) % groups) + (lane & 7), n = h % kHeadTile;
+  const int block = 4 * (int)(blockIdx.x & 3) + wave, piece = lane >> 3;  // values 32*block + 4*piece .. +4
+  const int64_t unit0 = b * a.splits * a.head_blocks + h / kHeadTile;
+  // the lane's 16 bytes of a unit (accumulator (block, n / 32), chunk piece / 2)
+  const f32x4* from = reinterpret_cast<const f32x4*>(a.part + unit0 * kPartials) +
+                      64 * (4 * (kHeadTile / 32 * block + n / 32) + piece / 2) + 32 * (piece & 1) + n % 32;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.part + (int64_t)a.rows * a.splits * a.head_blocks * kPartials) +
+                    kHeadTile * unit0 + n;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, total = 0.0f;
+#pragma unroll 1
+  for (int32_t s0 = 0; s0 < a.splits; s0 += kBatch) {
+    f32x2 mz[kBatch];
+    f32x4 v[kBatch];
 #pragma unroll
-  for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  // nothing live: nothing written, maybe
-  const bool live = !(mz.x == -INFINITY && mz.y == 0.0f);
-  const float f = live ? __builtin_amdgcn_exp2f(mz.x - ref) : 0.0f;
-  const uint64_t written = __ballot(live);
-  float total = mz.y * f;
-#pragma unroll
-  for (int k = 32; k > 0; k >>= 1) total += __shfl_xor(total, k);
-  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const float* rows = a.part + (b * a.splits * a.heads + h) * kLatent + 8 * lane;
-#pragma unroll 4
-  for (int32_t s = 0; s < a.splits; ++s) {
-    const float fs = __shfl(f, s);
-    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-    if (written >> s & 1) {
-      const f32x4* src = reinterpret_cast<const f32x4*>(rows + (int64_t)s * a.heads * kLatent);
-      lo = src[0];
-      hi = src[1];
+    for (int i = 0; i < kBatch; ++i) {
+      mz[i] = (f32x2){-INFINITY, 0.0f};
+      if (s0 + i < a.splits) {
+        mz[i] = ml[(int64_t)(s0 + i) * a.head_blocks * kHeadTile];
+        v[i] = from[(int64_t)(s0 + i) * a.head_blocks * (kPartials / 4)];
+      }
     }
+    float ref = top;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[e] = fmaf(lo[e], fs, o[e]);
-      o[4 + e] = fmaf(hi[e], fs, o[4 + e]);
+    for (int i = 0; i < kBatch; ++i) ref = fmaxf(ref, mz[i].x);
+    const float base = ref == -INFINITY ? 0.0f : ref, by = __builtin_amdgcn_exp2f(top - base);
+    top = ref;
+    total *= by;
+    o *= by;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // (nothing live in a split: nothing written, maybe)
+      if (s0 + i < a.splits && !(mz[i].x == -INFINITY && mz[i].y == 0.0f)) {
+        const float f = __builtin_amdgcn_exp2f(mz[i].x - base);
+        total = fmaf(mz[i].y, f, total);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(v[i][e], f, o[e]);
+      }
     }
   }
+  if (h >= a.heads) return;
+  const int64_t head = b * a.heads + h;
   const Closing c = close_sum(top, total, a.sinks ? a.sinks[h] * kLog2e : -INFINITY);
+  bf16x4 w;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = o[e] * c.by * c.half * c.half;
-  *reinterpret_cast<u32x4*>(a.out + (head * kLatent + 8 * lane) * 2) = float_to_bf16x8(o);
-  if (a.lse && lane == 0) a.lse[head] = c.lse;
+  for (int e = 0; e < 4; ++e) w[e] = (__bf16)(o[e] * c.by * c.half * c.half);
+  *reinterpret_cast<bf16x4*>(a.out + (head * kLatent + 32 * block + 4 * piece) * 2) = w;
+  if (a.lse && block == 0 && piece == 0) a.lse[head] = c.lse;
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 
 constexpr int kMaxHeads = 128;
-constexpr int kMaxSplits = 64;  // (a lane each where they are joined)
-constexpr int kHeadTile = 64;
-constexpr int kTile = 64;  // positions that a split has at least two of
 constexpr int32_t kMaxWidth = 1 << 24;
 
-// Splits of a row's positions: enough units for a workgroup a CU, at least
-// two tiles each.  From the scalar arguments alone (the lengths are on the
-// device).
+// Splits of a row's positions, from the scalar arguments alone (the lengths are
+// on the device): a unit takes about 2.2 us a tile, and joining s splits about
+// 2.2 * s / 8 more, so up to sqrt(8 * tiles), all of the same number of tiles,
+// while every unit has a CU of its own.  One row of 64 heads over 8, 16, 32 and
+// 4096 tiles takes 13.4, 14.9, 16.5 and 88 us; with a tile a split, or at most
+// 256 splits, 13.4, 15.0, 17.8 and 86; the first two unsplit 23 and 38.
 int splits_of(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
   const int64_t most = k >= 0 ? (k < (int64_t)table_width * kPage ? k : (int64_t)table_width * kPage)
                                 : (int64_t)table_width * kPage;
   const int64_t tiles = (most + kTile - 1) / kTile;
   const int64_t units = (int64_t)rows * ((num_heads + kHeadTile - 1) / kHeadTile);
   int64_t s = device_cu_count() / (units > 0 ? units : 1);
-  if (s > tiles / 2) s = tiles / 2;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : (int)s;
+  while (s > 1 && s * s > 8 * tiles) --s;
+  if (s <= 1) return 1;
+  const int64_t each = (tiles + s - 1) / s;
+  return (int)((tiles + each - 1) / each);
 }
 
 int64_t workspace_of(int32_t rows, int32_t num_heads, int splits) {
-  return splits > 1 ? (int64_t)rows * num_heads * splits * (kLatent + 2) * 4 : 0;
+  const int64_t blocks = (num_heads + kHeadTile - 1) / kHeadTile;
+  return splits > 1 ? rows * splits * blocks * (kPartials + 2 * kHeadTile) * 4 : 0;
 }
 
 bool dims_ok(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
@@ -824,8 +860,18 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   if (groups > (int64_t)1 << 28) return IDX_ERR_SHAPE;
   (void)hipGetLastError();  // start from a clean error state
   latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(Shape<KEY>::kThreads), 0, stream>>>(a);
-  if (a.splits > 1)
-    latent_combine_kernel<<<dim3((uint32_t)(((int64_t)rows * num_heads + 3) / 4)), dim3(256), 0, stream>>>(a);
+  if (a.splits > 1) {
+    const dim3 grid((uint32_t)(4 * rows * ((num_heads + 7) / 8)));
+    // A batch no larger than the splits: 4 of them take 8.0 us where the kernel
+    // for 16, with its registers, takes 12 (64 rows of 64 heads), and 16 take 4.0
+    // us at once and 7.4 with four under way at a time (one row).
+    if (a.splits <= 4)
+      latent_combine_kernel<4><<<grid, dim3(256), 0, stream>>>(a);
+    else if (a.splits <= 8)
+      latent_combine_kernel<8><<<grid, dim3(256), 0, stream>>>(a);
+    else
+      latent_combine_kernel<16><<<grid, dim3(256), 0, stream>>>(a);
+  }
   return launch_status();
 }
 
