@@ -5,6 +5,8 @@
 // (16 bytes of bf16) each: sums and maxima over a vector are butterflies inside
 // its lanes, a wave covers 64*8/D vectors, and a vector is read once and
 // written once.  All of them move memory and compute next to nothing.
+#include <type_traits>
+
 #include "idx_device.h"
 
 namespace {
@@ -22,63 +24,85 @@ struct Vectors {
   int32_t heads;
   int32_t rope;          // rotated values
   int32_t first;         // first rotated value
+  uint32_t per_pair;     // 2^20 / (rope / 2), rounded up: (i * per_pair) >> 20 is i / (rope / 2) for i < 2^10
   uint32_t flags;
   float eps;
 };
 
-// cos and sin of position * frequency.  The product and its reduction to a
-// fraction of a turn are float64: at position 2^20 a float32 angle would
-// already be off by 0.03 rad.  The fraction, at most half a turn, is rounded to
-// float32 (2^-26 of a turn, 1e-7 rad).
+// cos and sin of position * frequency.  The product and its reduction to
+// quarters of a turn are float64: at position 2^20 a float32 angle would already
+// be off by 0.03 rad.  What is left, x in [-1/2, 1/2] quarters, is rounded to
+// float32 (2^-26 of a quarter) and goes into polynomials fitted here (least
+// largest error over the interval: sin(pi/2 x) / x to 2^-28 of itself,
+// cos(pi/2 x) to 2^-34), about half of the instructions of a library's pair.
 __device__ __forceinline__ f32x2 turn(int64_t position, float freq) {
-  const double turns = (double)position * (double)freq * 0.15915494309189533577;
-  const float f = (float)(turns - rint(turns));
-  float s, c;
-  sincospif(2.0f * f, &s, &c);
-  return (f32x2){c, s};
+  const double angle = (double)position * (double)freq;
+  const double whole = rint(angle * 0.63661977236758134308);
+  const float x = (float)fma(angle, 0.63661977236758134308, -whole), xx = x * x;
+  // the quarter: 1.5 * 2^52 has the integers as its last bits
+  const uint32_t quarter = (uint32_t)__builtin_bit_cast(uint64_t, whole + 0x1.8p52);
+  const float s = x * fmaf(xx, fmaf(xx, fmaf(xx, -4.60166e-3f, 7.968003e-2f), -0.64596346f), 1.57079632f);
+  const float c = fmaf(xx, fmaf(xx, fmaf(xx, fmaf(xx, 9.04021671e-4f, -2.08602885e-2f), 0.253669244f), -1.23370054f), 1.0f);
+  const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
+  return (f32x2){__uint_as_float(__float_as_uint(b) ^ (quarter + 1) << 30 & 0x80000000u),
+                 __uint_as_float(__float_as_uint(a) ^ quarter << 30 & 0x80000000u)};
 }
 
-// cos/sin of all pairs of `tokens` tokens from t0 on, into LDS [tokens][rope/2].
-__device__ __forceinline__ void fill_turns(const Vectors& p, int64_t t0, int tokens, f32x2* table) {
-  const int pairs = p.rope >> 1;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-    const int64_t t = t0 + i / pairs;
-    if (t < p.n) table[i] = turn(p.pos[t], p.freq[i % pairs]);
+// The lane's value of another lane of its row of 16.
+template <int CTRL, class T>
+__device__ __forceinline__ T row_lane(T v) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// f over the LPV lanes of a vector, in all of them: neighbours, pairs of a
+// quad, mirrored halves of a row and rows as operands of the arithmetic itself
+// (shuffles go through LDS), then rows and halves of the wave.
+template <int LPV, class T, class F>
+__device__ __forceinline__ T vector_fold(T v, F f) {
+  v = f(v, row_lane<0xb1>(v));   // quad_perm 1 0 3 2
+  v = f(v, row_lane<0x4e>(v));   // quad_perm 2 3 0 1
+  v = f(v, row_lane<0x141>(v));  // row_half_mirror
+  if constexpr (LPV > 8) v = f(v, row_lane<0x140>(v));  // row_mirror
+  if constexpr (LPV > 16) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = f(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
   }
-}
-
-template <int LPV>
-__device__ __forceinline__ float vector_sum(float v) {
-#pragma unroll
-  for (int m = LPV / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  if constexpr (LPV > 32) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = f(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
+  }
   return v;
 }
 
-template <int LPV>
-__device__ __forceinline__ float vector_max(float v) {
-#pragma unroll
-  for (int m = LPV / 2; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
-  return v;
+// 1 / sqrt(v) to 2^-23 of itself; the instruction takes no denormals.
+__device__ __forceinline__ float inverse_root(float v) {
+  const bool tiny = v < 0x1p-100f;
+  return __builtin_amdgcn_rsqf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p32f : 1.0f);
 }
+
+// How the rotated values pair up: a kernel each (one kernel that asks takes 16
+// moves a token more to bring the three ways' values together).
+enum { kPlain, kNeighbours, kHalves };
 
 // Norm and rotation of the lane's 8 values; `table` holds its token's turns,
 // `w` its 8 weights.  Called by whole waves.
-template <int LPV>
+template <int LPV, int ROPE>
 __device__ __forceinline__ void norm_rotate(const Vectors& p, int sub, const float (&w)[8], const f32x2* table,
                                             float (&v)[8]) {
   if (!(p.flags & IDX_NORM_OFF)) {
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
-    s = vector_sum<LPV>(s);
-    const float r = 1.0f / sqrtf(s * (1.0f / (8 * LPV)) + p.eps);
+    s = vector_fold<LPV>(s, [](float a, float b) { return a + b; });
+    const float r = inverse_root(s * (1.0f / (8 * LPV)) + p.eps);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = v[k] * r * w[k];
   }
-  if (p.rope == 0) return;
   const int at = 8 * sub - p.first;  // the lane's first value within the rotated part
   const bool in = at >= 0 && at < p.rope;
-  if (p.flags & IDX_ROPE_HALVES) {
+  if constexpr (ROPE == kHalves) {
     const int half = p.rope >> 1;
     const bool low = at < half;
     // the other value of each pair is half/8 lanes away
@@ -91,7 +115,7 @@ __device__ __forceinline__ void norm_rotate(const Vectors& p, int sub, const flo
         v[k] = low ? v[k] * cs.x - o * cs.y : o * cs.y + v[k] * cs.x;
       }
     }
-  } else if (in) {
+  } else if (ROPE == kNeighbours && in) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const f32x2 cs = table[(at >> 1) + k];
@@ -109,7 +133,7 @@ __device__ __forceinline__ void load_weight(const Vectors& p, int sub, float (&w
 }
 
 // Unit = one token x `STEPS` groups of kWaves * 64/LPV heads.
-template <int LPV, int STEPS>
+template <int LPV, int ROPE, int STEPS>
 __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t* out, int32_t groups) {
   extern __shared__ f32x2 table[];
   constexpr int kDim = 8 * LPV, kVecs = 64 / LPV;
@@ -127,37 +151,45 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
       raw[u] = (u32x4){0u, 0u, 0u, 0u};
       if (h < p.heads) raw[u] = *reinterpret_cast<const u32x4*>(p.x + t * p.x_stride + ((int64_t)h * kDim + 8 * sub) * 2);
     }
-    __syncthreads();  // the last unit's turns have been used
-    fill_turns(p, t, 1, table);
-    __syncthreads();
+    if constexpr (ROPE != kPlain) {
+      __syncthreads();  // the last unit's turns have been used
+      for (int i = threadIdx.x; i < p.rope >> 1; i += kThreads) table[i] = turn(p.pos[t], p.freq[i]);
+      __syncthreads();
+    }
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       const int h = h0 + u * kWaves * kVecs;
       float v[8];
       bf16x8_to_float(raw[u], v);
-      norm_rotate<LPV>(p, sub, w, table, v);
+      norm_rotate<LPV, ROPE>(p, sub, w, table, v);
       if (h < p.heads)
         *reinterpret_cast<u32x4*>(out + ((t * p.heads + h) * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
     }
   }
 }
 
-// e4m3fn codes of v / scale, clamped to +-448: the quotients as the float32
-// division rounds them, from one reciprocal a vector.  q0 = v*y with y =
-// 1/scale correctly rounded, and the residual step q = q0 + (v - scale*q0)*y
-// gives the correctly rounded quotient away from underflow (Markstein's
-// correction); a scale outside [2^-60, 2^100] takes the division.  The sign
-// comes from v: a zero quotient may lose it.
-__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float scale) {
+// Scale amax / 448 of a vector and e4m3fn codes of its values / scale, clamped
+// to +-448: both quotients as the float32 division rounds them.  A division
+// takes some ten instructions and the kernel has time for 160 a token, so each
+// is a product and a correction by its residual (Markstein's), q0 = v*y with y
+// the reciprocal and q = q0 + (v - scale*q0)*y, which is the correctly rounded
+// quotient away from underflow and overflow; where the scale may leave [2^-60,
+// 2^100] the division is taken.  The sign comes from v: the correction takes it
+// from a zero.
+__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float amax, float& scale) {
+  const float m = amax > 0.0f ? amax : 448.0f;
   float q[8];
-  if (__ballot(!(scale >= 0x1p-60f && scale <= 0x1p100f)) == 0) {
-    const float y = 1.0f / scale;
+  if (__ballot(!(m >= 0x1p-51f && m <= 0x1p108f)) == 0) {
+    const float c = 1.0f / 448.0f, s0 = m * c;
+    scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
+    const float y0 = __builtin_amdgcn_rcpf(scale), y = fmaf(fmaf(-scale, y0, 1.0f), y0, y0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float q0 = v[k] * y;
       q[k] = fmaf(fmaf(-scale, q0, v[k]), y, q0);
     }
   } else {
+    scale = m / 448.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) q[k] = v[k] / scale;
   }
@@ -165,15 +197,11 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float scale) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float y[4];
-    uint32_t sign = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      y[k] = fminf(fmaxf(q[4 * h + k], -448.0f), 448.0f);
-      sign |= (__float_as_uint(v[4 * h + k]) >> 31) << (8 * k + 7);
-    }
-    uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], (int)c, true);
-    codes[h] = (c & 0x7f7f7f7fu) | sign;
+    for (int k = 0; k < 4; ++k)  // (a NaN becomes -448 by the median and takes its sign back)
+      y[k] = copysignf(__builtin_amdgcn_fmed3f(q[4 * h + k], -448.0f, 448.0f), v[4 * h + k]);
+    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
   }
   return codes;
 }
@@ -185,53 +213,79 @@ struct Pool {
   int64_t kv_stride, ks_stride;
 };
 
-// Unit = `STEPS` groups of kWaves * 64/LPV tokens.
-template <int KEY, int LPV, int STEPS>
+// Unit = `STEPS` groups of 64/LPV tokens, a wave's; the next unit's vectors are
+// on their way while one is worked on.  A wave has its tokens' turns to itself,
+// so no wave waits for another.
+template <int KEY, int LPV, int ROPE, int STEPS>
 __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
   extern __shared__ f32x2 table[];
-  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kWaves * kVecs;
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kVecs;
   const int lane = threadIdx.x & 63, sub = lane % LPV;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float w[8];
-  load_weight<LPV>(p, sub, w);
-  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.n; t0 += (int64_t)gridDim.x * kTokens) {
+  const int pairs = p.rope >> 1;
+  f32x2* turns = table + wave * kTokens * pairs;
+  struct Unit {
     u32x4 raw[STEPS];
     int64_t slot[STEPS];
+  };
+  auto load = [&](int64_t t0) {
+    Unit unit;
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-      const int64_t t = t0 + (u * kWaves + wave) * kVecs + lane / LPV;
-      raw[u] = (u32x4){0u, 0u, 0u, 0u};
-      slot[u] = -1;
+      const int64_t t = t0 + u * kVecs + lane / LPV;
+      unit.raw[u] = (u32x4){0u, 0u, 0u, 0u};
+      unit.slot[u] = -1;
       if (t < p.n) {
-        slot[u] = slots[t];
-        raw[u] = *reinterpret_cast<const u32x4*>(p.x + t * p.x_stride + 16 * sub);
+        unit.slot[u] = slots[t];
+        unit.raw[u] = *reinterpret_cast<const u32x4*>(p.x + t * p.x_stride + 16 * sub);
       }
     }
-    __syncthreads();
-    fill_turns(p, t0, kTokens, table);
-    __syncthreads();
+    return unit;
+  };
+  const int64_t step = (int64_t)gridDim.x * kWaves * kTokens;
+  int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * kTokens;
+  Unit next = load(t0);
+  float w[8];
+  load_weight<LPV>(p, sub, w);
+  for (; t0 < p.n; t0 += step) {
+    const Unit unit = next;
+    next = load(t0 + step);
+    if constexpr (ROPE != kPlain) {
+#pragma unroll 1
+      for (int i = lane; i < kTokens * pairs; i += 64) {
+        const int token = (int)((uint32_t)i * p.per_pair >> 20);
+        const int64_t t = t0 + token < p.n ? t0 + token : t0;
+        turns[i] = turn(p.pos[t], p.freq[i - token * pairs]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       float v[8];
-      bf16x8_to_float(raw[u], v);
-      norm_rotate<LPV>(p, sub, w, table + ((u * kWaves + wave) * kVecs + lane / LPV) * (p.rope >> 1), v);
-      const bool ok = slot[u] >= 0 && slot[u] < pool.slots;
-      const int64_t page = ok ? slot[u] / kPage : 0, i = ok ? slot[u] % kPage : 0;
+      bf16x8_to_float(unit.raw[u], v);
+      norm_rotate<LPV, ROPE>(p, sub, w, turns + (u * kVecs + lane / LPV) * pairs, v);
+      const int64_t slot = unit.slot[u];
+      const bool ok = slot >= 0 && slot < pool.slots;
+      const int64_t page = ok ? slot / kPage : 0, i = ok ? slot % kPage : 0;
       if constexpr (KEY == kBf16) {
         if (ok) *reinterpret_cast<u32x4*>(pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
       } else {
         float m = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
-        m = vector_max<LPV>(m);
-        const float scale = m > 0.0f ? m / 448.0f : 1.0f;
-        const u32x2 codes = quantise(v, scale);
+        // (neither NaN nor negative: ordered as its bits are)
+        const uint32_t top = vector_fold<LPV>(__float_as_uint(m), [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+        float scale;
+        const u32x2 codes = quantise(v, __uint_as_float(top), scale);
         if (ok) {
           *reinterpret_cast<u32x2*>(pool.kv + page * pool.kv_stride + i * kDim + 8 * sub) = codes;
           if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;
         }
       }
     }
+    __builtin_amdgcn_wave_barrier();  // the turns have been used
   }
 }
 
@@ -322,33 +376,48 @@ Vectors vectors_of(const void* x, const float* norm_weight, const int64_t* posit
   p.heads = num_heads;
   p.rope = rope_dim;
   p.first = (flags & IDX_ROPE_LEADING) ? 0 : head_dim - rope_dim;
+  p.per_pair = rope_dim > 0 ? ((1u << 20) + rope_dim / 2 - 1) / (uint32_t)(rope_dim / 2) : 0;
   p.flags = flags;
   p.eps = eps;
   return p;
+}
+
+// The kernel for a rotation: f(std::integral_constant<int, ROPE>).
+template <class F>
+void for_rotation(const Vectors& p, F f) {
+  if (p.rope == 0) f(std::integral_constant<int, kPlain>{});
+  else if (p.flags & IDX_ROPE_HALVES) f(std::integral_constant<int, kHalves>{});
+  else f(std::integral_constant<int, kNeighbours>{});
 }
 
 template <int LPV>
 void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
   constexpr int kOne = kWaves * (64 / LPV);  // heads of one step
   const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2);
-  const int32_t groups = (p.heads + 4 * kOne - 1) / (4 * kOne);
-  if (p.n * groups >= 4 * device_cu_count()) {
-    norm_rope_kernel<LPV, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, static_cast<uint8_t*>(out), groups);
-  } else {
-    const int32_t single = (p.heads + kOne - 1) / kOne;
-    norm_rope_kernel<LPV, 1><<<grid_of(p.n * single), dim3(kThreads), lds, stream>>>(p, static_cast<uint8_t*>(out), single);
-  }
+  const int32_t groups = (p.heads + 4 * kOne - 1) / (4 * kOne), single = (p.heads + kOne - 1) / kOne;
+  uint8_t* to = static_cast<uint8_t*>(out);
+  for_rotation(p, [&](auto rope) {
+    constexpr int kRope = decltype(rope)::value;
+    if (p.n * groups >= 4 * device_cu_count())
+      norm_rope_kernel<LPV, kRope, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, to, groups);
+    else
+      norm_rope_kernel<LPV, kRope, 1><<<grid_of(p.n * single), dim3(kThreads), lds, stream>>>(p, to, single);
+  });
 }
 
 template <int KEY, int LPV>
 void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipStream_t stream) {
   constexpr int kOne = kWaves * (64 / LPV);
   const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kOne;
-  if (p.n >= (int64_t)4 * kOne * 2 * device_cu_count())
-    norm_rope_store_kernel<KEY, LPV, 4><<<grid_of((p.n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 4 * lds, stream>>>(
-        p, pool, slots);
-  else
-    norm_rope_store_kernel<KEY, LPV, 1><<<grid_of((p.n + kOne - 1) / kOne), dim3(kThreads), lds, stream>>>(p, pool, slots);
+  const int64_t fill = 8 * device_cu_count(), twos = (p.n + 2 * kOne - 1) / (2 * kOne);
+  for_rotation(p, [&](auto rope) {
+    constexpr int kRope = decltype(rope)::value;
+    if (twos >= fill)
+      norm_rope_store_kernel<KEY, LPV, kRope, 2><<<dim3((uint32_t)fill), dim3(kThreads), 2 * lds, stream>>>(p, pool, slots);
+    else
+      norm_rope_store_kernel<KEY, LPV, kRope, 1><<<grid_of((p.n + kOne - 1) / kOne), dim3(kThreads), lds, stream>>>(
+          p, pool, slots);
+  });
 }
 
 template <int KEY>
