@@ -213,25 +213,27 @@ struct Pool {
   int64_t kv_stride, ks_stride;
 };
 
-// Unit = `STEPS` groups of 64/LPV tokens, a wave's; the next unit's vectors are
+// Unit = kSteps groups of 64/LPV tokens, a wave's; the next unit's vectors are
 // on their way while one is worked on.  A wave has its tokens' turns to itself,
 // so no wave waits for another.
-template <int KEY, int LPV, int ROPE, int STEPS>
+constexpr int kSteps = 2;
+
+template <int KEY, int LPV, int ROPE>
 __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
   extern __shared__ f32x2 table[];
-  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kVecs;
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = kSteps * kVecs;
   const int lane = threadIdx.x & 63, sub = lane % LPV;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int pairs = p.rope >> 1;
   f32x2* turns = table + wave * kTokens * pairs;
   struct Unit {
-    u32x4 raw[STEPS];
-    int64_t slot[STEPS];
+    u32x4 raw[kSteps];
+    int64_t slot[kSteps];
   };
   auto load = [&](int64_t t0) {
     Unit unit;
 #pragma unroll
-    for (int u = 0; u < STEPS; ++u) {
+    for (int u = 0; u < kSteps; ++u) {
       const int64_t t = t0 + u * kVecs + lane / LPV;
       unit.raw[u] = (u32x4){0u, 0u, 0u, 0u};
       unit.slot[u] = -1;
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
 #pragma unroll
-    for (int u = 0; u < STEPS; ++u) {
+    for (int u = 0; u < kSteps; ++u) {
       float v[8];
       bf16x8_to_float(unit.raw[u], v);
       norm_rotate<LPV, ROPE>(p, sub, w, turns + (u * kVecs + lane / LPV) * pairs, v);
@@ -398,7 +400,7 @@ void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
   uint8_t* to = static_cast<uint8_t*>(out);
   for_rotation(p, [&](auto rope) {
     constexpr int kRope = decltype(rope)::value;
-    if (p.n * groups >= 4 * device_cu_count())
+    if (p.n * groups >= 16 * device_cu_count())
       norm_rope_kernel<LPV, kRope, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, to, groups);
     else
       norm_rope_kernel<LPV, kRope, 1><<<grid_of(p.n * single), dim3(kThreads), lds, stream>>>(p, to, single);
@@ -407,16 +409,12 @@ void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
 
 template <int KEY, int LPV>
 void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipStream_t stream) {
-  constexpr int kOne = kWaves * (64 / LPV);
-  const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kOne;
-  const int64_t fill = 8 * device_cu_count(), twos = (p.n + 2 * kOne - 1) / (2 * kOne);
+  constexpr int kTokens = kSteps * kWaves * (64 / LPV);
+  const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kTokens;
+  const int64_t units = (p.n + kTokens - 1) / kTokens, most = 16 * device_cu_count();
+  const dim3 grid((uint32_t)(units < most ? units : most));
   for_rotation(p, [&](auto rope) {
-    constexpr int kRope = decltype(rope)::value;
-    if (twos >= fill)
-      norm_rope_store_kernel<KEY, LPV, kRope, 2><<<dim3((uint32_t)fill), dim3(kThreads), 2 * lds, stream>>>(p, pool, slots);
-    else
-      norm_rope_store_kernel<KEY, LPV, kRope, 1><<<grid_of((p.n + kOne - 1) / kOne), dim3(kThreads), lds, stream>>>(
-          p, pool, slots);
+    norm_rope_store_kernel<KEY, LPV, decltype(rope)::value><<<grid, dim3(kThreads), lds, stream>>>(p, pool, slots);
   });
 }
 
@@ -448,7 +446,7 @@ void launch_load(const Pool& pool, const int64_t* slots, int64_t n, void* out, i
                  hipStream_t stream) {
   constexpr int kOne = kWaves * (64 / LPV);
   uint8_t* o = static_cast<uint8_t*>(out);
-  if (n >= (int64_t)4 * kOne * 2 * device_cu_count())
+  if (n >= (int64_t)4 * kOne * 8 * device_cu_count())
     load_slots_kernel<KEY, LPV, 4><<<grid_of((n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 0, stream>>>(
         pool, slots, n, o, 2 * out_row_stride);
   else
