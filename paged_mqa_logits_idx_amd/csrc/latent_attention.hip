@@ -324,7 +324,9 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         for (int e = 0; e < 4; ++e) x[4 * k + e] = mine_[4 * k + e] + v[e];
       }
     };
-    auto score = [&](int32_t j) -> f32x16 {
+    // Scores of tile j, while tile j + 1 is gathered.
+    auto score = [&](int32_t j, const Source& from) -> f32x16 {
+      static_assert(KEY == kFp8 || S::kDmaOps == 8);
       const uint8_t* rows = sh.tile[j % S::kBuffers];
       f32x16 half0 = (f32x16)(0.0f);
 #pragma unroll
@@ -338,6 +340,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         }
         half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[s], half0, 0, 0, 0);
         half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[s + 1], half0, 0, 0, 0);
+        gather_part(j + 1, from, s / 2);
       }
       send(half0);
       return half0;
@@ -464,7 +467,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(t.lo, t.hi, 0, 1, 2, 3));
     };
     auto read_w = [&](int s, int nb) { return sh.p[s][32 * nb + n][half]; };
-    auto accumulate = [&](int32_t j) {
+    auto accumulate = [&](int32_t j, const Codes (&early)[MB]) {
       const uint8_t* rows = sh.tile[j % S::kBuffers];
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
@@ -473,7 +476,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         for (int nb = 0; nb < NB; ++nb) w[nb] = read_w(s, nb);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-          const bf16x8 v = widen(read_v(rows, s, mb));
+          const bf16x8 v = widen(s == 0 ? early[mb] : read_v(rows, s, mb));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
             acc[mb][nb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, w[nb], acc[mb][nb], 0, 0, 0);
@@ -638,19 +641,25 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       phase(j, std::false_type{}, std::true_type{});
     } else {
       // Two buffers: a tile is scored and added up while the next is on its way.
+      // Its gather is spread over the scores (2048 rows of 64 heads over 2048
+      // positions: 568 us, and 592 with it in one place), and the first latents of
+      // the outputs are read before the probabilities are there (592 and 606).
       for (int32_t j = 0; j < mine; ++j) {
         wait_vm<0>();
         barrier();  // tile j is there; every wave is done with tile j - 1
         if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;
-        gather(j + 1);
+        const Source from = source_of(j + 1);
         refill(j + 1);
-        const f32x16 half0 = score(j);
+        const f32x16 half0 = score(j, from);
         barrier();
         receive(half0);
         probabilities(j);
+        Codes early[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) early[i] = read_v(sh.tile[j % S::kBuffers], 0, i);
         barrier();
         settle(j);
-        accumulate(j);
+        accumulate(j, early);
       }
       wait_vm<0>();
     }
