@@ -697,8 +697,8 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     }
     return;
   }
-  // The outputs of all waves as rows of float32 in the tile buffers, so that
-  // they leave in whole lines.
+  // The outputs of all waves as rows in the tile buffers, so that they leave in
+  // whole lines.
   uint8_t* rows = &sh.tile[0][0];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -710,16 +710,17 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       const f32x16 o = acc[mb][nb] * c.by * c.half * c.half;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<f32x4*>(rows + h * 4 * kLatent + 16 * swizzle((S::kDims * wave + 32 * mb + 8 * k) / 4 + half, h)) =
-            (f32x4){o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]};
+        *reinterpret_cast<bf16x4*>(rows + h * 2 * kLatent + 16 * swizzle(S::kDims / 8 * wave + 4 * mb + k, h) + 8 * half) =
+            (bf16x4){(__bf16)o[4 * k], (__bf16)o[4 * k + 1], (__bf16)o[4 * k + 2], (__bf16)o[4 * k + 3]};
     }
   }
   barrier();
-  for (int h = wave; h < S::HT && h0 + h < a.heads; h += S::kWaves) {
-    const f32x4 lo = *reinterpret_cast<const f32x4*>(rows + h * 4 * kLatent + 16 * swizzle(2 * lane, h));
-    const f32x4 hi = *reinterpret_cast<const f32x4*>(rows + h * 4 * kLatent + 16 * swizzle(2 * lane + 1, h));
-    const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    *reinterpret_cast<u32x4*>(a.out + (((int64_t)b * a.heads + h0 + h) * kLatent + 8 * lane) * 2) = float_to_bf16x8(o);
+#pragma unroll
+  for (int e = 0; e < S::HT / S::kWaves; ++e) {
+    const int h = S::kWaves * e + wave;
+    if (h0 + h < a.heads)
+      *reinterpret_cast<u32x4*>(a.out + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent) + 16 * lane) =
+          *reinterpret_cast<const u32x4*>(rows + h * 2 * kLatent + 16 * swizzle(lane, h));
   }
 }
 
