@@ -146,7 +146,8 @@ int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, i
  *   q          bf16 [rows][num_heads][512], contiguous, 16-byte aligned.
  *   kv_pages, kscale, num_pages, kv_page_stride, kscale_page_stride
  *              the pool of 512-value pages: kv_page_stride >= 32768 bytes
- *              (bf16: 65536), the rest as in idx_paged_mqa_logits_fp8.
+ *              (bf16: 65536), num_pages at most 33,554,432, the rest as in
+ *              idx_paged_mqa_logits_fp8.
  *   page_table int32, 4-byte aligned: row b's table (table_width entries) at
  *              page_table + t*page_table_row_stride with t = b, or
  *              t = row_table[b] where row_table is not NULL.  A stride of 0
@@ -159,14 +160,15 @@ int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, i
  *   sinks      fp32 [num_heads], 4-byte aligned, or NULL.
  *   out        bf16 [rows][num_heads][512], 16-byte aligned.
  *   lse        fp32 [rows][num_heads], 4-byte aligned, or NULL.
- *   rows, num_heads   >= 0; 0 returns IDX_OK with no launch.
- *   num_heads  at most 128.    head_dim must be 512.
+ *   rows, num_heads   >= 0; 0 returns IDX_OK with no launch.  num_heads at most
+ *              128; rows times blocks of 64 heads at most 8,000,000.
+ *   head_dim   must be 512.
  *   table_width >= 0, at most 16,777,216 (page_table may be NULL if it is 0).
  *   k >= -1.   scale finite.
  *   workspace  idx_latent_attention_workspace(rows, num_heads, table_width, k)
- *              bytes on the call's device, 16-byte aligned; NULL where that is 0.  It holds nothing between calls,
- *              but calls that may run at the same time (captured ones
- *              included) need one each.
+ *              bytes on the call's device, 16-byte aligned; NULL where that is
+ *              0.  It holds nothing between calls, but calls that may run at the
+ *              same time (captured ones included) need one each.
  */
 int idx_latent_attention_fp8(const void* q, const void* kv_pages, const float* kscale,
                              const int32_t* page_table, const int32_t* row_table, int32_t num_tables,

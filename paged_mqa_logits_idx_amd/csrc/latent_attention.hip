@@ -789,6 +789,7 @@ __global__ __launch_bounds__(256) void latent_combine_kernel(Attend a) {
 
 constexpr int kMaxHeads = 128;
 constexpr int32_t kMaxWidth = 1 << 24;
+constexpr int64_t kMaxUnits = 8000000;  // a launch has less than 2^32 threads
 
 // Splits of a row's positions, from the scalar arguments alone (the lengths are
 // on the device): a unit takes about 2.2 us a tile, and joining s splits about
@@ -815,7 +816,7 @@ int64_t workspace_of(int32_t rows, int32_t num_heads, int splits) {
 
 bool dims_ok(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
   return rows >= 0 && num_heads >= 0 && num_heads <= kMaxHeads && table_width >= 0 && table_width <= kMaxWidth &&
-         k >= -1;
+         k >= -1 && (int64_t)rows * ((num_heads + kHeadTile - 1) / kHeadTile) <= kMaxUnits;
 }
 
 template <int KEY>
@@ -867,7 +868,6 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   a.head_blocks = (num_heads + kHeadTile - 1) / kHeadTile;
   a.scale2 = scale * kLog2e;
   const int64_t groups = ((int64_t)rows * a.splits + 7) / 8 * a.head_blocks;
-  if (groups > (int64_t)1 << 28) return IDX_ERR_SHAPE;
   (void)hipGetLastError();  // start from a clean error state
   latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(Shape<KEY>::kThreads), 0, stream>>>(a);
   if (a.splits > 1) {

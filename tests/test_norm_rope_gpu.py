@@ -272,3 +272,22 @@ def test_other_stream_and_graph(lib):
         both()
         torch.cuda.synchronize()
         assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_far_positions_still_turn(lib, halves):
+    """Up to |p| = 2^53 the rotation is one, whatever is left of the angle: pairs
+    keep their length.  Its cos and sin are float32 (3 2^-24 of the length), and
+    the outputs are rounded to bf16 (2^-9 of it at most in each of two values)."""
+    rng = np.random.default_rng(21)
+    n, dim = 64, 128
+    far = [2 ** 40, 2 ** 50 + 3, 2 ** 51 - 1, 2 ** 52 + 1, 2 ** 53, 2 ** 53 - 1]
+    positions = torch.tensor([rng.choice(far) * rng.choice([-1, 1]) for _ in range(n)], dtype=torch.int64)
+    freq = torch.cat([torch.tensor([1.0]), torch.from_numpy(rng.random(31).astype(np.float32))])
+    x = torch.from_numpy(rng.standard_normal((n, 1, dim))).to(torch.bfloat16)
+    out = torch.empty((n, 1, dim), dtype=torch.bfloat16, device="cuda")
+    lib.idx_norm_rope(x.cuda(), positions.cuda(), freq.cuda(), out, norm=False, halves=halves)
+    was, got = (t.double().cpu().numpy()[:, 0, dim - 64:] for t in (x, out))
+    pairs = (lambda v: np.hypot(v[:, :32], v[:, 32:])) if halves else (lambda v: np.hypot(v[:, 0::2], v[:, 1::2]))
+    assert (np.abs(pairs(got) - pairs(was)) <= pairs(was) * (2.0 ** -8 + 2.0 ** -21)).all()
+    assert torch.equal(out[..., : dim - 64].cpu(), x[..., : dim - 64])
