@@ -469,6 +469,10 @@ def _rows(name, x, dims) -> int:
     return x.stride(0) if shape[0] > 1 else dense
 
 
+# Where the library's text names the indexer's sizes.
+_STATUS_TEXT = {IDX_ERR_UNSUPPORTED: "unsupported num_heads, head_dim, rope_dim or flag"}
+
+
 def _launch(fn, dev, stream, check, *args) -> int:
     """Calls the library on the tensors' device, whatever the current one is."""
     if dev < 0:
@@ -480,7 +484,7 @@ def _launch(fn, dev, stream, check, *args) -> int:
         with torch.cuda.device(dev):
             status = fn(*args, handle)
     if check and status != IDX_OK:
-        raise IdxError(status, f"{fn.__name__}: {idx_status_string(status)}")
+        raise IdxError(status, f"{fn.__name__}: {_STATUS_TEXT.get(status) or idx_status_string(status)}")
     return status
 
 

@@ -2107,7 +2107,7 @@ const char* idx_status_string(int status) {
   switch (status) {
     case IDX_OK: return "ok";
     case IDX_ERR_NULL: return "null pointer (or kscale passed to the bf16 variant)";
-    case IDX_ERR_UNSUPPORTED: return "unsupported num_heads, head_dim, rope_dim or flag";
+    case IDX_ERR_UNSUPPORTED: return "unsupported num_heads/head_dim (need 64 and 128)";
     case IDX_ERR_SHAPE: return "invalid dimension or stride";
     case IDX_ERR_ALIGN: return "misaligned pointer or stride";
     case IDX_ERR_LAUNCH: return "kernel launch failed";
