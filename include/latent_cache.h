@@ -78,7 +78,9 @@ int idx_norm_rope(const void* x, const float* norm_weight, const int64_t* positi
  *   code_d = e4m3fn(clamp(y_d / scale, -448, 448)), round to nearest even
  *
  * and written to their slots: the quantiser of idx_store_keys_fp8 over
- * head_dim values (with IDX_NORM_OFF and rope_dim 0 the bytes are the same).
+ * head_dim values (with IDX_NORM_OFF and rope_dim 0 the bytes are the same).  A
+ * NaN has no part in amax; a quotient that is NaN becomes +-448 with the sign of
+ * y_d.
  * Arguments as idx_norm_rope and idx_store_keys_fp8 except:
  *   head_dim     128 (index keys) or 512 (latents).
  *   kv_page_stride  bytes, >= 64*head_dim, multiple of 16.

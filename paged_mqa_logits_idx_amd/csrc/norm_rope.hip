@@ -177,13 +177,21 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
 // Scale amax / 448 of a vector and e4m3fn codes of its values / scale, clamped
 // to +-448: both quotients as the float32 division rounds them.  A division
 // takes some ten instructions and the kernel is bound by them, so each is a
-// product and a correction by its residual (Markstein's), q0 = v*y with y
-// the reciprocal and q = q0 + (v - scale*q0)*y, which is the correctly rounded
-// quotient away from underflow and overflow; where the scale may leave [2^-60,
-// 2^100] the division is taken.  The sign comes from v: the correction takes it
-// from a zero.
-__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float amax, float& scale) {
-  const float m = amax > 0.0f ? amax : 448.0f;
+// product and a correction by its residual (Markstein's), q0 = v*y with y the
+// reciprocal and q = q0 - (scale*q0 - v)*y, which is the correctly rounded
+// quotient away from underflow and overflow, and keeps the sign of a zero; the
+// clamp does nothing then.  Where the scale may leave [2^-60, 2^100], or a value is
+// not a number, the division is taken; a NaN has no part in amax and becomes
+// +-448.
+template <int LPV>
+__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float& scale) {
+  float m = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = __builtin_elementwise_maximum(m, fabsf(v[k]));  // NaN if one is
+  // (never negative: ordered as its bits are, a NaN above all)
+  const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  uint32_t top = vector_fold<LPV>(__float_as_uint(m), larger);
+  m = top != 0 ? __uint_as_float(top) : 448.0f;
   float q[8];
   if (__ballot(!(m >= 0x1p-51f && m <= 0x1p108f)) == 0) {
     const float c = 1.0f / 448.0f, s0 = m * c;
@@ -192,22 +200,23 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float amax, float
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float q0 = v[k] * y;
-      q[k] = fmaf(fmaf(-scale, q0, v[k]), y, q0);
+      q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
     }
   } else {
+    m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+    top = vector_fold<LPV>(__float_as_uint(m), larger);
+    m = top != 0 ? __uint_as_float(top) : 448.0f;
     scale = m / 448.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = v[k] / scale;
+    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] / scale, -448.0f, 448.0f), v[k]);
   }
   u32x2 codes;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float y[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)  // (a NaN becomes -448 by the median and takes its sign back)
-      y[k] = copysignf(__builtin_amdgcn_fmed3f(q[4 * h + k], -448.0f, 448.0f), v[4 * h + k]);
-    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
+    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], c, true);
   }
   return codes;
 }
@@ -219,13 +228,13 @@ struct Pool {
   int64_t kv_stride, ks_stride;
 };
 
-constexpr int kSteps = 2;  // (1 and 4: 28 and 31 us where 2 takes 26.5; small calls take the same)
+constexpr int kSteps = 2;  // (1 and 4: 28 and 31 us where 2 took 26.5; small calls take the same)
 
 // Unit = kSteps groups of 64/LPV tokens, a wave's; the next unit's vectors are
 // on their way while one is worked on.  A wave has its tokens' turns to itself,
-// so no wave waits for another.  65536 latents to e4m3 take 26.5 us: 101 MB at
-// 3.8 TB/s, but bound by the vector instructions (184 a token of 4 clocks a wave,
-// 22 us of every SIMD); 32768 to bf16 take 14.4, 67 MB at 4.6 TB/s.
+// so no wave waits for another.  65536 latents to e4m3 take 26 us: 101 MB at
+// 3.9 TB/s, but bound by the vector instructions (174 a token, issuing in nearly
+// all of the SIMDs' cycles); 32768 to bf16 take 14.4, 67 MB at 4.6 TB/s.
 template <int KEY, int LPV, int ROPE>
 __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
   extern __shared__ f32x2 table[];
@@ -282,13 +291,8 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
       if constexpr (KEY == kBf16) {
         if (ok) *reinterpret_cast<u32x4*>(pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
       } else {
-        float m = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
-        // (neither NaN nor negative: ordered as its bits are)
-        const uint32_t top = vector_fold<LPV>(__float_as_uint(m), [](uint32_t a, uint32_t b) { return a > b ? a : b; });
         float scale;
-        const u32x2 codes = quantise(v, __uint_as_float(top), scale);
+        const u32x2 codes = quantise<LPV>(v, scale);
         if (ok) {
           *reinterpret_cast<u32x2*>(pool.kv + page * pool.kv_stride + i * kDim + 8 * sub) = codes;
           if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;
@@ -424,7 +428,7 @@ void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipS
   constexpr int kTokens = kSteps * kWaves * (64 / LPV);
   const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kTokens;
   // a grid of 16 blocks a CU goes round, with the next loads under way: 26.5 us
-  // where 8 a CU take 28.5 (65536 latents)
+  // where 8 a CU took 28.5 (65536 latents)
   const int64_t units = (p.n + kTokens - 1) / kTokens, most = 16 * device_cu_count();
   const dim3 grid((uint32_t)(units < most ? units : most));
   for_rotation(p, [&](auto rope) {

@@ -291,3 +291,29 @@ def test_far_positions_still_turn(lib, halves):
     pairs = (lambda v: np.hypot(v[:, :32], v[:, 32:])) if halves else (lambda v: np.hypot(v[:, 0::2], v[:, 1::2]))
     assert (np.abs(pairs(got) - pairs(was)) <= pairs(was) * (2.0 ** -8 + 2.0 ** -21)).all()
     assert torch.equal(out[..., : dim - 64].cpu(), x[..., : dim - 64])
+
+
+@pytest.mark.parametrize("n", [1, 7, 600])
+def test_plain_store_of_nan_and_inf(lib, n):
+    """Values next to the ends of the type, infinities and NaN: the scales and,
+    where the quotient is a number, the codes are idx_store_keys_fp8's (which
+    leaves the codes of NaN and infinities open); a quotient that is none (NaN,
+    or infinity over infinity) becomes +-448 with the value's sign."""
+    rng = np.random.default_rng(n)
+    x = torch.from_numpy(rng.standard_normal((n, 128)) * 10.0 ** rng.integers(-38, 38, (n, 1))).to(torch.bfloat16)
+    odd = torch.tensor([float("nan"), -float("nan"), float("inf"), -float("inf"), 3.3e38, -3.3e38, 1e-38, -1e-40, 0.0, -0.0]).to(torch.bfloat16)
+    where = torch.from_numpy(rng.random((n, 128)) < 0.01)
+    x[where] = odd[torch.from_numpy(rng.integers(0, len(odd), int(where.sum())))]
+    x[0, 5] = float("nan")
+    pages = n // PAGE + 1
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n])
+    a = torch.zeros(pages * 8448, dtype=torch.uint8, device="cuda")
+    b = torch.zeros_like(a)
+    lib.idx_norm_rope_store_fp8(x.cuda(), None, None, slots.cuda(), a, a.data_ptr() + 8192, norm=False, num_pages=pages)
+    lib.idx_store_keys_fp8(x.cuda(), slots.cuda(), b, b.data_ptr() + 8192, num_pages=pages)
+    (codes, scales), (keys, key_scales) = (split_pool(t, None, pages, 128, True, 8448, 8448) for t in (a, b))
+    assert np.array_equal(scales, key_scales)
+    none = (x.isnan() | (x.isinf() & torch.from_numpy(np.isinf(scales[slots.numpy()]))[:, None])).numpy()
+    codes, keys = codes[slots.numpy()], keys[slots.numpy()]
+    sign = ((x.view(torch.int16).numpy() >> 15) & 1).astype(np.uint8) << 7
+    assert np.array_equal(codes[~none], keys[~none]) and np.array_equal(codes[none], (sign | 0x7E)[none])
