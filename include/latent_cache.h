@@ -148,8 +148,7 @@ int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, i
  *   q          bf16 [rows][num_heads][512], contiguous, 16-byte aligned.
  *   kv_pages, kscale, num_pages, kv_page_stride, kscale_page_stride
  *              the pool of 512-value pages: kv_page_stride >= 32768 bytes
- *              (bf16: 65536), num_pages at most 33,554,432, the rest as in
- *              idx_paged_mqa_logits_fp8.
+ *              (bf16: 65536), the rest as in idx_paged_mqa_logits_fp8.
  *   page_table int32, 4-byte aligned: row b's table (table_width entries) at
  *              page_table + t*page_table_row_stride with t = b, or
  *              t = row_table[b] where row_table is not NULL.  A stride of 0

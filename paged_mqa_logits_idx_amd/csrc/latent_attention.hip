@@ -67,9 +67,9 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef int v2i __attribute__((ext_vector_type(2)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
-// A position that is masked, or whose page id lies outside the pool, is
-// gathered from here: it must not bring values of its own into the products.
-__device__ const u32x4 kZeroLatent[2 * kLatent / 16] = {};
+// A position that is masked, or (16 bytes on) whose page id lies outside the pool,
+// is gathered from here: it must not bring values of its own into the products.
+__device__ const u32x4 kZeroLatent[2 * kLatent / 16 + 1] = {};
 
 struct Attend {
   const uint8_t* q;    // bf16 [rows][heads][512]
@@ -153,28 +153,25 @@ struct Shape {
   static constexpr int kGather = kTile / kWaves;    // positions that a wave gathers
   static constexpr int kPerDma = 64 / kChunks;      // positions of one DMA
   static constexpr int kDmas = kGather / kPerDma;
-  static constexpr int kDmaOps = kDmas + (KEY == kFp8 ? 1 : 0);  // of a wave and tile, scales included
-  static constexpr int kRing = 16;                  // tiles whose positions are resolved ahead
+  static constexpr int kRing = 8;                   // tiles whose positions are resolved, four at a time
 };
 
 template <int KEY>
 struct AttendShared {
   using S = Shape<KEY>;
   uint8_t tile[S::kBuffers][kTile * S::kRowBytes];
-  float scale[S::kBuffers][kTile];   // e4m3 scales of the tiles' positions
-  uint32_t ref[S::kRing][kTile];     // slots of the positions (64 * page + i), or kMasked, kBad
+  uint64_t at[S::kRing][kTile];      // where the positions' latents are
+  float scale[S::kRing][kTile];      // their e4m3 scales
   bf16x8 p[4][S::HT][2];                // probabilities, by 16 positions and head, in operand order
-  f32x4 part[4][2][2][64];              // halves of scores on their way: by block, wave and lane
-  uint32_t special[S::kRing];           // whether a tile has a position that is masked or bad
+  union {
+    f32x4 part[4][2][2][64];            // halves of scores on their way: by block, wave and lane
+    float mx[S::HT][4];                 // maxima of the tile's blocks of 16 positions
+  };
+  __attribute__((aligned(4))) uint16_t special[S::kRing][2];  // whether half a tile has a position that is masked or bad
   uint32_t over[4];                     // whether a tile's scores exceed the references, by tile % 4
-  float mx[S::HT][4];                   // maxima of the tile's blocks of 16 positions
   float by[S::HT];                      // factors of a moved reference; at the end the references
   float sum[4][S::HT];
 };
-
-constexpr uint32_t kMasked = 0xffffffffu;  // no position
-constexpr uint32_t kBad = 0xfffffffeu;     // its page id lies outside the pool
-constexpr int64_t kMaxPages = (int64_t)1 << 25;  // 64 * page + i stays below kBad (and 2^25 pages are a TiB)
 
 template <int KEY>
 __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kernel(Attend a) {
@@ -208,6 +205,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   // instead of 2).  Heads past the last are zero.
   const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[0][0];
   const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[0][0];
+  const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroLatent);
   constexpr uint32_t kQueryAt = sizeof(sh.tile) - S::HT * 2 * kLatent;
   constexpr int kResolvers = S::kWaves / 2, kMany = S::kRing * kTile / (64 * kResolvers);
   const int32_t whole = a.width * kPage, bound = a.k >= 0 ? min(a.k, whole) : whole;
@@ -230,7 +228,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     for (int e = 0; e < S::HT / (S::kWaves - kResolvers); ++e) {
       const int h = (S::kWaves - kResolvers) * e + wave - kResolvers;
       const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent)
-                                            : reinterpret_cast<const uint8_t*>(kZeroLatent);
+                                            : zero;
       dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
     }
   }
@@ -252,48 +250,36 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   float m = 0.0f, most = -INFINITY, sum = 0.0f;
 
   if (mine > 0) {
-    // Slots of positions: page ids of the entries, then the ring's places of
-    // tile j's, a lane each.
+    // Where positions are: page ids of the entries, then the ring's places of tile
+    // j's, and its scales on their way; lane l has place l (or half + l of a tile).
     auto page_of = [&](int32_t p) -> int32_t { return (uint32_t)p < (uint32_t)whole && table_ok ? tab[p / kPage] : -1; };
-    auto keep = [&](int32_t j, int32_t p, int32_t page) {
-      uint32_t r = kMasked;
-      if ((split + j * a.splits) * kTile + lane < count && (uint32_t)p < (uint32_t)L)
-        r = (uint32_t)page < a.pages_lim ? (uint32_t)page * kPage + p % kPage : kBad;
-      sh.ref[j % S::kRing][lane] = r;
-      const uint64_t odd = __ballot(r >= kBad);
-      if (lane == 0) sh.special[j % S::kRing] = odd != 0;
-    };
-    // Tile j into its buffer (zeros, past the last); every wave issues kDmaOps
-    // operations.  Lane l holds the address of the wave's position l % kGather.
-    struct Source {
-      uint32_t lo, hi;      // of the latent
-      const uint8_t* scale;
-    };
-    auto source_of = [&](int32_t j) -> Source {
-      uint32_t slot = sh.ref[j % S::kRing][S::kGather * wave + lane % S::kGather];
-      slot = j < mine ? slot : kMasked;
-      const bool ok = slot < kBad;
-      const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroLatent);
-      const uint8_t* src = a.kv + (uint64_t)(slot / kPage) * (uint64_t)a.kv_stride + (slot % kPage) * kRowBytes;
-      src = ok ? src : zero;
-      Source from = {(uint32_t)(uintptr_t)src, (uint32_t)((uintptr_t)src >> 32), zero};
-      if (KEY == kFp8 && ok) from.scale = a.ks + (uint64_t)(slot / kPage) * (uint64_t)a.ks_stride + 4 * (slot % kPage);
-      return from;
-    };
-    auto gather_part = [&](int32_t j, const Source& from, int d) {
-      const int buf = j % S::kBuffers, first = d * S::kPerDma, r = first + lane / S::kChunks;
-      if (d < S::kDmas) {
-        const uintptr_t base = ((uintptr_t)__shfl(from.hi, r) << 32) | __shfl(from.lo, r);
-        dma16(reinterpret_cast<const uint8_t*>(base) + 16 * swizzle(lane % S::kChunks, S::kGather * wave + r),
-              lds_tile + (uint32_t)((buf * kTile + S::kGather * wave + first) * kRowBytes));
-      } else if (lane < S::kGather) {
-        dma4(from.scale, lds_scale + (uint32_t)((buf * kTile + S::kGather * wave) * 4));
+    auto keep = [&](int32_t j, int32_t half_, int32_t p, int32_t page) {
+      const int at = half_ + lane;
+      const uint8_t *src = zero, *scale = zero;
+      bool ok = false;
+      if ((split + j * a.splits) * kTile + at < count && (uint32_t)p < (uint32_t)L) {
+        ok = (uint32_t)page < a.pages_lim;
+        src = ok ? a.kv + (uint64_t)page * (uint64_t)a.kv_stride + (p % kPage) * kRowBytes : zero + 16;
+        if (ok) scale = a.ks + (uint64_t)page * (uint64_t)a.ks_stride + 4 * (p % kPage);
       }
+      sh.at[j % S::kRing][at] = (uintptr_t)src;
+      if (KEY == kFp8) dma4(scale, lds_scale + (uint32_t)((j % S::kRing * kTile + half_) * 4));
+      const uint64_t odd = __ballot(!ok);
+      if (lane % 32 == 0) sh.special[j % S::kRing][at / 32] = (uint32_t)(odd >> lane) != 0;
+    };
+    // Tile j into its buffer, in kDmas operations of every wave; past the last,
+    // whatever the ring has.
+    const uint32_t place = 16 * swizzle(lane % S::kChunks, S::kGather * wave + lane / S::kChunks);
+    auto source_of = [&](int32_t j, int d) -> uint64_t {
+      return sh.at[j % S::kRing][S::kGather * wave + d * S::kPerDma + lane / S::kChunks];
+    };
+    auto gather_part = [&](int32_t j, uint64_t from, int d) {
+      dma16(reinterpret_cast<const uint8_t*>(from + (place ^ (32 * S::kPerDma * d))),
+            lds_tile + (uint32_t)((j % S::kBuffers * kTile + S::kGather * wave + d * S::kPerDma) * kRowBytes));
     };
     auto gather = [&](int32_t j) {
-      const Source from = source_of(j);
 #pragma unroll
-      for (int d = 0; d < S::kDmaOps; ++d) gather_part(j, from, d);
+      for (int d = 0; d < S::kDmas; ++d) gather_part(j, source_of(j, d), d);
     };
 
     if (threadIdx.x < 4) sh.over[threadIdx.x] = 0;
@@ -302,13 +288,13 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
 #pragma unroll
       for (int e = 0; e < kMany; ++e) page[e] = page_of(early[e]);
 #pragma unroll
-      for (int e = 0; e < kMany; ++e) keep(kMany * wave + e, early[e], page[e]);
+      for (int e = 0; e < kMany; ++e) keep(kMany * wave + e, 0, early[e], page[e]);
     }
     barrier();
     constexpr int kEarly = S::kBuffers - S::HT * 2 * kLatent / (kTile * kRowBytes);  // tiles beside the queries
 #pragma unroll
     for (int32_t j = 0; j < kEarly; ++j) gather(j);
-    wait_vm<kEarly * S::kDmaOps>();
+    wait_vm<kEarly * S::kDmas>();
     barrier();
     // Lane (n, half) holds head n's values of step s: 16*(2*(s/2) + half) +
     // 8*(s%2) .. +8 (e4m3: two steps share a 16-byte chunk of codes) or
@@ -344,8 +330,9 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
     };
     // Scores of tile j, while tile j + 1 is gathered.
-    auto score = [&](int32_t j, const Source& from) -> f32x16 {
-      static_assert(KEY == kFp8 || S::kDmaOps == 8);
+    auto score = [&](int32_t j) -> f32x16 {
+      static_assert(KEY == kFp8 || S::kDmas == 8);
+      uint64_t from = source_of(j + 1, 0);
       const uint8_t* rows = sh.tile[j % S::kBuffers];
       f32x16 half0 = (f32x16)(0.0f);
 #pragma unroll
@@ -360,15 +347,17 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c0, q[s], half0, 0, 0, 0);
         half0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c1, q[s + 1], half0, 0, 0, 0);
         gather_part(j + 1, from, s / 2);
+        if (s < 14) from = source_of(j + 1, s / 2 + 1);
       }
       send(half0);
       return half0;
     };
     const int own = 32 * pb + 16 * kh + 4 * half;  // the lane's positions: own + 8*k .. +4
     auto read_ks = [&](int32_t j, int k) -> f32x4 {
-      if constexpr (KEY == kFp8) return *reinterpret_cast<const f32x4*>(&sh.scale[j % S::kBuffers][own + 8 * k]);
+      if constexpr (KEY == kFp8) return *reinterpret_cast<const f32x4*>(&sh.scale[j % S::kRing][own + 8 * k]);
       return (f32x4){1.f, 1.f, 1.f, 1.f};
     };
+    auto special_of = [&](int32_t j) { return *reinterpret_cast<const uint32_t*>(sh.special[j % S::kRing]); };
     float part;  // the sum of the lane's probabilities
     // Base-2 logits of tile j less a reference, masks applied.
     auto logits = [&](int32_t j, float ref, float (&t)[8]) {
@@ -378,15 +367,13 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[4 * k + e] = fmaf(x[4 * k + e], a.scale2 * ks[e], -ref);
       }
-      if (uniform(sh.special[j % S::kRing]) != 0) {
+      if (uniform(special_of(j)) != 0) {
+        const uint64_t masked = (uintptr_t)zero, bad = masked + 16;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const u32x4 slot = *reinterpret_cast<const u32x4*>(&sh.ref[j % S::kRing][own + 8 * k]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t[4 * k + e] = slot[e] == kBad ? __builtin_nanf("") : t[4 * k + e];
-            t[4 * k + e] = slot[e] == kMasked ? -INFINITY : t[4 * k + e];
-          }
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t at = sh.at[j % S::kRing][own + 8 * (e / 4) + e % 4];
+          t[e] = at == bad ? __builtin_nanf("") : t[e];
+          t[e] = at == masked ? -INFINITY : t[e];
         }
       }
     };
@@ -514,7 +501,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     //                    the conversion of the next codes and the gather,
     //   pairs 4 .. 7     in the time of the probabilities, before them in one of
     //                    a SIMD's two waves and behind them in the other.
-    // The gather's five operations stand apart: the memory path takes one in
+    // The gather's four operations stand apart: the memory path takes one in
     // about 50 cycles, and a wave whose operation has to wait issues nothing else
     // (all in one place they held up every phase by 1500 cycles).
     auto add = [&](const bf16x8& v, const bf16x8 (&w)[NB], int mb) {
@@ -531,7 +518,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       u32x4 kk[kAhead];
       bf16x8 w[4][NB], c0, c1, v;
       Codes vv[4];
-      Source from;
+      uint64_t from = 0;
       if constexpr (kAdd) {
         over = sh.over[j & 3];
 #pragma unroll
@@ -542,7 +529,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       if constexpr (kScore) {
 #pragma unroll
         for (int t = 0; t < kAhead; ++t) kk[t] = read_k(kt, t);
-        special = sh.special[(j + 1) % S::kRing];
+        special = special_of(j + 1);
       }
       if constexpr (kAdd) {
         if (j == 0 || uniform(over) != 0) {
@@ -558,7 +545,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         vv[0] = read_v(vt, 1, 0);
         add(widen(vv[1]), w[0], 1);
         vv[1] = read_v(vt, 1, 1);
-        if constexpr (kScore) from = source_of(j + 3);
+        if constexpr (kScore) from = source_of(j + 3, 0);
       }
       f32x16 sc = (f32x16)(0.0f);
       if constexpr (kScore) c0 = fp8x8_to_bf16x8(kk[0].x, kk[0].y), c1 = fp8x8_to_bf16x8(kk[0].z, kk[0].w);
@@ -581,8 +568,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
           if (t >= 6) w[t - 4][0] = read_w(t - 4, 0), w[t - 4][1] = read_w(t - 4, 1);
         }
         if constexpr (kScore && kAdd) {
-          if (t == 1 || t == 4) gather_part(j + 3, from, t / 4);
-          if (t == 7) gather_part(j + 3, from, 2);
+          if (t == 1 || t == 4 || t == 7) gather_part(j + 3, from, t / 3), from = source_of(j + 3, t / 3 + 1);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -620,7 +606,6 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         chances();
         __builtin_amdgcn_sched_barrier(0);
         if (kh != 0) outputs();
-        gather_part(j + 3, from, 4);
       } else if constexpr (kScore) {
         chances();
       } else {
@@ -628,16 +613,13 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
       if (kScore && uniform(special) != 0) probabilities(j + 1);
     };
-    // Half of the ring anew, a tile a wave, past the tiles whose slots are still
-    // read (from next - 4 on); `next` is the tile gathered last.
-    auto refill = [&](int32_t next) {
-      constexpr int kHalf = S::kRing / 2;
-      static_assert(kHalf == S::kWaves);
-      const int32_t done = next - 4;
-      if (done >= kHalf && done % kHalf == 0 && done + kHalf < mine) {
-        const int32_t j = done + kHalf + wave, p = entry(j, lane);
-        keep(j, p, page_of(p));
-      }
+    // The ring's places of tiles j + 4 .. j + 7, half a tile a wave: of those before
+    // tile j.
+    auto resolve = [&](int32_t j) {
+      const int32_t tile = j + 4 + wave / 2, half_ = kTile / 2 * (wave & 1);
+      if (j == 0 || j % 4 != 0 || j + 4 >= mine || lane >= 32) return;
+      const int32_t p = entry(tile, half_ + lane);
+      keep(tile, half_, p, page_of(p));
     };
 
     if constexpr (KEY == kFp8) {
@@ -645,15 +627,15 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       // when at most the operations of the tiles issued after it are outstanding
       // (they complete in order).
       gather(2);
-      wait_vm<2 * S::kDmaOps>();
+      wait_vm<2 * S::kDmas>();
       barrier();
       phase(-1, std::true_type{}, std::false_type{});
       int32_t j = 0;
       for (; j + 1 < mine; ++j) {
-        wait_vm<S::kDmaOps>();
+        wait_vm<S::kDmas>();
         barrier();  // tile j + 1 and tile j's probabilities are there; every wave is done with tile j - 1
         phase(j, std::false_type{}, std::false_type{});
-        refill(j + 3);
+        resolve(j);
       }
       wait_vm<0>();
       barrier();
@@ -667,9 +649,8 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         wait_vm<0>();
         barrier();  // tile j is there; every wave is done with tile j - 1
         if (threadIdx.x == 0) sh.over[(j + 3) & 3] = 0;
-        const Source from = source_of(j + 1);
-        refill(j + 1);
-        const f32x16 half0 = score(j, from);
+        resolve(j);
+        const f32x16 half0 = score(j);
         barrier();
         receive(half0);
         probabilities(j);
@@ -846,7 +827,7 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
                      int64_t page_table_row_stride, int32_t k, float scale, void* workspace,
                      int64_t workspace_bytes, hipStream_t stream) {
   if (head_dim != kLatent || num_heads > kMaxHeads) return IDX_ERR_UNSUPPORTED;
-  if (!dims_ok(rows, num_heads, table_width, k) || num_pages > kMaxPages || page_table_row_stride < 0 || num_tables < 0 ||
+  if (!dims_ok(rows, num_heads, table_width, k) || page_table_row_stride < 0 || num_tables < 0 ||
       !(scale > -INFINITY && scale < INFINITY) || workspace_bytes < 0)
     return IDX_ERR_SHAPE;
   int st = validate_pool(KEY, kLatent, num_pages, kv_page_stride, kscale_page_stride);
@@ -878,7 +859,7 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   a.kv_stride = kv_page_stride;
   a.ks_stride = kscale_page_stride;
   a.pt_stride = page_table_row_stride;
-  a.pages_lim = (uint32_t)num_pages;
+  a.pages_lim = (uint32_t)(num_pages < (int64_t)1 << 31 ? num_pages : (int64_t)1 << 31);
   a.rows = rows;
   a.heads = num_heads;
   a.width = table_width;
