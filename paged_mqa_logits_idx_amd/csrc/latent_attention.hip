@@ -42,9 +42,9 @@
 // page id, latent), two tiles and two launches.
 //
 // Running maximum: all waves agree on a reference m_h for each head.  It
-// moves, and the sums are rescaled, only when a tile's maximum exceeds it by
-// more than 2^8 (of base-2 logits): probabilities then reach 256 instead of 1,
-// which costs no precision, and most tiles rescale nothing.
+// moves, and the sums are rescaled, only when the probabilities that a lane has of
+// a tile add up to more than 256: they reach that instead of 1, which costs no
+// precision, and most tiles rescale nothing.
 //
 // Rounding: scores, exponentials, sums and outputs are float32; the products
 // take bf16 operands, which rounds the probability (times the e4m3 scale) once,
@@ -56,7 +56,8 @@
 
 namespace {
 
-constexpr float kLazy = 8.0f;       // base-2 logits that the maximum may exceed its reference by
+constexpr float kLimit = 256.0f;    // what a lane's 8 probabilities may add up to; one is above 2^kLazy then
+constexpr float kLazy = 5.0f;       // base-2 logits that a maximum exceeds its reference by where it moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kHeadTile = 64;       // heads of a unit
@@ -245,9 +246,10 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = (f32x16)(0.0f);
-  // Of head 32*hg + n: reference (0 before the first), what a logit may exceed
-  // it by (anything does before the first), sum of probabilities.
-  float m = 0.0f, most = -INFINITY, sum = 0.0f;
+  // Of head 32*hg + n: reference (0 before the first), what a lane's 8
+  // probabilities may add up to by it (nothing, before the first), sum of
+  // probabilities.
+  float m = 0.0f, limit = -1.0f, sum = 0.0f;
 
   if (mine > 0) {
     // Where positions are: page ids of the entries, then the ring's places of tile
@@ -398,13 +400,13 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
       sh.p[2 * pb + kh][32 * hg + n][half] = w;
     };
-    // Tile j's probabilities by the reference as it is, and whether it will do:
-    // a logit more than kLazy over it, or the head's first, and it will not.
+    // Tile j's probabilities by the reference as it is, and whether it will do: it
+    // will not where a lane's add up to more than kLimit, or the head has none.
     auto probabilities = [&](int32_t j) {
       float t[8];
       logits(j, m, t);
-      if (__ballot(max_of(t) > most) != 0) sh.over[j & 3] = 1;
       weigh(j, t);
+      if (__ballot(part > limit) != 0) sh.over[j & 3] = 1;
     };
     // The heads' references anew from tile j's maxima, the sums so far to match,
     // and the tile's probabilities again.
@@ -418,9 +420,9 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       barrier();
       const f32x4 all = *reinterpret_cast<const f32x4*>(sh.mx[h]);
       top = fmaxf(fmaxf(all.x, all.y), fmaxf(all.z, all.w));
-      const bool moves = top - m > most;
-      const float f = moves ? (most == kLazy ? __builtin_amdgcn_exp2f(m - top) : 0.0f) : 1.0f;
-      if (moves) m = top, most = kLazy;
+      const bool live = limit > 0.0f, moves = live ? top - m > kLazy : top > -INFINITY;
+      const float f = moves ? (live ? __builtin_amdgcn_exp2f(m - top) : 0.0f) : 1.0f;
+      if (moves) m = top, limit = kLimit;
       sum *= f;
       if (pb == 0 && kh == 0 && half == 0) sh.by[h] = f;
 #pragma unroll
@@ -585,19 +587,17 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       };
       auto chances = [&]() {
         const f32x4 ks[2] = {read_ks(j + 1, 0), read_ks(j + 1, 1)};
-        float top = -INFINITY;
         part = 0.0f;
         bf16x8 out;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float by = ks[e / 4][e % 4], t = fmaf(x[e], a.scale2 * by, -m);
-          top = fmaxf(top, t);
           const float p = __builtin_amdgcn_exp2f(t);
           part += p;
           out[e] = (__bf16)(p * by);
         }
         sh.p[2 * pb + kh][32 * hg + n][half] = out;
-        if (__ballot(top > most) != 0) sh.over[(j + 1) & 3] = 1;
+        if (__ballot(part > limit) != 0) sh.over[(j + 1) & 3] = 1;
       };
       if constexpr (kScore && kAdd) {
         gather_part(j + 3, from, 3);
@@ -670,7 +670,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   {
     const float s = sum + __shfl_xor(sum, 32);
     if (half == 0) sh.sum[2 * pb + kh][32 * hg + n] = s;
-    if (half == 0 && pb == 0 && kh == 0) sh.by[32 * hg + n] = most == kLazy ? m : -INFINITY;
+    if (half == 0 && pb == 0 && kh == 0) sh.by[32 * hg + n] = limit > 0.0f ? m : -INFINITY;
   }
   wait_vm<0>();  // (nothing in it: the queries are still on their way)
   barrier();
