@@ -23,23 +23,22 @@
 // So a latent is moved from memory once a unit, and its codes are widened to bf16
 // (exactly) on the way into the matrix units; the position's scale is applied to
 // its scores and to its probabilities, in float32.  The e4m3 products of the
-// matrix units themselves would need no widening, but drop what lies 2^-13 below
-// the largest product: 1.7e-5 of the result (bf16 operands: 2e-7), of scores
-// whose errors the exponential passes on in full.
+// matrix units themselves would need no widening, but drop what lies 2^-12.5
+// below the largest product: 1.7e-5 of the result (bf16 operands: 2e-7), of
+// scores whose errors the exponential passes on in full.
 //
 // A row is split where its units are fewer than the CUs; the splits leave sums
 // and outputs in float32, which a second kernel joins.
 //
 // What bounds it.  Many rows: 4096 of 64 heads over 2048 of 5632 positions take
-// 0.98 - 1.0 ms, 0.9 PFLOP/s (a library product of that size 1.2 - 1.3).  Of the
-// SIMDs' cycles the matrix units have 40 %, vector instructions 44 % (the
-// widening, 96 a wave and tile of 7.5 clocks each, is half of them), the LDS 36 % of
-// its own; a tile takes 4100 clocks where its products take 2048, and taking away
-// any one of the parts shortens it by a tenth at most.  A unit's start and end
-// take 10 us of 62.  Few rows: 64 of 64 heads over 2048 of 32768 positions take 41
-// us, of which 8 the joining: 90 MB are read and 34 written (the splits'
-// outputs) in 33 us, then 35 read; one row takes 16.4, three loads in a row (list,
-// page id, latent), two tiles and two launches.
+// 0.92 ms, 0.98 PFLOP/s (a library product of 8192^3 1.18).  Of the SIMDs' cycles
+// the matrix units have 43 %, vector instructions issue in 44 % (173 a wave and
+// tile, 96 of them the widening's, which take 7.5 clocks, not 4), the LDS has 34 %
+// of its own; taking away any one part shortens a tile by a tenth at most.  A
+// unit's start and end take 9 us of 57.  Few rows: 64 of 64 heads over 2048 of
+// 32768 positions take 41 us, of which 8 the joining: 107 MB are read and 34
+// written (the splits' outputs) in 32 us, then 35 read; one row takes 15.5, three
+// loads in a row (list, page id, latent), two tiles and two launches.
 //
 // Running maximum: all waves agree on a reference m_h for each head.  It
 // moves, and the sums are rescaled, only when the probabilities that a lane has of
@@ -213,12 +212,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   const int32_t* idx = a.k >= 0 ? a.idx + (int64_t)b * a.k : nullptr;
   auto entry = [&](int32_t j, int32_t i) -> int32_t {  // entry i of the unit's tile j, or -1
     const int32_t t = (split + j * a.splits) * kTile + i;
-    const int32_t* list = idx;
-    // Keeps the compiler from a second copy of the loop over the bf16 tiles: 53
-    // against 60 us (16 rows of 8192 positions and 128 heads).  The e4m3 tiles'
-    // loop is 2 % faster as two copies.
-    if constexpr (KEY == kBf16) asm("" : "+s"(list));
-    return t >= bound ? -1 : list ? list[t] : t;
+    return t >= bound ? -1 : idx ? idx[t] : t;
   };
   int32_t early[kMany];  // lane's entry of tiles kMany * wave ..
   if (wave < kResolvers) {
@@ -795,8 +789,9 @@ constexpr int64_t kMaxUnits = 8000000;  // a launch has less than 2^32 threads
 // on the device): a unit takes about 2.2 us a tile, and joining s splits about
 // 2.2 * s / 8 more, so up to sqrt(8 * tiles), all of the same number of tiles,
 // while every unit has a CU of its own.  One row of 64 heads over 8, 16, 32 and
-// 4096 tiles takes 13.4, 14.9, 16.5 and 88 us; with a tile a split, or at most
-// 256 splits, 13.4, 15.0, 17.8 and 86; the first two unsplit 23 and 38.
+// 4096 tiles took 13.4, 14.9, 16.5 and 88 us when this was chosen; with a tile a
+// split, or at most 256 splits, 13.4, 15.0, 17.8 and 86; the first two unsplit 23
+// and 38.
 int splits_of(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
   const int64_t most = k >= 0 ? (k < (int64_t)table_width * kPage ? k : (int64_t)table_width * kPage)
                                 : (int64_t)table_width * kPage;
