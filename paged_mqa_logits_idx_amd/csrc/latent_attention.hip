@@ -59,6 +59,7 @@ constexpr float kLimit = 256.0f;    // what a lane's 8 probabilities may add up 
 constexpr float kLazy = 5.0f;       // base-2 logits that a maximum exceeds its reference by where it moves
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxHeads = 128;
 constexpr int kHeadTile = 64;       // heads of a unit
 constexpr int kTile = 64;           // positions of a tile
 constexpr int kPartials = kHeadTile * kLatent;  // float32 outputs of a unit
@@ -107,6 +108,7 @@ __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t dst) {
 __device__ __forceinline__ void dma4(const uint8_t* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
 }
+
 // Waits until at most N vector-memory operations are outstanding.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -187,11 +189,12 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   // Units of one row and split (its head blocks read the same latents) follow
   // each other on one XCD; the last rows, the longest of a causal batch, start
   // first.
-  const int32_t at = blockIdx.x >> 3;
-  const int32_t hb = at % a.head_blocks;
-  const int64_t rs = (int64_t)(at / a.head_blocks) * 8 + (blockIdx.x & 7);
-  if (rs >= (int64_t)a.rows * a.splits) return;
-  const int32_t b = a.rows - 1 - (int32_t)(rs / a.splits), split = (int32_t)(rs % a.splits);
+  static_assert(kMaxHeads <= 2 * kHeadTile);  // one block of heads a row or two
+  const int hshift = a.head_blocks - 1, hb = (int)(blockIdx.x >> 3) & hshift;
+  const uint32_t rs = blockIdx.x >> (3 + hshift) << 3 | (blockIdx.x & 7), splits = (uint32_t)a.splits;
+  if (rs >= (uint32_t)a.rows * splits) return;
+  const uint32_t row = splits > 1 ? rs / splits : rs;
+  const int32_t b = a.rows - 1 - (int32_t)row, split = (int32_t)(rs - row * splits);
   const int32_t h0 = hb * S::HT;
 
   // What depends on nothing but the arguments goes out first: waves 0 .. 3 load
@@ -222,15 +225,15 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
 #pragma unroll
     for (int e = 0; e < S::HT / (S::kWaves - kResolvers); ++e) {
       const int h = (S::kWaves - kResolvers) * e + wave - kResolvers;
-      const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent)
-                                            : zero;
+      const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent) : zero;
       dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
     }
   }
   const int32_t L = uniform(min(max(a.sl[b], 0), whole));
   const int32_t count = min(bound, L);
   const int32_t tiles = (count + kTile - 1) / kTile;
-  const int32_t mine = tiles > split ? (tiles - split + a.splits - 1) / a.splits : 0;
+  const uint32_t left = tiles > split ? (uint32_t)(tiles - split) : 0u;
+  const int32_t mine = (int32_t)(splits > 1 ? (left + splits - 1) / splits : left);
   const int32_t table = a.rt ? a.rt[b] : 0;
   const bool table_ok = !a.rt || (table >= 0 && table < a.num_tables);
   const int32_t* tab = a.pt + (int64_t)(a.rt ? (table_ok ? table : 0) : b) * a.pt_stride;
@@ -781,7 +784,6 @@ __global__ __launch_bounds__(256) void latent_combine_kernel(Attend a) {
 // ---------------------------------------------------------------------------
 // Host side.
 
-constexpr int kMaxHeads = 128;
 constexpr int32_t kMaxWidth = 1 << 24;
 constexpr int64_t kMaxUnits = 8000000;  // a launch has less than 2^32 threads
 
