@@ -116,10 +116,14 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // Where chunk c (16 bytes) of position r stands within the position's LDS row:
-// rows of a multiple of 256 bytes would put one chunk of all positions into
-// the same banks.  16 positions spread over 16 chunks, 8 consecutive ones over
-// 8 even offsets (the transposing bf16 reads take pairs of chunks).
-__device__ __forceinline__ int swizzle(int c, int r) { return c ^ (((r & 7) << 1) | ((r >> 3) & 1)); }
+// rows of a multiple of 256 bytes would put one chunk of all positions into the
+// same banks.  Any 16 positions in a row take 16 places.  The transposing reads
+// take, of 32 lanes, two chunks of 8 positions whose bit 2 is one (e4m3), or four
+// chunks of 4 positions (bf16): also 16 places.
+template <int KEY>
+__device__ __forceinline__ constexpr int swizzle(int c, int r) {
+  return c ^ (KEY == kFp8 ? (r & 3) << 1 | (r & 8) | (r >> 2 & 1) : (r & 3) << 2 | (r >> 2 & 3));
+}
 
 // The end of a softmax: sums relative to 2^m become outputs (times by * half *
 // half) and the log of the denominator, in which a sink's base-2 logit joins.
@@ -164,7 +168,7 @@ struct AttendShared {
   uint8_t tile[S::kBuffers][kTile * S::kRowBytes];
   uint64_t at[S::kRing][kTile];      // where the positions' latents are
   float scale[S::kRing][kTile];      // their e4m3 scales
-  bf16x8 p[4][S::HT][2];                // probabilities, by 16 positions and head, in operand order
+  bf16x8 p[4][2][S::HT];                // probabilities, by 16 positions, half of a wave and head
   union {
     f32x4 part[4][2][2][64];            // halves of scores on their way: by block, wave and lane
     float mx[S::HT][4];                 // maxima of the tile's blocks of 16 positions
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     for (int e = 0; e < S::HT / (S::kWaves - kResolvers); ++e) {
       const int h = (S::kWaves - kResolvers) * e + wave - kResolvers;
       const uint8_t* src = h0 + h < a.heads ? a.q + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent) : zero;
-      dma16(src + 16 * swizzle(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
+      dma16(src + 16 * swizzle<KEY>(lane, h), lds_tile + kQueryAt + (uint32_t)(h * 2 * kLatent));
     }
   }
   const int32_t L = uniform(min(max(a.sl[b], 0), whole));
@@ -268,12 +272,12 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     };
     // Tile j into its buffer, in kDmas operations of every wave; past the last,
     // whatever the ring has.
-    const uint32_t place = 16 * swizzle(lane % S::kChunks, S::kGather * wave + lane / S::kChunks);
+    const uint32_t place = 16 * swizzle<KEY>(lane % S::kChunks, S::kGather * wave + lane / S::kChunks);
     auto source_of = [&](int32_t j, int d) -> uint64_t {
       return sh.at[j % S::kRing][S::kGather * wave + d * S::kPerDma + lane / S::kChunks];
     };
     auto gather_part = [&](int32_t j, uint64_t from, int d) {
-      dma16(reinterpret_cast<const uint8_t*>(from + (place ^ (32 * S::kPerDma * d))),
+      dma16(reinterpret_cast<const uint8_t*>(from + (place ^ (16 * swizzle<KEY>(0, S::kPerDma * d)))),
             lds_tile + (uint32_t)((j % S::kBuffers * kTile + S::kGather * wave + d * S::kPerDma) * kRowBytes));
     };
     auto gather = [&](int32_t j) {
@@ -302,7 +306,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
 #pragma unroll
     for (int s = 0; s < 16; ++s) {
       const int h = 32 * hg + n, c = 32 * kh + (KEY == kFp8 ? 2 * (2 * (s >> 1) + half) + (s & 1) : 2 * s + half);
-      q[s] = *reinterpret_cast<const bf16x8*>(&sh.tile[0][0] + kQueryAt + h * 2 * kLatent + 16 * swizzle(c, h));
+      q[s] = *reinterpret_cast<const bf16x8*>(&sh.tile[0][0] + kQueryAt + h * 2 * kLatent + 16 * swizzle<KEY>(c, h));
     }
     barrier();
 
@@ -312,7 +316,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     // (8*(i/4) + 4*half + i%4 of them) and products 8..15 its partner's.
     const int kr = 32 * pb + (n ^ 16 * kh);
     auto read_k = [&](const uint8_t* rows, int t) {  // fp8: values 16 of step pair t; bf16: 8 of step t
-      return *reinterpret_cast<const u32x4*>(rows + kr * kRowBytes + 16 * swizzle((KEY == kFp8 ? 16 : 32) * kh + 2 * t + half, kr));
+      return *reinterpret_cast<const u32x4*>(rows + kr * kRowBytes + 16 * swizzle<KEY>((KEY == kFp8 ? 16 : 32) * kh + 2 * t + half, kr));
     };
     auto send = [&](const f32x16& x) {
 #pragma unroll
@@ -395,7 +399,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
           w[4 * k + e] = (__bf16)(p * ks[e]);
         }
       }
-      sh.p[2 * pb + kh][32 * hg + n][half] = w;
+      sh.p[2 * pb + kh][half][32 * hg + n] = w;
     };
     // Tile j's probabilities by the reference as it is, and whether it will do: it
     // will not where a lane's add up to more than kLimit, or the head has none.
@@ -451,7 +455,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
         // position k, lane i gets value i of the 8 positions
         const int k = lane16 >> 1, r = 16 * s + 8 * (k >> 2) + 4 * half + (k & 3), c = 2 * (MB * wave + mb) + (g & 1);
         t.lo = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) v2i*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (lane & 1)));
+            (__attribute__((address_space(3))) v2i*)(rows + r * kRowBytes + 16 * swizzle<KEY>(c, r) + 8 * (lane & 1)));
       } else {
         // 16 lanes read 4 positions x 16 values: lanes 4k .. 4k+3 the 32 bytes of
         // position k
@@ -461,7 +465,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
           const int r = 16 * s + 8 * e + 4 * half + (lane16 >> 2);
           const int c = 4 * (MB * wave + mb) + 2 * (g & 1) + (lane16 >> 1 & 1);
           u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) v4s*)(rows + r * kRowBytes + 16 * swizzle(c, r) + 8 * (lane & 1)));
+              (__attribute__((address_space(3))) v4s*)(rows + r * kRowBytes + 16 * swizzle<KEY>(c, r) + 8 * (lane & 1)));
         }
         t.lo = __builtin_bit_cast(v2i, u[0]), t.hi = __builtin_bit_cast(v2i, u[1]);
       }
@@ -471,7 +475,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       if constexpr (KEY == kFp8) return fp8x8_to_bf16x8((uint32_t)t.lo.x, (uint32_t)t.lo.y);
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(t.lo, t.hi, 0, 1, 2, 3));
     };
-    auto read_w = [&](int s, int nb) { return sh.p[s][32 * nb + n][half]; };
+    auto read_w = [&](int s, int nb) { return sh.p[s][half][32 * nb + n]; };
     auto accumulate = [&](int32_t j, const Codes (&early)[MB]) {
       const uint8_t* rows = sh.tile[j % S::kBuffers];
 #pragma unroll
@@ -593,7 +597,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
           part += p;
           out[e] = (__bf16)(p * by);
         }
-        sh.p[2 * pb + kh][32 * hg + n][half] = out;
+        sh.p[2 * pb + kh][half][32 * hg + n] = out;
         if (__ballot(part > limit) != 0) sh.over[(j + 1) & 3] = 1;
       };
       if constexpr (kScore && kAdd) {
@@ -620,6 +624,9 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     };
 
     if constexpr (KEY == kFp8) {
+      // Of a SIMD's two waves one goes first throughout: they drift apart, and one
+      // has matrix instructions where the other has not (1 % of a prefill).
+      if (kh != 0) __builtin_amdgcn_s_setprio(1);
       // Tiles j + 2 and j + 3 are on their way during phase j.  A tile has arrived
       // when at most the operations of the tiles issued after it are outstanding
       // (they complete in order).
@@ -707,7 +714,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       const f32x16 o = acc[mb][nb] * c.by * c.half * c.half;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<bf16x4*>(rows + h * 2 * kLatent + 16 * swizzle(S::kDims / 8 * wave + 4 * mb + k, h) + 8 * half) =
+        *reinterpret_cast<bf16x4*>(rows + h * 2 * kLatent + 16 * swizzle<KEY>(S::kDims / 8 * wave + 4 * mb + k, h) + 8 * half) =
             (bf16x4){(__bf16)o[4 * k], (__bf16)o[4 * k + 1], (__bf16)o[4 * k + 2], (__bf16)o[4 * k + 3]};
     }
   }
@@ -717,7 +724,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
     const int h = S::kWaves * e + wave;
     if (h0 + h < a.heads)
       *reinterpret_cast<u32x4*>(a.out + ((int64_t)b * a.heads + h0 + h) * (2 * kLatent) + 16 * lane) =
-          *reinterpret_cast<const u32x4*>(rows + h * 2 * kLatent + 16 * swizzle(lane, h));
+          *reinterpret_cast<const u32x4*>(rows + h * 2 * kLatent + 16 * swizzle<KEY>(lane, h));
   }
 }
 
