@@ -728,18 +728,18 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   }
 }
 
-// Joins the splits of a row: a wave has 32 values of 8 heads, 4 a lane, which
-// are 16 bytes of a unit's outputs (8 heads of them a line).  16 splits' loads
-// are under way at once, outputs and sums together: which splits have written
-// any is known only with the sums.  The order of the splits is fixed, so the
+// Joins the splits of a row: a wave, a workgroup of its own (of four waves, one
+// row took 0.7 us more), has 32 values of 8 heads, 4 a lane, which are 16 bytes
+// of a unit's outputs (8 heads of them a line).  16 splits' loads are under way at
+// once, outputs and sums together: which splits have written any is known only
+// with the sums.  The order of the splits is fixed, so the
 // result does not depend on their timing.
 template <int kBatch>
-__global__ __launch_bounds__(256) void latent_combine_kernel(Attend a) {
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const uint32_t groups = (uint32_t)(a.heads + 7) / 8;
-  const int64_t b = (blockIdx.x >> 2) / groups;
-  const int32_t h = 8 * (int32_t)((blockIdx.x >> 2) % groups) + (lane & 7), n = h % kHeadTile;
-  const int block = 4 * (int)(blockIdx.x & 3) + wave, piece = lane >> 3;  // values 32*block + 4*piece .. +4
+__global__ __launch_bounds__(64) void latent_combine_kernel(Attend a) {
+  const int lane = threadIdx.x;
+  const int block = (int)blockIdx.x, piece = lane >> 3;  // values 32*block + 4*piece .. +4
+  const int32_t h = 8 * (int32_t)blockIdx.y + (lane & 7), n = h % kHeadTile;
+  const int64_t b = blockIdx.z;
   const int64_t unit0 = b * a.splits * a.head_blocks + h / kHeadTile;
   // the lane's 16 bytes of a unit (accumulator (block, n / 32), chunk piece / 2)
   const f32x4* from = reinterpret_cast<const f32x4*>(a.part + unit0 * kPartials) +
@@ -875,16 +875,16 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   (void)hipGetLastError();  // start from a clean error state
   latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(Shape<KEY>::kThreads), 0, stream>>>(a);
   if (a.splits > 1) {
-    const dim3 grid((uint32_t)(4 * rows * ((num_heads + 7) / 8)));
+    const dim3 grid(kLatent / 32, (uint32_t)((num_heads + 7) / 8), (uint32_t)rows);  // (at most a row a CU)
     // A batch no larger than the splits: 4 of them take 8.0 us where the kernel
     // for 16, with its registers, takes 12 (64 rows of 64 heads), and 16 take 4.0
     // us at once and 7.4 with four under way at a time (one row).
     if (a.splits <= 4)
-      latent_combine_kernel<4><<<grid, dim3(256), 0, stream>>>(a);
+      latent_combine_kernel<4><<<grid, dim3(64), 0, stream>>>(a);
     else if (a.splits <= 8)
-      latent_combine_kernel<8><<<grid, dim3(256), 0, stream>>>(a);
+      latent_combine_kernel<8><<<grid, dim3(64), 0, stream>>>(a);
     else
-      latent_combine_kernel<16><<<grid, dim3(256), 0, stream>>>(a);
+      latent_combine_kernel<16><<<grid, dim3(64), 0, stream>>>(a);
   }
   return launch_status();
 }
