@@ -11,7 +11,6 @@ or ``__graft_entry__.build()``); importing this module without it raises.
 from __future__ import annotations
 
 import ctypes
-import math
 from pathlib import Path
 
 import torch  # loads the HIP runtime the library binds to (same soname)
@@ -429,7 +428,9 @@ def idx_store_keys_bf16(keys, slots, kv_pages, *, num_pages, n=None, kv_page_str
 # tensors; a call on a few tokens takes the GPU a few microseconds, so the checks
 # below stay short: dtype, shape, layout and device of each, once.
 
-# (the public current_stream builds an object, which takes half as long as a launch)
+# (the public current_stream builds an object, which takes half as long as a
+# launch, and the public current_device looks whether the runtime has started)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -460,7 +461,7 @@ def _rows(name, x, dims) -> int:
     if len(shape) != dims:
         raise ValueError(f"{name} must have {dims} dims, got {list(shape)}")
     if x.is_contiguous():
-        return math.prod(shape[1:])
+        return shape[1] if dims == 2 else shape[1] * shape[2]
     dense = 1
     for size, step in zip(reversed(shape[1:]), reversed(x.stride()[1:])):
         if size > 1 and step != dense:
@@ -478,7 +479,7 @@ def _launch(fn, dev, stream, check, *args) -> int:
     if dev < 0:
         raise ValueError("tensors passed to the indexer library must be device tensors")
     handle = _raw_stream(dev) if stream is None else _stream_handle(stream, dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
