@@ -17,6 +17,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
+// Outputs of a call that writes 16 MiB or more pass the caches by: the inputs
+// keep their place, and the next kernel would not find them there whole.  65536
+// latents stored 26.7 -> 23.0 us, stored and read back 53.1 -> 48.6; but 16384
+// stored and read back 16.6 -> 17.2.
+inline bool is_far(int64_t n, int64_t bytes) { return n >= (((int64_t)1 << 24) + bytes - 1) / bytes; }
+
+template <bool FAR, class T>
+__device__ __forceinline__ void put(T v, uint8_t* to) {
+  if constexpr (FAR) __builtin_nontemporal_store(v, reinterpret_cast<T*>(to));
+  else *reinterpret_cast<T*>(to) = v;
+}
+
 struct Vectors {
   const uint8_t* x;      // bf16
   const float* weight;   // [D] or NULL
@@ -137,8 +149,8 @@ __device__ __forceinline__ void load_weight(const Vectors& p, int sub, float (&w
 }
 
 // Unit = one token x `STEPS` groups of kWaves * 64/LPV heads, which share the
-// token's turns.  Bound by memory: 4096 tokens of 64 heads of 512 take 95 us, 537
-// MB at 5.6 TB/s.
+// token's turns.  Bound by memory: 4096 tokens of 64 heads of 512 take 92 us, 537
+// MB at 5.8 TB/s.
 template <int LPV, int ROPE, int STEPS>
 __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t* out, int32_t groups) {
   extern __shared__ f32x2 table[];
@@ -169,7 +181,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
       bf16x8_to_float(raw[u], v);
       norm_rotate<LPV, ROPE>(p, sub, w, table, v);
       if (h < p.heads)
-        *reinterpret_cast<u32x4*>(out + ((t * p.heads + h) * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
+        put<(STEPS > 1)>(float_to_bf16x8(v), out + ((t * p.heads + h) * kDim + 8 * sub) * 2);
     }
   }
 }
@@ -232,10 +244,10 @@ constexpr int kSteps = 2;  // (1 and 4: 28 and 31 us where 2 took 26.5; small ca
 
 // Unit = kSteps groups of 64/LPV tokens, a wave's; the next unit's vectors are
 // on their way while one is worked on.  A wave has its tokens' turns to itself,
-// so no wave waits for another.  65536 latents to e4m3 take 26 us: 101 MB at
-// 3.9 TB/s, but bound by the vector instructions (174 a token, issuing in nearly
-// all of the SIMDs' cycles); 32768 to bf16 take 14.4, 67 MB at 4.6 TB/s.
-template <int KEY, int LPV, int ROPE>
+// so no wave waits for another.  65536 latents to e4m3 take 23 us: 101 MB at
+// 4.4 TB/s, but bound by the vector instructions (174 a token, issuing in nearly
+// all of the SIMDs' cycles); to bf16 23 us too, 135 MB at 5.8 TB/s.
+template <int KEY, int LPV, int ROPE, bool FAR>
 __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
   extern __shared__ f32x2 table[];
   constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = kSteps * kVecs;
@@ -289,12 +301,12 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
       const bool ok = slot >= 0 && slot < pool.slots;
       const int64_t page = ok ? slot / kPage : 0, i = ok ? slot % kPage : 0;
       if constexpr (KEY == kBf16) {
-        if (ok) *reinterpret_cast<u32x4*>(pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2) = float_to_bf16x8(v);
+        if (ok) put<FAR>(float_to_bf16x8(v), pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2);
       } else {
         float scale;
         const u32x2 codes = quantise<LPV>(v, scale);
         if (ok) {
-          *reinterpret_cast<u32x2*>(pool.kv + page * pool.kv_stride + i * kDim + 8 * sub) = codes;
+          put<FAR>(codes, pool.kv + page * pool.kv_stride + i * kDim + 8 * sub);
           if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;
         }
       }
@@ -305,8 +317,8 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
 
 // Unit = `STEPS` groups of kWaves * 64/LPV slots: their loads are under way at
 // once, in two trips (slots, then codes and scales).  Bound by memory: 262208
-// latents from e4m3 take 86 us, 404 MB at 4.7 TB/s.
-template <int KEY, int LPV, int STEPS>
+// latents from e4m3 take 78 us, 404 MB at 5.2 TB/s.
+template <int KEY, int LPV, int STEPS, bool FAR>
 __global__ __launch_bounds__(kThreads) void load_slots_kernel(Pool pool, const int64_t* slots, int64_t n,
                                                               uint8_t* out, int64_t out_stride) {
   constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kTokens = STEPS * kWaves * kVecs;
@@ -348,7 +360,7 @@ __global__ __launch_bounds__(kThreads) void load_slots_kernel(Pool pool, const i
         for (int k = 0; k < 8; ++k) v[k] *= scale[u];
         r = float_to_bf16x8(v);
       }
-      *reinterpret_cast<u32x4*>(out + t * out_stride + 16 * sub) = r;
+      put<FAR>(r, out + t * out_stride + 16 * sub);
     }
   }
 }
@@ -414,8 +426,9 @@ void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
   uint8_t* to = static_cast<uint8_t*>(out);
   for_rotation(p, [&](auto rope) {
     constexpr int kRope = decltype(rope)::value;
-    // four steps where they leave the device full: 95 and 114 us (4096 tokens of
-    // 64 heads of 512), but 11.2 and 10.1 (1024 of 64 of 128, 1024 units)
+    // four steps, and past the caches, where they leave the device full (some 64
+    // MiB): 92 us, 96 with ordinary stores, 114 in one step (4096 tokens of 64 heads
+    // of 512); but 11.2 and, in one step, 10.1 (1024 of 64 of 128, 1024 units)
     if (p.n * groups >= 16 * device_cu_count())
       norm_rope_kernel<LPV, kRope, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, to, groups);
     else
@@ -432,7 +445,11 @@ void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipS
   const int64_t units = (p.n + kTokens - 1) / kTokens, most = 16 * device_cu_count();
   const dim3 grid((uint32_t)(units < most ? units : most));
   for_rotation(p, [&](auto rope) {
-    norm_rope_store_kernel<KEY, LPV, decltype(rope)::value><<<grid, dim3(kThreads), lds, stream>>>(p, pool, slots);
+    constexpr int kRope = decltype(rope)::value;
+    if (is_far(p.n, LPV * (KEY == kFp8 ? 8 : 16)))
+      norm_rope_store_kernel<KEY, LPV, kRope, true><<<grid, dim3(kThreads), lds, stream>>>(p, pool, slots);
+    else
+      norm_rope_store_kernel<KEY, LPV, kRope, false><<<grid, dim3(kThreads), lds, stream>>>(p, pool, slots);
   });
 }
 
@@ -464,14 +481,17 @@ void launch_load(const Pool& pool, const int64_t* slots, int64_t n, void* out, i
                  hipStream_t stream) {
   constexpr int kOne = kWaves * (64 / LPV);
   uint8_t* o = static_cast<uint8_t*>(out);
-  // four steps where they leave the device full: 86 and 96 us (262208 latents),
-  // 10.9 and 11.8 (32768), but 8.3 and 7.7 (16384)
-  if (n >= (int64_t)4 * kOne * 8 * device_cu_count())
-    load_slots_kernel<KEY, LPV, 4><<<grid_of((n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 0, stream>>>(
-        pool, slots, n, o, 2 * out_row_stride);
+  const dim3 ones = grid_of((n + kOne - 1) / kOne);
+  // past the caches: 78 us, 86 with ordinary stores (262208 latents from e4m3);
+  // four steps of e4m3 then, 88 us in one, but bf16 moves as much in one: 77 and 73
+  // us (196608)
+  if (!is_far(n, 16 * LPV))
+    load_slots_kernel<KEY, LPV, 1, false><<<ones, dim3(kThreads), 0, stream>>>(pool, slots, n, o, 2 * out_row_stride);
+  else if constexpr (KEY == kBf16)
+    load_slots_kernel<KEY, LPV, 1, true><<<ones, dim3(kThreads), 0, stream>>>(pool, slots, n, o, 2 * out_row_stride);
   else
-    load_slots_kernel<KEY, LPV, 1><<<grid_of((n + kOne - 1) / kOne), dim3(kThreads), 0, stream>>>(pool, slots, n, o,
-                                                                                                 2 * out_row_stride);
+    load_slots_kernel<KEY, LPV, 4, true><<<grid_of((n + 4 * kOne - 1) / (4 * kOne)), dim3(kThreads), 0, stream>>>(
+        pool, slots, n, o, 2 * out_row_stride);
 }
 
 template <int KEY>
