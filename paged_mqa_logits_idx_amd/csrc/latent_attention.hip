@@ -31,13 +31,13 @@
 // and outputs in float32, which a second kernel joins.
 //
 // What bounds it.  Many rows: 4096 of 64 heads over 2048 of 5632 positions take
-// 0.92 ms, 0.98 PFLOP/s (a library product of 8192^3 1.18).  Of the SIMDs' cycles
-// the matrix units have 43 %, vector instructions issue in 44 % (173 a wave and
-// tile, 96 of them the widening's, which take 7.5 clocks, not 4), the LDS has 34 %
+// 0.90 ms, 1.0 PFLOP/s (a library product of 8192^3 1.18).  Of the SIMDs' cycles
+// the matrix units have 45 %, vector instructions issue in 46 % (173 a wave and
+// tile, 96 of them the widening's, which take 7.5 clocks, not 4), the LDS has 26 %
 // of its own; taking away any one part shortens a tile by a tenth at most.  A
-// unit's start and end take 9 us of 57.  Few rows: 64 of 64 heads over 2048 of
-// 32768 positions take 41 us, of which 8 the joining: 107 MB are read and 34
-// written (the splits' outputs) in 32 us, then 35 read; one row takes 15.5, three
+// unit's start and end take 9 us of 55.  Few rows: 64 of 64 heads over 2048 of
+// 32768 positions take 39 us, of which 8 the joining: 107 MB are read and 34
+// written (the splits' outputs) in 31 us, then 35 read; one row takes 14.5, three
 // loads in a row (list, page id, latent), two tiles and two launches.
 //
 // Running maximum: all waves agree on a reference m_h for each head.  It

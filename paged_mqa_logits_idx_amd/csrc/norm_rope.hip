@@ -103,18 +103,21 @@ __device__ __forceinline__ float inverse_root(float v) {
 enum { kPlain, kNeighbours, kHalves };
 
 // Norm and rotation of the lane's 8 values; `table` holds its token's turns,
-// `w` its 8 weights.  Called by whole waves.
-template <int LPV, int ROPE>
-__device__ __forceinline__ void norm_rotate(const Vectors& p, int sub, const float (&w)[8], const f32x2* table,
-                                            float (&v)[8]) {
+// `w` its 8 weights.  LATE: without the norm's factor, which is returned.  Called by
+// whole waves.
+template <int LPV, int ROPE, bool LATE>
+__device__ __forceinline__ float norm_rotate(const Vectors& p, int sub, const float (&w)[8], const f32x2* table,
+                                             float (&v)[8]) {
+  float factor = 1.0f;
   if (!(p.flags & IDX_NORM_OFF)) {
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(v[k], v[k], s);
     s = vector_fold<LPV>(s, [](float a, float b) { return a + b; });
     const float r = inverse_root(s * (1.0f / (8 * LPV)) + p.eps);
+    if constexpr (LATE) factor = r;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = v[k] * r * w[k];
+    for (int k = 0; k < 8; ++k) v[k] = LATE ? v[k] * w[k] : v[k] * r * w[k];
   }
   const int at = 8 * sub - p.first;  // the lane's first value within the rotated part
   const bool in = at >= 0 && at < p.rope;
@@ -140,6 +143,7 @@ __device__ __forceinline__ void norm_rotate(const Vectors& p, int sub, const flo
       v[2 * k + 1] = a * cs.y + b * cs.x;
     }
   }
+  return factor;
 }
 
 template <int LPV>
@@ -179,24 +183,27 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
       const int h = h0 + u * kWaves * kVecs;
       float v[8];
       bf16x8_to_float(raw[u], v);
-      norm_rotate<LPV, ROPE>(p, sub, w, table, v);
+      norm_rotate<LPV, ROPE, false>(p, sub, w, table, v);
       if (h < p.heads)
         put<(STEPS > 1)>(float_to_bf16x8(v), out + ((t * p.heads + h) * kDim + 8 * sub) * 2);
     }
   }
 }
 
-// Scale amax / 448 of a vector and e4m3fn codes of its values / scale, clamped
-// to +-448: both quotients as the float32 division rounds them.  A division
+// Scale amax / 448 of the vector v * factor and e4m3fn codes of its values / scale,
+// clamped to +-448: both quotients as the float32 division rounds them.  The
+// factor is left out of the quotients, which do not depend on it: 8 products and a
+// rounding of every value less.  A division
 // takes some ten instructions and the kernel is bound by them, so each is a
 // product and a correction by its residual (Markstein's), q0 = v*y with y the
 // reciprocal and q = q0 - (scale*q0 - v)*y, which is the correctly rounded
 // quotient away from underflow and overflow, and keeps the sign of a zero; the
-// clamp does nothing then.  Where the scale may leave [2^-60, 2^100], or a value is
-// not a number, the division is taken; a NaN has no part in amax and becomes
-// +-448.
+// clamp does nothing then.  Where the scale may leave [2^-60, 2^100], the factor is
+// far from 1 (or 0, of squares that overflow), or a value is not a number, the
+// values take the factor and the division is taken; a NaN has no part in amax and
+// becomes +-448.
 template <int LPV>
-__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float& scale) {
+__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, float& scale) {
   float m = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = __builtin_elementwise_maximum(m, fabsf(v[k]));  // NaN if one is
@@ -205,7 +212,7 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float& scale) {
   uint32_t top = vector_fold<LPV>(__float_as_uint(m), larger);
   m = top != 0 ? __uint_as_float(top) : 448.0f;
   float q[8];
-  if (__ballot(!(m >= 0x1p-51f && m <= 0x1p108f)) == 0) {
+  if (__ballot(!(m >= 0x1p-51f && m <= 0x1p108f && factor >= 0x1p-60f && factor <= 0x1p60f)) == 0) {
     const float c = 1.0f / 448.0f, s0 = m * c;
     scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
     const float y0 = __builtin_amdgcn_rcpf(scale), y = fmaf(fmaf(-scale, y0, 1.0f), y0, y0);
@@ -214,15 +221,16 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float& scale) {
       const float q0 = v[k] * y;
       q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
     }
+    scale *= top != 0 ? factor : 1.0f;  // (1 for a vector of zeros)
   } else {
     m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k] * factor));
     top = vector_fold<LPV>(__float_as_uint(m), larger);
     m = top != 0 ? __uint_as_float(top) : 448.0f;
     scale = m / 448.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] / scale, -448.0f, 448.0f), v[k]);
+    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] * factor / scale, -448.0f, 448.0f), v[k]);
   }
   u32x2 codes;
 #pragma unroll
@@ -245,7 +253,7 @@ constexpr int kSteps = 2;  // (1 and 4: 28 and 31 us where 2 took 26.5; small ca
 // Unit = kSteps groups of 64/LPV tokens, a wave's; the next unit's vectors are
 // on their way while one is worked on.  A wave has its tokens' turns to itself,
 // so no wave waits for another.  65536 latents to e4m3 take 23 us: 101 MB at
-// 4.4 TB/s, but bound by the vector instructions (174 a token, issuing in nearly
+// 4.4 TB/s, but bound by the vector instructions (some 170 a token, issuing in nearly
 // all of the SIMDs' cycles); to bf16 23 us too, 135 MB at 5.8 TB/s.
 template <int KEY, int LPV, int ROPE, bool FAR>
 __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Pool pool, const int64_t* slots) {
@@ -296,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
     for (int u = 0; u < kSteps; ++u) {
       float v[8];
       bf16x8_to_float(unit.raw[u], v);
-      norm_rotate<LPV, ROPE>(p, sub, w, turns + (u * kVecs + lane / LPV) * pairs, v);
+      const float factor = norm_rotate<LPV, ROPE, KEY == kFp8>(p, sub, w, turns + (u * kVecs + lane / LPV) * pairs, v);
       const int64_t slot = unit.slot[u];
       const bool ok = slot >= 0 && slot < pool.slots;
       const int64_t page = ok ? slot / kPage : 0, i = ok ? slot % kPage : 0;
@@ -304,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
         if (ok) put<FAR>(float_to_bf16x8(v), pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2);
       } else {
         float scale;
-        const u32x2 codes = quantise<LPV>(v, scale);
+        const u32x2 codes = quantise<LPV>(v, factor, scale);
         if (ok) {
           put<FAR>(codes, pool.kv + page * pool.kv_stride + i * kDim + 8 * sub);
           if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;
