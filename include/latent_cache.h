@@ -78,9 +78,13 @@ int idx_norm_rope(const void* x, const float* norm_weight, const int64_t* positi
  *   code_d = e4m3fn(clamp(y_d / scale, -448, 448)), round to nearest even
  *
  * and written to their slots: the quantiser of idx_store_keys_fp8 over
- * head_dim values (with IDX_NORM_OFF and rope_dim 0 the bytes are the same).  A
- * NaN has no part in amax; a quotient that is NaN becomes +-448 with the sign of
- * y_d.
+ * head_dim values (with IDX_NORM_OFF and rope_dim 0 the bytes are the same).  The
+ * norm's factor 1 / sqrt(mean(x^2) + eps), which the quotients do not depend on,
+ * may be applied to the scale instead of the values: scale and quotients are the
+ * formula's but for the order of their float32 roundings, and a code beside a
+ * rounding border may be the other one.  A token's bytes depend on its own
+ * arguments alone, not on the tokens beside it.  A NaN has no part in amax; a
+ * quotient that is NaN becomes +-448 with the sign of y_d.
  * Arguments as idx_norm_rope and idx_store_keys_fp8 except:
  *   head_dim     128 (index keys) or 512 (latents).
  *   kv_page_stride  bytes, >= 64*head_dim, multiple of 16.

@@ -190,6 +190,17 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
   }
 }
 
+// Rounds to the nearest e4m3fn codes, ties to even.
+__device__ __forceinline__ u32x2 float_to_fp8x8(const float (&q)[8]) {
+  u32x2 codes;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
+    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], c, true);
+  }
+  return codes;
+}
+
 // Scale amax / 448 of the vector v * factor and e4m3fn codes of its values / scale,
 // clamped to +-448: both quotients as the float32 division rounds them.  The
 // factor is left out of the quotients, which do not depend on it: 8 products and a
@@ -201,7 +212,8 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
 // clamp does nothing then.  Where the scale may leave [2^-60, 2^100], the factor is
 // far from 1 (or 0, of squares that overflow), or a value is not a number, the
 // values take the factor and the division is taken; a NaN has no part in amax and
-// becomes +-448.
+// becomes +-448.  The two round differently, so each vector has its own choice:
+// that another one of the wave needs the division must not change its bytes.
 template <int LPV>
 __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, float& scale) {
   float m = 0.0f;
@@ -211,32 +223,29 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, flo
   const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
   uint32_t top = vector_fold<LPV>(__float_as_uint(m), larger);
   m = top != 0 ? __uint_as_float(top) : 448.0f;
+  const bool near = m >= 0x1p-51f && m <= 0x1p108f && factor >= 0x1p-60f && factor <= 0x1p60f;
+  const float c = 1.0f / 448.0f, s0 = m * c;
+  scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
+  const float y0 = __builtin_amdgcn_rcpf(scale), y = fmaf(fmaf(-scale, y0, 1.0f), y0, y0);
   float q[8];
-  if (__ballot(!(m >= 0x1p-51f && m <= 0x1p108f && factor >= 0x1p-60f && factor <= 0x1p60f)) == 0) {
-    const float c = 1.0f / 448.0f, s0 = m * c;
-    scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
-    const float y0 = __builtin_amdgcn_rcpf(scale), y = fmaf(fmaf(-scale, y0, 1.0f), y0, y0);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float q0 = v[k] * y;
-      q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
-    }
-    scale *= top != 0 ? factor : 1.0f;  // (1 for a vector of zeros)
-  } else {
+  for (int k = 0; k < 8; ++k) {
+    const float q0 = v[k] * y;
+    q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
+  }
+  u32x2 codes = float_to_fp8x8(q);
+  scale *= top != 0 ? factor : 1.0f;  // (1 for a vector of zeros)
+  if (__ballot(!near) != 0) {
     m = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k] * factor));
     top = vector_fold<LPV>(__float_as_uint(m), larger);
     m = top != 0 ? __uint_as_float(top) : 448.0f;
-    scale = m / 448.0f;
+    const float far = m / 448.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] * factor / scale, -448.0f, 448.0f), v[k]);
-  }
-  u32x2 codes;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
-    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], c, true);
+    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] * factor / far, -448.0f, 448.0f), v[k]);
+    const u32x2 divided = float_to_fp8x8(q);
+    if (!near) scale = far, codes = divided;
   }
   return codes;
 }

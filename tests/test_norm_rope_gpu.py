@@ -317,3 +317,48 @@ def test_plain_store_of_nan_and_inf(lib, n):
     codes, keys = codes[slots.numpy()], keys[slots.numpy()]
     sign = ((x.view(torch.int16).numpy() >> 15) & 1).astype(np.uint8) << 7
     assert np.array_equal(codes[~none], keys[~none]) and np.array_equal(codes[none], (sign | 0x7E)[none])
+
+
+def stored_bytes(lib, x, positions, freq, weight, slots, pages, dim, **opts):
+    """Codes and scales by slot after a store into a pool of zeros."""
+    kv = torch.zeros(pages * PAGE * (dim + 4), dtype=torch.uint8, device="cuda")
+    lib.idx_norm_rope_store_fp8(x, positions, freq, slots, kv, kv.data_ptr() + PAGE * dim, num_pages=pages, weight=weight, **opts)
+    return split_pool(kv, None, pages, dim, True, PAGE * (dim + 4), PAGE * (dim + 4))
+
+
+@pytest.mark.parametrize("dim", [128, 512])
+@pytest.mark.parametrize("neighbours", ["nan", "inf", "zero", "tiny", "huge", "none"])
+@pytest.mark.parametrize("halves", [False, True])
+def test_a_tokens_bytes_are_its_own(lib, dim, neighbours, halves):
+    """What a token is stored as depends on nothing but the token: not on what
+    stands beside it in the batch (padding without a slot included), nor on
+    where the batch ends."""
+    rng = np.random.default_rng(dim + len(neighbours))
+    n, pages, eps = 203, 4, 0.0  # (eps 0: the factor of a zero vector is infinite)
+    x = torch.from_numpy(rng.standard_normal((n, dim)) * np.exp(rng.standard_normal((n, 1)))).to(torch.bfloat16)
+    weight = torch.from_numpy(1 + rng.standard_normal(dim).astype(np.float32) * 0.3).cuda()
+    freq = inv_freq(32).cuda()
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, n))
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n])
+    odd = torch.from_numpy(rng.random(n) < 0.25)
+    odd[:8] = torch.tensor([1, 0, 0, 0, 0, 1, 0, 0]).bool()
+    mixed = x.clone()
+    fill = {"nan": float("nan"), "inf": float("inf"), "zero": 0.0, "tiny": 1e-30, "huge": 3e38}.get(neighbours)
+    if fill is None:
+        odd[:] = False
+    else:
+        mixed[odd] = fill
+    skipped = slots.clone()
+    skipped[odd & torch.from_numpy(rng.random(n) < 0.5)] = -1
+    kept = ~odd
+    call = dict(eps=eps, halves=halves)
+    codes, scales = stored_bytes(lib, mixed.cuda(), positions.cuda(), freq, weight, skipped.cuda(), pages, dim, **call)
+    for t in range(n):  # alone, a call each
+        if kept[t]:
+            one = [v[t: t + 1].cuda() for v in (x, positions, slots)]
+            c, s = stored_bytes(lib, one[0], one[1], freq, weight, one[2], pages, dim, **call)
+            at = int(slots[t])
+            assert s[at] == scales[at] and np.array_equal(c[at], codes[at]), f"token {t}"
+    at = slots[kept].numpy()
+    y, size = norm_rope(x[kept], positions[kept], freq.cpu(), weight.cpu(), eps=eps, halves=halves)
+    assert_near_fp8(codes[at], scales[at], y, size)
