@@ -210,19 +210,20 @@ __device__ __forceinline__ u32x2 float_to_fp8x8(const float (&q)[8]) {
 // reciprocal and q = q0 - (scale*q0 - v)*y, which is the correctly rounded
 // quotient away from underflow and overflow, and keeps the sign of a zero; the
 // clamp does nothing then.  Where the scale may leave [2^-60, 2^100], the factor is
-// far from 1 (or 0, of squares that overflow), or a value is not a number, the
-// values take the factor and the division is taken; a NaN has no part in amax and
-// becomes +-448.  The two round differently, so each vector has its own choice:
-// that another one of the wave needs the division must not change its bytes.
-template <int LPV>
-__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, float& scale) {
+// far from 1 (or 0, of squares that overflow), or a value is not a number or all are
+// zero, `normed` gives the values with the factor in, from the input (without it they may
+// have left float32's range), and the division is taken; a NaN has no part in amax
+// and becomes +-448.  The two round differently, so each vector has its own choice:
+// that another one of the wave needs the division must not change its bytes.  `used`:
+// the lane's vector has a slot, its result matters.
+template <int LPV, class F>
+__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, bool used, float& scale, F normed) {
   float m = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = __builtin_elementwise_maximum(m, fabsf(v[k]));  // NaN if one is
   // (never negative: ordered as its bits are, a NaN above all)
   const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  uint32_t top = vector_fold<LPV>(__float_as_uint(m), larger);
-  m = top != 0 ? __uint_as_float(top) : 448.0f;
+  m = __uint_as_float(vector_fold<LPV>(__float_as_uint(m), larger));
   const bool near = m >= 0x1p-51f && m <= 0x1p108f && factor >= 0x1p-60f && factor <= 0x1p60f;
   const float c = 1.0f / 448.0f, s0 = m * c;
   scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
@@ -234,16 +235,17 @@ __device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, flo
     q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
   }
   u32x2 codes = float_to_fp8x8(q);
-  scale *= top != 0 ? factor : 1.0f;  // (1 for a vector of zeros)
-  if (__ballot(!near) != 0) {
+  scale *= factor;
+  if (__ballot(used && !near) != 0) {
+    float f[8];
+    normed(f);
     m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k] * factor));
-    top = vector_fold<LPV>(__float_as_uint(m), larger);
-    m = top != 0 ? __uint_as_float(top) : 448.0f;
-    const float far = m / 448.0f;
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+    m = __uint_as_float(vector_fold<LPV>(__float_as_uint(m), larger));
+    const float far = m > 0.0f ? m / 448.0f : 1.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(v[k] * factor / far, -448.0f, 448.0f), v[k]);
+    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(f[k] / far, -448.0f, 448.0f), f[k]);
     const u32x2 divided = float_to_fp8x8(q);
     if (!near) scale = far, codes = divided;
   }
@@ -311,9 +313,10 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
     }
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
+      const f32x2* mine = turns + (u * kVecs + lane / LPV) * pairs;
       float v[8];
       bf16x8_to_float(unit.raw[u], v);
-      const float factor = norm_rotate<LPV, ROPE, KEY == kFp8>(p, sub, w, turns + (u * kVecs + lane / LPV) * pairs, v);
+      const float factor = norm_rotate<LPV, ROPE, KEY == kFp8>(p, sub, w, mine, v);
       const int64_t slot = unit.slot[u];
       const bool ok = slot >= 0 && slot < pool.slots;
       const int64_t page = ok ? slot / kPage : 0, i = ok ? slot % kPage : 0;
@@ -321,7 +324,10 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
         if (ok) put<FAR>(float_to_bf16x8(v), pool.kv + page * pool.kv_stride + (i * kDim + 8 * sub) * 2);
       } else {
         float scale;
-        const u32x2 codes = quantise<LPV>(v, factor, scale);
+        const u32x2 codes = quantise<LPV>(v, factor, ok, scale, [&](float (&f)[8]) {
+          bf16x8_to_float(unit.raw[u], f);
+          norm_rotate<LPV, ROPE, false>(p, sub, w, mine, f);
+        });
         if (ok) {
           put<FAR>(codes, pool.kv + page * pool.kv_stride + i * kDim + 8 * sub);
           if (sub == 0) *reinterpret_cast<float*>(pool.ks + page * pool.ks_stride + 4 * i) = scale;

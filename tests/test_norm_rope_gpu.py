@@ -362,3 +362,22 @@ def test_a_tokens_bytes_are_its_own(lib, dim, neighbours, halves):
     at = slots[kept].numpy()
     y, size = norm_rope(x[kept], positions[kept], freq.cpu(), weight.cpu(), eps=eps, halves=halves)
     assert_near_fp8(codes[at], scales[at], y, size)
+
+
+@pytest.mark.parametrize("dim", [128, 512])
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("of_x,of_w", [(2.0 ** 50, 2.0 ** 90), (2.0 ** 50, 2.0 ** 62), (2.0 ** -55, 2.0 ** -90), (2.0 ** -55, 2.0 ** -30), (2.0 ** -59, 2.0 ** -95),
+                                       (2.0 ** -40, 2.0 ** 100), (2.0 ** 40, 2.0 ** -100)])
+def test_store_at_the_ends_of_the_range(lib, dim, halves, of_x, of_w):
+    """x times the weight leaves float32's range, or its normal range, where the
+    normed value times it does not: the stored values are those of the latter."""
+    rng = np.random.default_rng(dim)
+    n, pages = 101, 2
+    # (magnitudes within 2^+-1 of one another: no value leaves the normal range)
+    x = torch.from_numpy(of_x * (1 + rng.random((n, dim))) * rng.choice([-1, 1], (n, dim))).to(torch.bfloat16)
+    weight = torch.from_numpy((of_w * (1 + rng.random(dim))).astype(np.float32))
+    freq, positions = inv_freq(32), torch.from_numpy(rng.integers(0, 1 << 20, n))
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n])
+    codes, scales = stored_bytes(lib, x.cuda(), positions.cuda(), freq.cuda(), weight.cuda(), slots.cuda(), pages, dim, eps=0.0, halves=halves)
+    y, size = norm_rope(x, positions, freq, weight, eps=0.0, halves=halves)
+    assert_near_fp8(codes[slots.numpy()], scales[slots.numpy()], y, size)
