@@ -53,8 +53,10 @@ struct Vectors {
 __device__ __forceinline__ f32x2 turn(int64_t position, float freq) {
   const double angle = (double)position * (double)freq;
   const double whole = rint(angle * 0.63661977236758134308);
-  // (the bounds hold by themselves until nothing is left of the angle, past 2^52)
-  const float x = __builtin_amdgcn_fmed3f((float)fma(angle, 0.63661977236758134308, -whole), -0.5f, 0.5f), xx = x * x;
+  // (the bounds hold by themselves, but for a rounding, until little is left of the
+  // angle; a NaN, which the angle of an infinite frequency is, passes them)
+  const float left = (float)fma(angle, 0.63661977236758134308, -whole);
+  const float x = __builtin_elementwise_maximum(__builtin_elementwise_minimum(left, 0.5f), -0.5f), xx = x * x;
   // the quarter: 1.5 * 2^52 has the integers as its last bits
   const uint32_t quarter = (uint32_t)__builtin_bit_cast(uint64_t, whole + 0x1.8p52);
   const float s = x * fmaf(xx, fmaf(xx, fmaf(xx, -4.60166e-3f, 7.968003e-2f), -0.64596346f), 1.57079632f);

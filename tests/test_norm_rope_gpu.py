@@ -381,3 +381,23 @@ def test_store_at_the_ends_of_the_range(lib, dim, halves, of_x, of_w):
     codes, scales = stored_bytes(lib, x.cuda(), positions.cuda(), freq.cuda(), weight.cuda(), slots.cuda(), pages, dim, eps=0.0, halves=halves)
     y, size = norm_rope(x, positions, freq, weight, eps=0.0, halves=halves)
     assert_near_fp8(codes[slots.numpy()], scales[slots.numpy()], y, size)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+def test_frequencies_that_are_no_numbers(lib, halves):
+    """A frequency that is NaN or infinite has no cos and sin: the values it
+    turns become NaN, and no others.  (Position 0 times infinity is NaN too.)"""
+    rng = np.random.default_rng(22)
+    n, heads, dim = 9, 3, 128
+    x = torch.from_numpy(rng.standard_normal((n, heads, dim))).to(torch.bfloat16)
+    positions = torch.from_numpy(rng.integers(0, 1000, n))
+    positions[2] = 0
+    freq = inv_freq(16)
+    for j, v in ((1, float("nan")), (4, float("inf")), (9, -float("inf"))):
+        freq[j] = v
+    out = torch.empty((n, heads, dim), dtype=torch.bfloat16, device="cuda")
+    lib.idx_norm_rope(x.cuda(), positions.cuda(), freq.cuda(), out, halves=halves)
+    none = torch.zeros(dim, dtype=torch.bool)
+    for j in (1, 4, 9):
+        none[[dim - 32 + j, dim - 16 + j] if halves else [dim - 32 + 2 * j, dim - 31 + 2 * j]] = True
+    assert torch.equal(out.isnan().cpu(), none.expand(n, heads, dim))
