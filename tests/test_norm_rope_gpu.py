@@ -401,3 +401,30 @@ def test_frequencies_that_are_no_numbers(lib, halves):
     for j in (1, 4, 9):
         none[[dim - 32 + j, dim - 16 + j] if halves else [dim - 32 + 2 * j, dim - 31 + 2 * j]] = True
     assert torch.equal(out.isnan().cpu(), none.expand(n, heads, dim))
+
+
+@pytest.mark.parametrize("n,heads,dim,rope,opts", [
+    (2050, 130, 64, 0, {}),
+    (2100, 70, 128, 64, {"halves": True}),
+    (2060, 40, 256, 64, {}),
+    (1400, 33, 512, 64, {"leading": True}),
+    (4200, 1, 128, 64, {"halves": True}),
+    (4200, 3, 512, 48, {}),
+])
+def test_norm_rope_of_many_tokens(lib, n, heads, dim, rope, opts):
+    """Batches that fill the device, with heads that fill a workgroup's steps,
+    or the last of them in part, or few of their places; in place too."""
+    rng = np.random.default_rng(n + heads)
+    weight = torch.from_numpy(1 + rng.standard_normal(dim).astype(np.float32) * 0.3)
+    x = vectors(rng, (n, heads, dim))
+    freq = inv_freq(rope // 2) if rope else None
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, n)) if rope else None
+    xd = x.cuda()
+    out = torch.empty_like(xd)
+    lib.idx_norm_rope(xd, dev(positions), dev(freq), out, weight=dev(weight), **opts)
+    lib.idx_norm_rope(xd, dev(positions), dev(freq), xd, weight=dev(weight), **opts)
+    assert torch.equal(xd.view(torch.int16), out.view(torch.int16))
+    for a in range(0, n, 500):  # (a part at a time: float64 takes four times the room)
+        b = min(n, a + 500)
+        y, size = norm_rope(x[a:b], None if positions is None else positions[a:b], freq, weight, **opts)
+        assert_near_bf16(out[a:b], y, size)
