@@ -467,3 +467,88 @@ def test_indexer_step(lib, fp8):
     chosen = selected.cpu().numpy()
     assert [(c >= 0).sum() for c in chosen] == [256, 256, 256, 256, 100, 0]
     assert_attention(out, lse, attention(aq, values, table.cpu().numpy(), lengths.cpu().numpy(), SCALE, chosen))
+
+
+def repeated(rows, distinct, *tensors):
+    """Rows 0 .. distinct-1 of each tensor, over and over."""
+    at = torch.arange(rows) % distinct
+    return [t[at].contiguous() for t in tensors]
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("heads", [8, 70])
+def test_long_lists_in_one_unit(lib, fp8, heads):
+    """Rows enough that none is split, so that one workgroup goes through all
+    tiles of a list: lists of 8, 9, 12, 13, 16, 17 and 32 tiles, whole and with a
+    part of a tile behind them, with entries to skip and a bad page in the tiles
+    whose places are resolved while the first are used."""
+    rng = np.random.default_rng(21 + heads)
+    rows, width, k, scale = 264, 48, 2048, SCALE
+    counts = [512, 513, 576, 577, 768, 769, 832, 900, 1024, 1030, 1100, 2047, 2048, 2048, 2048, 2048]
+    distinct = len(counts)
+    pages = 60
+    table = np.stack([rng.permutation(pages)[:width] for _ in range(distinct)]).astype(np.int32)
+    lengths = np.array([c if c < k else width * PAGE - 5 for c in counts])
+    selected = np.stack([some(rng, int(L), k, k) for L in lengths])
+    announce(f"long lists fp8={fp8} rows={rows} heads={heads}")
+    for b, c in enumerate(counts):  # skipped: padding, past the row, past the table, before it
+        for tile in (0, 7, 8, 9, 11, 12, (c - 1) // 64):
+            if 64 * tile < c:
+                at = 64 * tile + rng.permutation(min(64, c - 64 * tile))[:4]
+                selected[b, at] = np.array([-1, lengths[b], width * PAGE + 3, -2 ** 31])[: len(at)]
+    selected[12, 8 * 64: 9 * 64] = -1             # a tile with nothing in it
+    selected[13, : 9 * 64] = -1                   # nothing before tile 9
+    selected[14, 31 * 64:] = -1                   # nothing in the last tile
+    bad = {10: 8, 11: 12, 15: 31}                 # one bad page in that tile
+    for b, tile in bad.items():
+        live = [p for p in selected[b, 64 * tile: 64 * tile + 64] if 0 <= p < lengths[b]]
+        page = live[len(live) // 2] // PAGE
+        inside = (selected[b] >= page * PAGE) & (selected[b] < (page + 1) * PAGE)
+        inside[64 * tile: 64 * tile + 64] = False
+        selected[b, inside] = -1                  # only that tile names it
+        table[b, page] = pages + b
+    cache = Cache(rng, pages, fp8)
+    used = set()
+    for b in range(distinct):
+        at = selected[b][: min(k, lengths[b])].astype(np.int64)
+        at = at[(at >= 0) & (at < lengths[b])]
+        page = table[b][at // PAGE]
+        used |= set((page * PAGE + at % PAGE)[page < pages].tolist())
+    cache.poison(used)
+    q = queries(rng, distinct, heads)
+    sinks = torch.from_numpy(rng.standard_normal(heads).astype(np.float32))
+    want = attention(q, np.nan_to_num(cache.values()), table, lengths, scale, selected, sinks)
+    assert [b for b in range(distinct) if np.isnan(want[0][b]).any()] == sorted(bad)
+    assert lib.idx_latent_attention_workspace(rows, heads, width, k) == 0  # unsplit
+    args = repeated(rows, distinct, q, torch.from_numpy(table), torch.from_numpy(selected), torch.from_numpy(lengths.astype(np.int32)))
+    out, lse = call(lib, cache, *args, sinks=sinks)
+    assert_attention(out[:distinct], lse[:distinct], want)
+    # the same rows elsewhere in the batch: the same bits
+    first = torch.arange(rows, device="cuda") % distinct
+    assert torch.equal(out.view(torch.int16), out[first].view(torch.int16))
+    again, logs = call(lib, cache, *args, sinks=sinks)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16)) and torch.equal(logs.view(torch.int32), lse.view(torch.int32))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("scale", [0.3, -0.3, 4.0])
+def test_scores_that_grow_in_one_unit(lib, fp8, scale):
+    """The running maximum moves from tile to tile of one workgroup's, by a few
+    and by hundreds, up and (negative scales) down."""
+    rng = np.random.default_rng(30)
+    rows, heads, width, distinct = 260, 40, 30, 4
+    cache = Cache(rng, 40, fp8)
+    grow = torch.linspace(0.05, 3.0, 40)[:, None]
+    if fp8:
+        cache.scales = cache.scales * grow
+    else:
+        cache.kv = (cache.kv.float() * grow[..., None]).to(torch.bfloat16)
+    table = np.stack([np.sort(rng.permutation(40)[:width]) for _ in range(distinct)]).astype(np.int32)
+    lengths = np.array([1920, 1919, 700, 64])
+    q = queries(rng, distinct, heads, 1.0)
+    assert lib.idx_latent_attention_workspace(rows, heads, width) == 0
+    args = repeated(rows, distinct, q, torch.from_numpy(table), torch.from_numpy(lengths.astype(np.int32)))
+    out, lse = call(lib, cache, args[0], args[1], None, args[2], scale=scale)
+    assert_attention(out[:distinct], lse[:distinct], attention(q, cache.values(), table, lengths, scale))
+    first = torch.arange(rows, device="cuda") % distinct
+    assert torch.equal(out.view(torch.int16), out[first].view(torch.int16))
