@@ -100,18 +100,20 @@ __device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n
 
 // 64 lanes x 16 bytes from `src` (each lane its own) to LDS `dst` + 16 * lane.
 // In assembly so that the compiler, which would wait for every DMA before any
-// LDS read, leaves the order to the explicit waits.
+// LDS read, leaves the order to the explicit waits; m0, which the instruction takes
+// the place from, is an operand, so that the compiler knows what is in it (the
+// s_nop: a state between its write and the DMA).
 __device__ __forceinline__ void dma16(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(dst) : "memory");
 }
 
 // The same of what no other workgroup reads: it is the first to leave the caches.
 __device__ __forceinline__ void dma16_once(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(dst) : "memory");
 }
 
 __device__ __forceinline__ void dma4(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(dst) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "{m0}"(dst) : "memory");
 }
 
 // Waits until at most N vector-memory operations are outstanding.
