@@ -169,7 +169,7 @@ int idx_load_slots_bf16(const void* kv_pages, const int64_t* slots, int64_t n, i
  *              128; rows times blocks of 64 heads at most 8,000,000.
  *   head_dim   must be 512.
  *   table_width >= 0, at most 16,777,216 (page_table may be NULL if it is 0).
- *   k >= -1.   scale finite.
+ *   k >= -1.   scale * log2(e) finite.
  *   workspace  idx_latent_attention_workspace(rows, num_heads, table_width, k)
  *              bytes on the call's device, 16-byte aligned; NULL where that is
  *              0.  It holds nothing between calls, but calls that may run at the

@@ -846,7 +846,7 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
                      int64_t workspace_bytes, hipStream_t stream) {
   if (head_dim != kLatent || num_heads > kMaxHeads) return IDX_ERR_UNSUPPORTED;
   if (!dims_ok(rows, num_heads, table_width, k) || page_table_row_stride < 0 || num_tables < 0 ||
-      !(scale > -INFINITY && scale < INFINITY) || workspace_bytes < 0)
+      !(fabsf(scale * kLog2e) < INFINITY) || workspace_bytes < 0)
     return IDX_ERR_SHAPE;
   int st = validate_pool(KEY, kLatent, num_pages, kv_page_stride, kscale_page_stride);
   if (st != IDX_OK || rows == 0 || num_heads == 0) return st;

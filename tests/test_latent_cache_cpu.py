@@ -236,3 +236,12 @@ def test_attention_size_limits(raw):
         assert b.idx_latent_attention_workspace(rows, heads, 1, 8) == -1
     assert b.idx_latent_attention_workspace(8_000_000, 64, 1, 8) == 0
     assert b.idx_latent_attention_workspace(4_000_000, 65, 1, 8) == 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38])
+def test_attention_scale_in_base_2(raw, scale):
+    """The kernels take the scale times log2(e): one that overflows there would
+    make every row NaN."""
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, scale=scale) == SHAPE
+    assert call(raw, "idx_latent_attention_bf16", ATT16_ORDER, ATT, scale=scale) == SHAPE
+    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, scale=scale / 1.1, rows=0) == OK
