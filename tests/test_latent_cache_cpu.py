@@ -244,4 +244,8 @@ def test_attention_scale_in_base_2(raw, scale):
     make every row NaN."""
     assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, scale=scale) == SHAPE
     assert call(raw, "idx_latent_attention_bf16", ATT16_ORDER, ATT, scale=scale) == SHAPE
-    assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, scale=scale / 1.1, rows=0) == OK
+
+
+def test_attention_scale_below_the_limit(raw):
+    for scale in (2.35e38, -2.35e38):  # (3.4028e38 / 1.4427 = 2.3587e38)
+        assert call(raw, "idx_latent_attention_fp8", ATT8_ORDER, ATT, scale=scale, rows=0) == OK
