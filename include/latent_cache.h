@@ -46,8 +46,10 @@ extern "C" {
  *
  * for the pairs (a, b) of the rope_dim rotated values of y, the rest of y as
  * it is.  Everything in float32 but the angle, whose product and reduction are
- * in float64 (inv_freq's fp32 values taken as exact), and one rounding to bf16
- * at the end.  A negated inv_freq turns a rotation back.
+ * in float64 (inv_freq's fp32 values taken as exact): theta is off by at most
+ * |theta| 2^-51 + 2^-25, and nothing is left of angles from 2^51 on but that the
+ * rotation is one.  One rounding to bf16 at the end.  A negated inv_freq turns a
+ * rotation back; one that is NaN or infinite makes its pairs NaN.
  *
  *   x            bf16, vector h of token t at x + t*x_row_stride + h*head_dim
  *                (elements); 16-byte aligned, x_row_stride a multiple of 8 and

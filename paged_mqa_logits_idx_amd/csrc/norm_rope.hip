@@ -46,10 +46,13 @@ struct Vectors {
 
 // cos and sin of position * frequency.  The product and its reduction to
 // quarters of a turn are float64: at position 2^20 a float32 angle would already
-// be off by 0.03 rad.  What is left, x in [-1/2, 1/2] quarters, is rounded to
-// float32 (2^-26 of a quarter) and goes into polynomials fitted here (least
-// largest error over the interval: sin(pi/2 x) / x to 2^-28 of itself,
-// cos(pi/2 x) to 2^-34), about half of the instructions of a library's pair.
+// be off by 0.03 rad.  (2 / pi as a double and the product's rounding leave
+// |angle| 2^-51 rad of error: 10^-6 at 2^31.)  What is left, x in [-1/2, 1/2]
+// quarters, is rounded to float32 (2^-26 of a quarter) and goes into polynomials
+// fitted here for the least largest error over the interval.  With their float32
+// coefficients they are off by 2^-25.0 (sin) and 2^-27.1 (cos), in float32
+// arithmetic by 2^-23.4 and 2^-24.0; about half of the instructions of a library's
+// pair.
 __device__ __forceinline__ f32x2 turn(int64_t position, float freq) {
   const double angle = (double)position * (double)freq;
   const double whole = rint(angle * 0.63661977236758134308);

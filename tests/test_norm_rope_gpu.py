@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from latent_reference import PAGE, assert_near_bf16, assert_near_fp8, e4m3_values, f64, inv_freq, norm_rope, vectors
+from latent_reference import F32, PAGE, assert_near_bf16, assert_near_fp8, e4m3_values, f64, inv_freq, norm_rope, vectors
 
 pytestmark = pytest.mark.gpu
 
@@ -428,3 +428,25 @@ def test_norm_rope_of_many_tokens(lib, n, heads, dim, rope, opts):
         b = min(n, a + 500)
         y, size = norm_rope(x[a:b], None if positions is None else positions[a:b], freq, weight, **opts)
         assert_near_bf16(out[a:b], y, size)
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("power", [20, 31, 36, 40, 43])
+def test_far_positions_keep_what_float64_leaves(lib, halves, power):
+    """The angle is off by |theta| 2^-51 + 2^-25 at most (its product and its
+    reduction by float64's 2 / pi, each within 2^-53 of itself or so, and the
+    fraction of a quarter turn rounded to float32): values are off by as much of
+    their pair's length, besides the roundings of any position."""
+    rng = np.random.default_rng(power)
+    n, dim = 200, 64
+    positions = torch.from_numpy(rng.integers(1 << (power - 1), 1 << power, n) * rng.choice([-1, 1], n))
+    freq = torch.cat([torch.tensor([1.0, 0.5]), torch.from_numpy(rng.random(30).astype(np.float32))])
+    x = torch.from_numpy(rng.standard_normal((n, 1, dim))).to(torch.bfloat16)
+    out = torch.empty((n, 1, dim), dtype=torch.bfloat16, device="cuda")
+    lib.idx_norm_rope(x.cuda(), positions.cuda(), freq.cuda(), out, norm=False, halves=halves)
+    y, size = norm_rope(x, positions, freq, norm=False, halves=halves)
+    theta = np.abs(f64(positions))[:, None] * f64(freq)
+    off = theta * 2.0 ** -51 + 2.0 ** -25
+    off = np.concatenate([off, off], -1) if halves else np.repeat(off, 2, -1)
+    # (assert_near_bf16 takes F32 of `size`)
+    assert_near_bf16(out, y, size * (1 + off[:, None] / F32))
