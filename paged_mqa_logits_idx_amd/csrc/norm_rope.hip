@@ -330,7 +330,9 @@ __global__ __launch_bounds__(kThreads) void norm_rope_store_kernel(Vectors p, Po
       } else {
         float scale;
         const u32x2 codes = quantise<LPV>(v, factor, ok, scale, [&](float (&f)[8]) {
-          bf16x8_to_float(unit.raw[u], f);
+          u32x4 raw = unit.raw[u];
+          asm volatile("" : "+v"(raw));  // (or the values of every token are kept for here: 8 moves)
+          bf16x8_to_float(raw, f);
           norm_rotate<LPV, ROPE, false>(p, sub, w, mine, f);
         });
         if (ok) {
