@@ -28,17 +28,25 @@
 // scores whose errors the exponential passes on in full.
 //
 // A row is split where its units are fewer than the CUs; the splits leave sums
-// and outputs in float32, which a second kernel joins.
+// and outputs in float32, which a second kernel joins.  All rows are split alike,
+// by the table's width: a batch of several lengths takes as long as its longest row
+// (16 rows of 2432 to 8192 positions: 16 tiles for the longest row's units, 10.4 on
+// average), and units that no whole number of splits spreads over the CUs leave
+// some idle (64 heads over 2048 positions: 128 rows 64 us, 129 rows 71, 256 rows
+// 98, 257 rows 151).
 //
 // What bounds it.  Many rows: 4096 of 64 heads over 2048 of 5632 positions take
-// 0.90 ms, 1.0 PFLOP/s (a library product of 8192^3 1.18).  Of the SIMDs' cycles
-// the matrix units have 45 %, vector instructions issue in 46 % (173 a wave and
-// tile, 96 of them the widening's, which take 7.5 clocks, not 4), the LDS has 26 %
-// of its own; taking away any one part shortens a tile by a tenth at most.  A
-// unit's start and end take 9 us of 55.  Few rows: 64 of 64 heads over 2048 of
-// 32768 positions take 39 us, of which 8 the joining: 107 MB are read and 34
-// written (the splits' outputs) in 31 us, then 35 read; one row takes 14.5, three
-// loads in a row (list, page id, latent), two tiles and two launches.
+// 0.90 to 0.95 ms (the cards differ), 0.95 to 1.0 PFLOP/s (a library product of
+// 8192^3 1.18).  Of the SIMDs' cycles the matrix units have 45 %, vector
+// instructions issue in 46 % (173 a wave and tile, 96 of them the widening's, which
+// take 7.5 clocks, not 4), the LDS has 26 % of its own; taking away any one part
+// shortens a tile by a seventh at most.  A unit's start and end take 10 us of 59:
+// lists of 64 positions 86 us for 2048 rows, of 512 180, of 2048 450 to 480.  Heads
+// are multiplied in blocks of 64, whatever their number: 8 heads take 0.80 ms, 72
+// heads 1.74.  Few rows: 64 of 64 heads over 2048 of 32768 positions take 39 us, of
+// which 8 the joining: 107 MB are read and 34 written (the splits' outputs) in 31
+// us, then 35 read; one row takes 14.5, three loads in a row (list, page id,
+// latent), two tiles and two launches.
 //
 // Running maximum: all waves agree on a reference m_h for each head.  It
 // moves, and the sums are rescaled, only when the probabilities that a lane has of
@@ -47,7 +55,7 @@
 //
 // Rounding: scores, exponentials, sums and outputs are float32; the products
 // take bf16 operands, which rounds the probability (times the e4m3 scale) once,
-// by 2^-9 of itself at most, independently from position to position.  The
+// by 2^-8 of itself at most, independently from position to position.  The
 // denominator sums the unrounded probabilities.
 #include <type_traits>
 
@@ -242,7 +250,7 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       }
     };
     // An unsplit row's queries are read once: 1 to 3 % of a prefill; read like that
-    // by several splits, 33 rows took 22.8 us, not 21.4.
+    // by several splits, 33 rows take 22.5 us, not 21.4.
     if (splits > 1) ask([](const uint8_t* src, uint32_t dst) { dma16(src, dst); });
     else ask([](const uint8_t* src, uint32_t dst) { dma16_once(src, dst); });
   }
@@ -661,7 +669,8 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
       // Two buffers: a tile is scored and added up while the next is on its way.
       // Its gather is spread over the scores, and the first latents of the outputs
       // are read before the probabilities are there (2048 rows of 64 heads over 2048
-      // positions took 606 us without, 592 with the second, 568 with both).
+      // positions, 480 to 510 us now, took 606 us without, 592 with the second, 568
+      // with both when these came).
       for (int32_t j = 0; j < mine; ++j) {
         wait_vm<0>();
         barrier();  // tile j is there; every wave is done with tile j - 1
@@ -716,7 +725,8 @@ __global__ __launch_bounds__(Shape<KEY>::kThreads, 2) void latent_attention_kern
   }
   // The outputs of all waves as rows in the tile buffers, so that they leave in
   // whole lines; past the caches, where the latents stay (2048 rows of 64 heads over
-  // 512 and 2048 positions: 190 and 465 us, so 179 and 458).
+  // 512 and 2048 positions 180 and 482 us, with ordinary stores 185 and 485; 4096
+  // rows 948 and 964).
   uint8_t* rows = &sh.tile[0][0];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
@@ -812,9 +822,8 @@ constexpr int64_t kMaxUnits = 8000000;  // a launch has less than 2^32 threads
 // on the device): a unit takes about 2.2 us a tile, and joining s splits about
 // 2.2 * s / 8 more, so up to sqrt(8 * tiles), all of the same number of tiles,
 // while every unit has a CU of its own.  One row of 64 heads over 8, 16, 32 and
-// 4096 tiles took 13.4, 14.9, 16.5 and 88 us when this was chosen; with a tile a
-// split, or at most 256 splits, 13.4, 15.0, 17.8 and 86; the first two unsplit 23
-// and 38.
+// 4097 tiles takes 12.1, 13.4, 14.6 and 74 us; with a tile a split, at most 256
+// splits, 12.1, 13.1, 15.6 and 75; the first three unsplit 20, 34 and 61.
 int splits_of(int32_t rows, int32_t num_heads, int32_t table_width, int32_t k) {
   const int64_t most = k >= 0 ? (k < (int64_t)table_width * kPage ? k : (int64_t)table_width * kPage)
                                 : (int64_t)table_width * kPage;
@@ -890,9 +899,10 @@ int latent_attention(const void* q, const void* kv_pages, const float* kscale, c
   latent_attention_kernel<KEY><<<dim3((uint32_t)(8 * groups)), dim3(Shape<KEY>::kThreads), 0, stream>>>(a);
   if (a.splits > 1) {
     const dim3 grid(kLatent / 32, (uint32_t)((num_heads + 7) / 8), (uint32_t)rows);  // (at most a row a CU)
-    // A batch no larger than the splits: 4 of them take 8.0 us where the kernel
-    // for 16, with its registers, takes 12 (64 rows of 64 heads), and 16 take 4.0
-    // us at once and 7.4 with four under way at a time (one row).
+    // A batch no larger than the splits: the kernel for 16 has registers for fewer
+    // waves (64 rows of 64 heads, 4 splits: 40 us with the attention itself, 43 by
+    // the kernel for 16), and a kernel for 4 makes more trips (one row of 16 splits
+    // 14.5 and 15.2, of 179 splits 74 and 84).
     if (a.splits <= 4)
       latent_combine_kernel<4><<<grid, dim3(64), 0, stream>>>(a);
     else if (a.splits <= 8)

@@ -19,8 +19,9 @@ constexpr int kWaves = kThreads / 64;
 
 // Outputs of a call that writes 16 MiB or more pass the caches by: the inputs
 // keep their place, and the next kernel would not find them there whole.  65536
-// latents stored 26.7 -> 23.0 us, stored and read back 53.1 -> 48.6; but 16384
-// stored and read back 16.6 -> 17.2.
+// latents stored 23.1 us, 26 by ordinary stores, stored and read back 48.2 and 53.2;
+// but 16384 stored 8.7 and 9.5, stored and read back 16.6 and 16.2, and 32768 26.3
+// and 25.8.
 inline bool is_far(int64_t n, int64_t bytes) { return n >= (((int64_t)1 << 24) + bytes - 1) / bytes; }
 
 template <bool FAR, class T>
@@ -158,8 +159,8 @@ __device__ __forceinline__ void load_weight(const Vectors& p, int sub, float (&w
 }
 
 // Unit = one token x `STEPS` groups of kWaves * 64/LPV heads, which share the
-// token's turns.  Bound by memory: 4096 tokens of 64 heads of 512 take 92 us, 537
-// MB at 5.8 TB/s.
+// token's turns.  Bound by memory: 4096 tokens of 64 heads of 512 take 90 to 93 us,
+// 537 MB at 5.8 to 6.0 TB/s (of a bare copy as large 97).
 template <int LPV, int ROPE, int STEPS>
 __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t* out, int32_t groups) {
   extern __shared__ f32x2 table[];
@@ -264,11 +265,11 @@ struct Pool {
   int64_t kv_stride, ks_stride;
 };
 
-constexpr int kSteps = 2;  // (1 and 4: 28 and 31 us where 2 took 26.5; small calls take the same)
+constexpr int kSteps = 2;  // (65536 latents: 24.2 us, 24.6 with 1 and 23.4 with 4; 16384: 9.5, 9.5 and 10.6)
 
 // Unit = kSteps groups of 64/LPV tokens, a wave's; the next unit's vectors are
 // on their way while one is worked on.  A wave has its tokens' turns to itself,
-// so no wave waits for another.  65536 latents to e4m3 take 23 us: 101 MB at
+// so no wave waits for another.  65536 latents to e4m3 take 23 us: 102 MB at
 // 4.4 TB/s, but bound by the vector instructions (some 170 a token, issuing in nearly
 // all of the SIMDs' cycles); to bf16 23 us too, 135 MB at 5.8 TB/s.
 template <int KEY, int LPV, int ROPE, bool FAR>
@@ -458,7 +459,8 @@ void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
     constexpr int kRope = decltype(rope)::value;
     // four steps, and past the caches, where a token's heads fill them and the units
     // the device (more than 32 MiB then): 93 us, 96 with ordinary stores, 106 in one
-    // step (4096 tokens of 64 heads of 512), 30 and 31 (4096 of 17 of 512); but 11.2
+    // step (4096 tokens of 64 heads of 512; with a kernel that reads all of it next
+    // 194, 185 and 195), 30 and 31 (4096 of 17 of 512); but 11.2
     // and, in one step, 10.1 (1024 of 64 of 128, 1024 units), and with fewer heads
     // 10.2 and 6.4 (4096 of one of 128), 104 and 59 (65536 of one of 512)
     if (p.heads >= 4 * kOne && p.n * groups >= 16 * device_cu_count())
@@ -472,8 +474,8 @@ template <int KEY, int LPV>
 void launch_store(const Vectors& p, const Pool& pool, const int64_t* slots, hipStream_t stream) {
   constexpr int kTokens = kSteps * kWaves * (64 / LPV);
   const size_t lds = (size_t)(p.rope / 2) * sizeof(f32x2) * kTokens;
-  // a grid of 16 blocks a CU goes round, with the next loads under way: 26.5 us
-  // where 8 a CU took 28.5 (65536 latents)
+  // a grid of 16 blocks a CU goes round, with the next loads under way (65536
+  // latents to e4m3 and bf16: 24.2 and 23.3 us, 24.0 and 23.7 with 8 a CU)
   const int64_t units = (p.n + kTokens - 1) / kTokens, most = 16 * device_cu_count();
   const dim3 grid((uint32_t)(units < most ? units : most));
   for_rotation(p, [&](auto rope) {
@@ -514,9 +516,9 @@ void launch_load(const Pool& pool, const int64_t* slots, int64_t n, void* out, i
   constexpr int kOne = kWaves * (64 / LPV);
   uint8_t* o = static_cast<uint8_t*>(out);
   const dim3 ones = grid_of((n + kOne - 1) / kOne);
-  // past the caches: 78 us, 86 with ordinary stores (262208 latents from e4m3);
-  // four steps of e4m3 then, 88 us in one, but bf16 moves as much in one: 77 and 73
-  // us (196608)
+  // past the caches: 78 us, 96 with ordinary stores (262208 latents from e4m3);
+  // four steps of e4m3 then, 87 us in one, but bf16 moves as much in one: 73 us, 77
+  // in four (196608)
   if (!is_far(n, 16 * LPV))
     load_slots_kernel<KEY, LPV, 1, false><<<ones, dim3(kThreads), 0, stream>>>(pool, slots, n, o, 2 * out_row_stride);
   else if constexpr (KEY == kBf16)
