@@ -552,3 +552,42 @@ def test_scores_that_grow_in_one_unit(lib, fp8, scale):
     assert_attention(out[:distinct], lse[:distinct], attention(q, cache.values(), table, lengths, scale))
     first = torch.arange(rows, device="cuda") % distinct
     assert torch.equal(out.view(torch.int16), out[first].view(torch.int16))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("rows", [4, 270])
+def test_no_numbers_stay_where_they_are(lib, fp8, rows):
+    """A query that holds a NaN or infinities of both signs makes its own head
+    NaN, a latent that holds a NaN the rows that select it, a sink that is NaN its
+    head; the other heads and rows have the bits that they have without."""
+    rng = np.random.default_rng(31)
+    heads, width, distinct, k = 40, 12, 4, 400
+    cache = Cache(rng, 30, fp8)
+    table = np.stack([rng.permutation(28)[:width] for _ in range(distinct)]).astype(np.int32)
+    table[2, 5] = 28  # a page of row 2's alone
+    lengths = np.array([768, 700, 768, 65])
+    selected = np.stack([some(rng, int(n), k, k) for n in lengths])
+    inside = np.flatnonzero(selected[2] // PAGE == 5)[0]
+    q = queries(rng, distinct, heads)
+    sinks = torch.from_numpy(rng.standard_normal(heads).astype(np.float32))
+    args = lambda q: repeated(rows, distinct, q, torch.from_numpy(table), torch.from_numpy(selected), torch.from_numpy(lengths.astype(np.int32)))  # noqa: E731
+    plain, plain_lse = call(lib, cache, *args(q), sinks=sinks)
+    bad = q.clone()
+    bad[0, 3, 100] = float("nan")
+    bad[1, 35] = torch.where(torch.arange(LATENT) % 2 == 0, float("inf"), -float("inf")).to(torch.bfloat16)
+    slot = int(selected[2][inside]) % PAGE
+    if fp8:
+        cache.kv[28, slot, 77] = 0xFF
+    else:
+        cache.kv[28, slot, 77] = float("nan")
+    odd = sinks.clone()
+    odd[7] = float("nan")
+    out, lse = call(lib, cache, *args(bad), sinks=odd)
+    none = torch.zeros((distinct, heads), dtype=torch.bool)
+    none[0, 3] = none[1, 35] = True
+    none[2] = True
+    none[:, 7] = True
+    none = none[torch.arange(rows) % distinct].cuda()
+    assert out[none].isnan().all() and lse[none].isnan().all()
+    assert torch.equal(out[~none].view(torch.int16), plain[~none].view(torch.int16))
+    assert torch.equal(lse[~none].view(torch.int32), plain_lse[~none].view(torch.int32))
