@@ -457,13 +457,15 @@ void launch_norm_rope(const Vectors& p, void* out, hipStream_t stream) {
   uint8_t* to = static_cast<uint8_t*>(out);
   for_rotation(p, [&](auto rope) {
     constexpr int kRope = decltype(rope)::value;
-    // four steps, and past the caches, where a token's heads fill them and the units
-    // the device (more than 32 MiB then): 93 us, 96 with ordinary stores, 106 in one
-    // step (4096 tokens of 64 heads of 512; with a kernel that reads all of it next
-    // 194, 185 and 195), 30 and 31 (4096 of 17 of 512); but 11.2
-    // and, in one step, 10.1 (1024 of 64 of 128, 1024 units), and with fewer heads
-    // 10.2 and 6.4 (4096 of one of 128), 104 and 59 (65536 of one of 512)
-    if (p.heads >= 4 * kOne && p.n * groups >= 16 * device_cu_count())
+    // four steps, and past the caches, where a token's heads are more than one step
+    // has places for and the units fill the device (more than 16 MiB then).  128 MiB:
+    // 2048 tokens of 64 heads of 512 49 us, 53 in one step, 26214 of 5 65 and 71,
+    // 30840 of 17 of 128 68 and 79; but 32768 of 4 of 512 74 and 54, 131072 of one 226
+    // and 137, and 4096 of one of 128 10 and 6.4; 1024 of 64 of 128, 1024 units, 11.2
+    // and 10.1.  Ordinary stores instead: 4096 of 64 of 512 93 -> 96, 2048 of 40 28 ->
+    // 35, 2048 of 64 49 -> 47, but with a kernel that reads all of it next 194 -> 185,
+    // 60 -> 59 and 98 -> 87.
+    if (p.heads > kOne && p.n * groups >= 16 * device_cu_count())
       norm_rope_kernel<LPV, kRope, 4><<<grid_of(p.n * groups), dim3(kThreads), lds, stream>>>(p, to, groups);
     else
       norm_rope_kernel<LPV, kRope, 1><<<grid_of(p.n * single), dim3(kThreads), lds, stream>>>(p, to, single);

@@ -410,6 +410,7 @@ def test_frequencies_that_are_no_numbers(lib, halves):
     (1400, 33, 512, 64, {"leading": True}),
     (4200, 1, 128, 64, {"halves": True}),
     (4200, 3, 512, 48, {}),
+    (4200, 5, 512, 48, {}),
 ])
 def test_norm_rope_of_many_tokens(lib, n, heads, dim, rope, opts):
     """Batches that fill the device, with heads that fill a workgroup's steps,
