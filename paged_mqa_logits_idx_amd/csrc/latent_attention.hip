@@ -65,16 +65,10 @@ namespace {
 
 constexpr float kLimit = 256.0f;    // what a lane's 8 probabilities may add up to; one is above 2^kLazy then
 constexpr float kLazy = 5.0f;       // base-2 logits that a maximum exceeds its reference by where it moves
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxHeads = 128;
 constexpr int kHeadTile = 64;       // heads of a unit
 constexpr int kTile = 64;           // positions of a tile
 constexpr int kPartials = kHeadTile * kLatent;  // float32 outputs of a unit
-
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef int v2i __attribute__((ext_vector_type(2)));
-typedef short v4s __attribute__((ext_vector_type(4)));
 
 // A position that is masked, or (16 bytes on) whose page id lies outside the pool,
 // is gathered from here: it must not bring values of its own into the products.
@@ -100,36 +94,6 @@ struct Attend {
   float scale2;        // scale * log2(e)
 };
 
-__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
-
-// The workgroup's waves meet here; their LDS writes before it are visible
-// after it.  Memory operations other than LDS ones stay in flight.
-__device__ __forceinline__ void barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// 64 lanes x 16 bytes from `src` (each lane its own) to LDS `dst` + 16 * lane.
-// In assembly so that the compiler, which would wait for every DMA before any
-// LDS read, leaves the order to the explicit waits; m0, which the instruction takes
-// the place from, is an operand, so that the compiler knows what is in it (the
-// s_nop: a state between its write and the DMA).
-__device__ __forceinline__ void dma16(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(dst) : "memory");
-}
-
-// The same of what no other workgroup reads: it is the first to leave the caches.
-__device__ __forceinline__ void dma16_once(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(src), "{m0}"(dst) : "memory");
-}
-
-__device__ __forceinline__ void dma4(const uint8_t* src, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "{m0}"(dst) : "memory");
-}
-
-// Waits until at most N vector-memory operations are outstanding.
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Where chunk c (16 bytes) of position r stands within the position's LDS row:
 // rows of a multiple of 256 bytes would put one chunk of all positions into the
 // same banks.  Any 16 positions in a row take 16 places.  The transposing reads
@@ -138,23 +102,6 @@ __device__ __forceinline__ void wait_vm() {
 template <int KEY>
 __device__ __forceinline__ constexpr int swizzle(int c, int r) {
   return c ^ (KEY == kFp8 ? (r & 3) << 1 | (r & 8) | (r >> 2 & 1) : (r & 3) << 2 | (r >> 2 & 3));
-}
-
-// The end of a softmax: sums relative to 2^m become outputs (times by * half *
-// half) and the log of the denominator, in which a sink's base-2 logit joins.
-// 2^(m - ref) is applied in two halves: it may be far below float32's range
-// where the sink is far above the scores, and the outputs not yet.
-struct Closing {
-  float by, half, lse;
-};
-__device__ __forceinline__ Closing close_sum(float m, float z, float sink) {
-  const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
-  Closing c;
-  c.half = __builtin_amdgcn_exp2f(0.5f * (m - ref));
-  const float total = z * c.half * c.half + __builtin_amdgcn_exp2f(sink - ref);
-  c.by = total == 0.0f ? 0.0f : 1.0f / total;
-  c.lse = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
-  return c;
 }
 
 // A unit's tile: 64 positions x 64 heads, four 32 x 32 blocks of scores.  Eight

@@ -17,19 +17,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
-// Outputs of a call that writes 16 MiB or more pass the caches by: the inputs
-// keep their place, and the next kernel would not find them there whole.  65536
-// latents stored 23.1 us, 26 by ordinary stores, stored and read back 48.2 and 53.2;
-// but 16384 stored 8.7 and 9.5, stored and read back 16.6 and 16.2, and 32768 26.3
-// and 25.8.
-inline bool is_far(int64_t n, int64_t bytes) { return n >= (((int64_t)1 << 24) + bytes - 1) / bytes; }
-
-template <bool FAR, class T>
-__device__ __forceinline__ void put(T v, uint8_t* to) {
-  if constexpr (FAR) __builtin_nontemporal_store(v, reinterpret_cast<T*>(to));
-  else *reinterpret_cast<T*>(to) = v;
-}
-
 struct Vectors {
   const uint8_t* x;      // bf16
   const float* weight;   // [D] or NULL
@@ -68,34 +55,6 @@ __device__ __forceinline__ f32x2 turn(int64_t position, float freq) {
   const float a = quarter & 1 ? c : s, b = quarter & 1 ? s : c;
   return (f32x2){__uint_as_float(__float_as_uint(b) ^ (quarter + 1) << 30 & 0x80000000u),
                  __uint_as_float(__float_as_uint(a) ^ quarter << 30 & 0x80000000u)};
-}
-
-// The lane's value of another lane of its row of 16.
-template <int CTRL, class T>
-__device__ __forceinline__ T row_lane(T v) {
-  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-
-// f over the LPV lanes of a vector, in all of them: neighbours, pairs of a
-// quad, mirrored halves of a row and rows as operands of the arithmetic itself
-// (shuffles go through LDS), then rows and halves of the wave.
-template <int LPV, class T, class F>
-__device__ __forceinline__ T vector_fold(T v, F f) {
-  v = f(v, row_lane<0xb1>(v));   // quad_perm 1 0 3 2
-  v = f(v, row_lane<0x4e>(v));   // quad_perm 2 3 0 1
-  v = f(v, row_lane<0x141>(v));  // row_half_mirror
-  if constexpr (LPV > 8) v = f(v, row_lane<0x140>(v));  // row_mirror
-  if constexpr (LPV > 16) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    v = f(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
-  }
-  if constexpr (LPV > 32) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    v = f(__builtin_bit_cast(T, (uint32_t)r[0]), __builtin_bit_cast(T, (uint32_t)r[1]));
-  }
-  return v;
 }
 
 // 1 / sqrt(v) to 2^-23 of itself; the instruction takes no denormals.
@@ -194,68 +153,6 @@ __global__ __launch_bounds__(kThreads) void norm_rope_kernel(Vectors p, uint8_t*
         put<(STEPS > 1)>(float_to_bf16x8(v), out + ((t * p.heads + h) * kDim + 8 * sub) * 2);
     }
   }
-}
-
-// Rounds to the nearest e4m3fn codes, ties to even.
-__device__ __forceinline__ u32x2 float_to_fp8x8(const float (&q)[8]) {
-  u32x2 codes;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
-    codes[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], c, true);
-  }
-  return codes;
-}
-
-// Scale amax / 448 of the vector v * factor and e4m3fn codes of its values / scale,
-// clamped to +-448: both quotients as the float32 division rounds them.  The
-// factor is left out of the quotients, which do not depend on it: 8 products and a
-// rounding of every value less.  A division
-// takes some ten instructions and the kernel is bound by them, so each is a
-// product and a correction by its residual (Markstein's), q0 = v*y with y the
-// reciprocal and q = q0 - (scale*q0 - v)*y, which is the correctly rounded
-// quotient away from underflow and overflow, and keeps the sign of a zero; the
-// clamp does nothing then.  Where the scale may leave [2^-60, 2^100], the factor is
-// far from 1 (or 0, of squares that overflow), or a value is not a number or all are
-// zero, `normed` gives the values with the factor in, from the input (without it they may
-// have left float32's range), and the division is taken; a NaN has no part in amax
-// and becomes +-448.  The two round differently, so each vector has its own choice:
-// that another one of the wave needs the division must not change its bytes.  `used`:
-// the lane's vector has a slot, its result matters.
-template <int LPV, class F>
-__device__ __forceinline__ u32x2 quantise(const float (&v)[8], float factor, bool used, float& scale, F normed) {
-  float m = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m = __builtin_elementwise_maximum(m, fabsf(v[k]));  // NaN if one is
-  // (never negative: ordered as its bits are, a NaN above all)
-  const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  m = __uint_as_float(vector_fold<LPV>(__float_as_uint(m), larger));
-  const bool near = m >= 0x1p-51f && m <= 0x1p108f && factor >= 0x1p-60f && factor <= 0x1p60f;
-  const float c = 1.0f / 448.0f, s0 = m * c;
-  scale = fmaf(fmaf(-448.0f, s0, m), c, s0);
-  const float y0 = __builtin_amdgcn_rcpf(scale), y = fmaf(fmaf(-scale, y0, 1.0f), y0, y0);
-  float q[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float q0 = v[k] * y;
-    q[k] = fmaf(-fmaf(scale, q0, -v[k]), y, q0);
-  }
-  u32x2 codes = float_to_fp8x8(q);
-  scale *= factor;
-  if (__ballot(used && !near) != 0) {
-    float f[8];
-    normed(f);
-    m = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
-    m = __uint_as_float(vector_fold<LPV>(__float_as_uint(m), larger));
-    const float far = m > 0.0f ? m / 448.0f : 1.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) q[k] = copysignf(__builtin_amdgcn_fmed3f(f[k] / far, -448.0f, 448.0f), f[k]);
-    const u32x2 divided = float_to_fp8x8(q);
-    if (!near) scale = far, codes = divided;
-  }
-  return codes;
 }
 
 struct Pool {
