@@ -55,6 +55,15 @@ _SYMBOLS = (
     "idx_latent_attention_fp8",
     "idx_latent_attention_bf16",
     "idx_latent_attention_workspace",
+    "idx_plan_batch",
+    "idx_store_kv_fp8",
+    "idx_store_kv_bf16",
+    "idx_page_bounds_fp8",
+    "idx_page_bounds_bf16",
+    "idx_page_scores",
+    "idx_kv_attention_fp8",
+    "idx_kv_attention_bf16",
+    "idx_kv_attention_workspace",
     "idx_status_string",
     "idx_abi_version",
 )
@@ -115,12 +124,24 @@ def _load() -> ctypes.CDLL:
             ("idx_latent_attention_fp8", [ptr] * 5 + [i32] + [ptr] * 5 + [i32] * 4 + [i64] * 4
              + [i32, ctypes.c_float, ptr, i64, ptr]),
             ("idx_latent_attention_bf16", [ptr] * 4 + [i32] + [ptr] * 5 + [i32] * 4 + [i64] * 3
+             + [i32, ctypes.c_float, ptr, i64, ptr]),
+            ("idx_plan_batch", [ptr, ptr, i32, ptr, i64, ptr, i32, i64, i64] + [ptr] * 7),
+            ("idx_store_kv_fp8", [ptr] * 3 + [i64, i32, i32, i64, i64] + [ptr] * 4 + [i64] * 5 + [ptr]),
+            ("idx_store_kv_bf16", [ptr] * 3 + [i64, i32, i32, i64, i64] + [ptr] * 2 + [i64] * 3 + [ptr]),
+            ("idx_page_bounds_fp8", [ptr] * 4 + [i32] + [ptr] * 3 + [i32] * 4 + [i64] * 6 + [ptr]),
+            ("idx_page_bounds_bf16", [ptr] * 3 + [i32] + [ptr] * 3 + [i32] * 4 + [i64] * 4 + [ptr]),
+            ("idx_page_scores", [ptr] * 4 + [i32] + [ptr] * 3 + [i32] * 5 + [i64] * 3 + [i32, i32, ptr]),
+            ("idx_kv_attention_fp8", [ptr] * 7 + [i32] + [ptr] * 5 + [i32] * 5 + [i64] * 6
+             + [i32, ctypes.c_float, ptr, i64, ptr]),
+            ("idx_kv_attention_bf16", [ptr] * 5 + [i32] + [ptr] * 5 + [i32] * 5 + [i64] * 4
              + [i32, ctypes.c_float, ptr, i64, ptr])):
         fn = getattr(lib, name)
         fn.argtypes = types
         fn.restype = ctypes.c_int
     lib.idx_latent_attention_workspace.argtypes = [i32] * 4
     lib.idx_latent_attention_workspace.restype = i64
+    lib.idx_kv_attention_workspace.argtypes = [i32] * 6
+    lib.idx_kv_attention_workspace.restype = i64
     lib.idx_status_string.argtypes = [ctypes.c_int]
     lib.idx_status_string.restype = ctypes.c_char_p
     lib.idx_abi_version.argtypes = []
@@ -624,14 +645,15 @@ def idx_latent_attention_workspace(rows, num_heads, table_width, k=None) -> int:
     return _lib.idx_latent_attention_workspace(rows, num_heads, table_width, -1 if k is None else k)
 
 
-def _latent_workspace(rows, heads, width, k, dev, stream) -> torch.Tensor | None:
-    """A workspace from torch's allocator, on the call's device and stream."""
+def _workspace(size, dims, dev, stream) -> torch.Tensor | None:
+    """A workspace of ``size(*dims)`` bytes from torch's allocator, on the call's
+    device and stream."""
     if dev < 0:
         return None
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _latent_workspace(rows, heads, width, k, dev, stream)
-    need = idx_latent_attention_workspace(rows, heads, width, k)
+            return _workspace(size, dims, dev, stream)
+    need = size(*dims)
     if need <= 0:
         return None
     if stream is None:
@@ -683,7 +705,7 @@ def _latent_attention(fn, q, kv_pages, kscale, page_table, topk_idx, seqlens, ou
     kv, *ks = _pool(kv_pages, kscale[0] if kscale else None, num_pages,
                     PAGE_POSITIONS * LATENT_DIM * (1 if kscale else 2), strides[0], strides[-1], dev)
     if workspace is None:
-        workspace = _latent_workspace(rows, heads, width, None if k < 0 else k, dev, stream)
+        workspace = _workspace(_lib.idx_latent_attention_workspace, (rows, heads, width, k), dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     elif workspace.get_device() != dev:
@@ -724,6 +746,311 @@ def idx_latent_attention_bf16(q, kv_pages, page_table, topk_idx, seqlens, out, l
                              stream, check)
 
 
+# --- the cache of keys and values by head (include/kv_cache.h).  Its pools are
+# tensors [pages, kv_heads, 64, D], whose strides the kernels take.
+
+
+def _table(page_table, rows, row_table, dev):
+    """A page table's address, that of its rows' map, its width, tables and row stride."""
+    if page_table.dtype is not torch.int32:
+        raise ValueError(f"page_table must be torch.int32, got {page_table.dtype}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have two dims")
+    tables, width = page_table.shape
+    step, unit = page_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("page_table must be unit-stride along its last dim")
+    if page_table.get_device() != dev:
+        raise _elsewhere("page_table", page_table, dev)
+    which = None
+    if row_table is not None:
+        which = _dense("row_table", row_table, torch.int32, (rows,), dev)
+    elif tables == 1:
+        step = 0
+    elif tables < rows:
+        raise ValueError(f"page_table holds {tables} tables for {rows} rows")
+    return page_table.data_ptr(), which, width, tables, step
+
+
+def _blocks(name, pool, dtypes, last, dev, like=None):
+    """Address, page stride and head stride (bytes) of a pool's blocks: [pages,
+    heads, *last], dense behind its first two dims; ``like``: a tensor that it
+    must agree with."""
+    shape = pool.shape
+    if pool.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {pool.dtype}")
+    if len(shape) != 2 + len(last) or shape[2:] != last:
+        raise ValueError(f"{name} must be [pages, kv_heads, {', '.join(str(n) for n in last)}], got {list(shape)}")
+    step = pool.stride()
+    if step[-1] != 1 or (len(last) == 2 and step[2] != last[1]):
+        raise ValueError(f"{name} must be dense behind its first two dims")
+    if pool.get_device() != dev:
+        raise _elsewhere(name, pool, dev)
+    if like is not None and (shape[:2] != like.shape[:2] or pool.dtype is not like.dtype):
+        raise ValueError(f"{name} must be of the keys' pages, heads and type")
+    size = pool.element_size()
+    block = 1
+    for n in last:
+        block *= n
+    return pool.data_ptr(), (step[0] if shape[0] > 1 else max(step[0], block)) * size, step[1] * size
+
+
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16,)
+
+
+def _kv_pools(fp8, k_pages, v_pages, scales, dim, dev):
+    """Addresses of the pools ([keys, values, their scales]) and their strides."""
+    block = (PAGE_POSITIONS, dim)
+    kv, page, head = _blocks("k_pages", k_pages, _FP8 if fp8 else _BF16, block, dev)
+    where, strides = [kv], [page, head]
+    if v_pages is not None:
+        v, *same = _blocks("v_pages", v_pages, _FP8 if fp8 else _BF16, block, dev, k_pages)
+        if same != strides:
+            raise ValueError("k_pages and v_pages must have the same strides")
+        where.append(v)
+    if fp8:
+        first = None
+        for name, scale in zip(("kscale", "vscale"), scales):
+            s, *same = _blocks(name, scale, (torch.float32,), (PAGE_POSITIONS,), dev)
+            if scale.shape[:2] != k_pages.shape[:2]:
+                raise ValueError(f"{name} must be of the keys' pages and heads")
+            if first is not None and same != first:
+                raise ValueError("kscale and vscale must have the same strides")
+            first = same
+            where.append(s)
+        strides += first
+    return where, strides
+
+
+def _num_pages(num_pages, pool):
+    """Pages of a pool, of which a call may take the first ``num_pages``."""
+    if num_pages is None:
+        return pool.shape[0]
+    if num_pages > pool.shape[0]:
+        raise ValueError(f"the pool holds {pool.shape[0]} pages, not {num_pages}")
+    return num_pages
+
+
+def idx_plan_batch(cached, added, free_pages, page_table, slots=None, positions=None, row_table=None, seqlens=None,
+                   starts=None, taken=None, *, stream=None, check=True) -> int:
+    """Page tables and slot maps of a step, from its requests' lengths.
+
+    Request r holds ``cached[r]`` positions (int32) and gets ``added[r]`` more; the
+    pages it lacks come from ``free_pages`` (int32, in order, request by request)
+    into its row of ``page_table`` (int32 [requests, width]).  Its new tokens are
+    rows of the batch, request by request: ``slots`` and ``positions`` int64 [n],
+    ``row_table`` and ``seqlens`` int32 [n] (rows past the last token: slot -1,
+    length 0), ``starts`` int64 [requests + 1] each request's first row, ``taken``
+    int64 [1] the pages asked for.  Those that are None are not written.
+    """
+    dev = cached.get_device()
+    requests = cached.shape[0] if cached.dim() == 1 else -1
+    have = _dense("cached", cached, torch.int32, (requests,), dev)
+    more = _dense("added", added, torch.int32, (requests,), dev)
+    num_free = free_pages.numel()
+    free = _dense("free_pages", free_pages, torch.int32, (num_free,), dev)
+    if page_table.dim() != 2 or page_table.shape[0] != requests:
+        raise ValueError(f"page_table must be [{requests}, width], got {list(page_table.shape)}")
+    if page_table.dtype is not torch.int32:
+        raise ValueError(f"page_table must be torch.int32, got {page_table.dtype}")
+    width = page_table.shape[1]
+    step, unit = page_table.stride()
+    if unit != 1 and width > 1:
+        raise ValueError("page_table must be unit-stride along its last dim")
+    if page_table.get_device() != dev:
+        raise _elsewhere("page_table", page_table, dev)
+    n, rows = None, []
+    for name, x, dtype in (("slots", slots, torch.int64), ("positions", positions, torch.int64),
+                           ("row_table", row_table, torch.int32), ("seqlens", seqlens, torch.int32)):
+        if x is None:
+            rows.append(None)
+            continue
+        n = x.numel() if n is None else n
+        rows.append(_dense(name, x, dtype, (n,), dev))
+    begin = None if starts is None else _dense("starts", starts, torch.int64, (requests + 1,), dev)
+    count = None if taken is None else _dense("taken", taken, torch.int64, (1,), dev)
+    return _launch(_lib.idx_plan_batch, dev, stream, check, have, more, requests, free, num_free, page_table.data_ptr(),
+                   width, step if requests > 1 else width, n or 0, *rows, begin, count)
+
+
+def _store_kv(fn, fp8, keys, values, slots, k_pages, v_pages, scales, num_pages, stream, check):
+    k_step, dev = _rows("keys", keys, 3), keys.get_device()
+    v_step = _rows("values", values, 3)
+    n, heads, dim = keys.shape
+    if values.shape != keys.shape:
+        raise ValueError(f"values must be {list(keys.shape)}, got {list(values.shape)}")
+    if values.get_device() != dev:
+        raise _elsewhere("values", values, dev)
+    at = _dense("slots", slots, torch.int64, (n,), dev)
+    where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
+    if k_pages.shape[1] != heads:
+        raise ValueError(f"k_pages must have {heads} heads, got {k_pages.shape[1]}")
+    return _launch(fn, dev, stream, check, keys.data_ptr(), values.data_ptr(), at, n, heads, dim, k_step, v_step, *where,
+                   _num_pages(num_pages, k_pages), *strides)
+
+
+def idx_store_kv_fp8(keys, values, slots, k_pages, v_pages, kscale, vscale, *, num_pages=None, stream=None,
+                     check=True) -> int:
+    """Quantise bf16 ``keys`` and ``values`` [n, kv_heads, D] (D 64, 128 or 256; first
+    dims may be strided), vector by vector (scale = amax/448, e4m3fn codes), into pool
+    slots.
+
+    ``k_pages`` and ``v_pages``: uint8 or float8_e4m3fn [pages, kv_heads, 64, D], of the
+    same strides, dense behind the first two dims; ``kscale`` and ``vscale``: fp32 [pages,
+    kv_heads, 64] likewise.  ``slots`` int64 [n] (64*page + position; out of range skips
+    the token).
+    """
+    return _store_kv(_lib.idx_store_kv_fp8, True, keys, values, slots, k_pages, v_pages, (kscale, vscale), num_pages,
+                     stream, check)
+
+
+def idx_store_kv_bf16(keys, values, slots, k_pages, v_pages, *, num_pages=None, stream=None, check=True) -> int:
+    """bf16 counterpart of :func:`idx_store_kv_fp8`: a copy."""
+    return _store_kv(_lib.idx_store_kv_bf16, False, keys, values, slots, k_pages, v_pages, (), num_pages, stream, check)
+
+
+def _page_bounds(fn, fp8, k_pages, kscale, page_table, seqlens, bounds, first, row_table, num_pages, stream, check):
+    dev = seqlens.get_device()
+    rows = seqlens.shape[0] if seqlens.dim() == 1 else -1
+    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
+    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
+    dim = k_pages.shape[-1]
+    where, strides = _kv_pools(fp8, k_pages, None, (kscale,), dim, dev)
+    heads, pages = k_pages.shape[1], _num_pages(num_pages, k_pages)
+    if bounds.dim() != 4 or bounds.shape[0] < pages:
+        raise ValueError(f"bounds must be [{pages}, {heads}, 2, {dim}], got {list(bounds.shape)}")
+    to = _dense("bounds", bounds, torch.bfloat16, (bounds.shape[0], heads, 2, dim), dev)
+    begin = None if first is None else _dense("first", first, torch.int32, (rows,), dev)
+    return _launch(fn, dev, stream, check, *where, table, which, 0 if which is None else tables, begin, lengths, to, rows,
+                   heads, dim, width, pages, *strides, step)
+
+
+def idx_page_bounds_fp8(k_pages, kscale, page_table, seqlens, bounds, *, first=None, row_table=None, num_pages=None,
+                        stream=None, check=True) -> int:
+    """Least and largest value of each dim of the keys in pages: for row b the pages of
+    its positions from ``first[b]`` (int32 [rows]; None: 0) to ``seqlens[b]``, into bf16
+    ``bounds`` [pages, kv_heads, 2, D], rounded outwards.
+
+    Pools as in :func:`idx_store_kv_fp8`, ``page_table`` int32 [tables, width]: one for
+    all rows, one per row, or row b's at ``row_table[b]``.
+    """
+    return _page_bounds(_lib.idx_page_bounds_fp8, True, k_pages, kscale, page_table, seqlens, bounds, first, row_table,
+                        num_pages, stream, check)
+
+
+def idx_page_bounds_bf16(k_pages, page_table, seqlens, bounds, *, first=None, row_table=None, num_pages=None, stream=None,
+                         check=True) -> int:
+    """bf16 counterpart of :func:`idx_page_bounds_fp8`."""
+    return _page_bounds(_lib.idx_page_bounds_bf16, False, k_pages, None, page_table, seqlens, bounds, first, row_table,
+                        num_pages, stream, check)
+
+
+def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *, first_pages=0, last_pages=0,
+                    row_table=None, stream=None, check=True) -> int:
+    """The most that any key within a page's ``bounds`` (bf16 [pages, kv_heads, 2, D])
+    could score with the query heads of bf16 ``q`` [rows, heads, D] that share a key
+    head, into ``scores`` fp32 [rows, kv_heads, width] (rows may be strided); +inf for
+    a row's first and last pages, -inf past them.  ``page_counts`` int32 [rows,
+    kv_heads]: live pages.
+
+    ``scores.flatten(0, 1)`` and ``page_counts.flatten()`` are what
+    :func:`idx_topk_logits` selects pages from (score rows a multiple of 4 apart).
+    """
+    dev, shape = q.get_device(), q.shape
+    if len(shape) != 3 or bounds.dim() != 4:
+        raise ValueError(f"q must be [rows, heads, D] and bounds [pages, kv_heads, 2, D], got {list(shape)} and "
+                         f"{list(bounds.shape)}")
+    rows, heads, dim = shape
+    pages, kv_heads = bounds.shape[:2]
+    from_q = _dense("q", q, torch.bfloat16, shape, dev)
+    near = _dense("bounds", bounds, torch.bfloat16, (pages, kv_heads, 2, dim), dev)
+    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
+    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
+    if scores.dtype is not torch.float32:
+        raise ValueError(f"scores must be torch.float32, got {scores.dtype}")
+    if scores.shape != (rows, kv_heads, width):
+        raise ValueError(f"scores must be {[rows, kv_heads, width]}, got {list(scores.shape)}")
+    if scores.get_device() != dev:
+        raise _elsewhere("scores", scores, dev)
+    row, head, unit = scores.stride()
+    apart = head if kv_heads > 1 else row if rows > 1 else width
+    if (unit != 1 and width > 1) or (rows > 1 and kv_heads > 1 and row != kv_heads * head):
+        raise ValueError("scores must be unit-stride along its last dim, its rows evenly apart")
+    counts = None if page_counts is None else _dense("page_counts", page_counts, torch.int32, (rows, kv_heads), dev)
+    return _launch(_lib.idx_page_scores, dev, stream, check, from_q, near, table, which, 0 if which is None else tables,
+                   lengths, scores.data_ptr(), counts, rows, heads, kv_heads, dim, width, pages, step, apart, first_pages,
+                   last_pages)
+
+
+def idx_kv_attention_workspace(rows, num_heads, kv_heads, head_dim, table_width, k=None) -> int:
+    """Bytes of workspace that a call of :func:`idx_kv_attention_fp8` or its counterpart
+    of these sizes needs on the current device (``k`` None: no selection)."""
+    return _lib.idx_kv_attention_workspace(rows, num_heads, kv_heads, head_dim, table_width, -1 if k is None else k)
+
+
+def _kv_attention(fn, fp8, q, k_pages, v_pages, scales, page_table, page_idx, seqlens, out, lse, scale, num_pages, sinks,
+                  row_table, workspace, stream, check):
+    dev, shape = q.get_device(), q.shape
+    if len(shape) != 3 or out.shape != shape:
+        raise ValueError(f"q and out must be [rows, heads, D], got {list(shape)} and {list(out.shape)}")
+    rows, heads, dim = shape
+    from_q = _dense("q", q, torch.bfloat16, shape, dev)
+    to = _dense("out", out, torch.bfloat16, shape, dev)
+    where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
+    kv_heads = k_pages.shape[1]
+    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
+    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
+    idx = sink = log = None
+    k = -1
+    if page_idx is not None:
+        if page_idx.dim() == 2 and page_idx.shape[0] == rows * kv_heads:  # (as the top-k's rows)
+            k = page_idx.shape[1]
+            idx = _dense("page_idx", page_idx, torch.int32, (rows * kv_heads, k), dev)
+        else:
+            k = page_idx.shape[-1] if page_idx.dim() == 3 else 0
+            idx = _dense("page_idx", page_idx, torch.int32, (rows, kv_heads, k), dev)
+    if sinks is not None:
+        sink = _dense("sinks", sinks, torch.float32, (heads,), dev)
+    if lse is not None:
+        log = _dense("lse", lse, torch.float32, (rows, heads), dev)
+    if workspace is None:
+        workspace = _workspace(_lib.idx_kv_attention_workspace, (rows, heads, kv_heads, dim, width, k), dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    elif workspace.get_device() != dev:
+        raise _elsewhere("workspace", workspace, dev)
+    space, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    return _launch(fn, dev, stream, check, from_q, *where, table, which, 0 if which is None else tables, idx, lengths, sink,
+                   to, log, rows, heads, kv_heads, dim, width, _num_pages(num_pages, k_pages), *strides, step, k, scale,
+                   space, nbytes)
+
+
+def idx_kv_attention_fp8(q, k_pages, v_pages, kscale, vscale, page_table, page_idx, seqlens, out, lse=None, *, scale,
+                         sinks=None, row_table=None, workspace=None, num_pages=None, stream=None, check=True) -> int:
+    """Attention of bf16 ``q`` [rows, heads, D], one new token a row, to the fp8 keys and
+    values of its pages (pools as in :func:`idx_store_kv_fp8`; heads / kv_heads query
+    heads share a key head) into ``out`` (as ``q``) and, if given, ``lse`` fp32 [rows,
+    heads].
+
+    ``page_idx`` int32 [rows, kv_heads, k] (or [rows * kv_heads, k]): the pages to attend
+    to, as the top-k leaves them; None: all below ``seqlens``.  ``page_table`` int32
+    [tables, width]: one for all rows, one per row, or row b's at ``row_table[b]``.
+    ``sinks`` fp32 [heads] join the softmax's denominator.  ``workspace``: a tensor of
+    :func:`idx_kv_attention_workspace` bytes, of this call's own while it runs; None takes
+    one from torch's allocator.
+    """
+    return _kv_attention(_lib.idx_kv_attention_fp8, True, q, k_pages, v_pages, (kscale, vscale), page_table, page_idx,
+                         seqlens, out, lse, scale, num_pages, sinks, row_table, workspace, stream, check)
+
+
+def idx_kv_attention_bf16(q, k_pages, v_pages, page_table, page_idx, seqlens, out, lse=None, *, scale, sinks=None,
+                          row_table=None, workspace=None, num_pages=None, stream=None, check=True) -> int:
+    """bf16 counterpart of :func:`idx_kv_attention_fp8`."""
+    return _kv_attention(_lib.idx_kv_attention_bf16, False, q, k_pages, v_pages, (), page_table, page_idx, seqlens, out, lse,
+                         scale, num_pages, sinks, row_table, workspace, stream, check)
+
+
 __all__ = [
     "idx_paged_mqa_logits_fp8", "idx_paged_mqa_logits_bf16", "idx_paged_mqa_logits_varlen_fp8",
     "idx_paged_mqa_logits_varlen_bf16", "idx_topk_logits",
@@ -732,5 +1059,7 @@ __all__ = [
     "idx_norm_rope", "idx_norm_rope_store_fp8", "idx_norm_rope_store_bf16",
     "idx_load_slots_fp8", "idx_load_slots_bf16",
     "idx_latent_attention_fp8", "idx_latent_attention_bf16", "idx_latent_attention_workspace",
+    "idx_plan_batch", "idx_store_kv_fp8", "idx_store_kv_bf16", "idx_page_bounds_fp8", "idx_page_bounds_bf16",
+    "idx_page_scores", "idx_kv_attention_fp8", "idx_kv_attention_bf16", "idx_kv_attention_workspace",
     "idx_abi_version", "IdxError", "LIB_PATH", "NUM_HEADS", "HEAD_DIM", "PAGE_POSITIONS", "LATENT_DIM",
 ]

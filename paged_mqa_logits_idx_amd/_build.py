@@ -1,5 +1,5 @@
 """Build step for the HIP libraries (gfx950, in-tree): libidx_paged_mqa.so, the
-indexer and its latent cache, and libidx_read_stream.so, the bare key-page read stream that the
+indexer and its caches, and libidx_read_stream.so, the bare key-page read stream that the
 benchmark measures as the reachable HBM read rate."""
 from __future__ import annotations
 
@@ -10,7 +10,8 @@ from pathlib import Path
 
 PKG_DIR = Path(__file__).resolve().parent
 REPO_DIR = PKG_DIR.parent
-SOURCES = [PKG_DIR / "csrc" / name for name in ("paged_mqa_logits.hip", "norm_rope.hip", "latent_attention.hip")]
+SOURCES = [PKG_DIR / "csrc" / name for name in ("paged_mqa_logits.hip", "norm_rope.hip", "latent_attention.hip",
+                                                "kv_cache.hip", "kv_attention.hip")]
 LIB_PATH = PKG_DIR / "libidx_paged_mqa.so"
 STREAM_SOURCES = [PKG_DIR / "csrc" / "read_stream.hip"]
 STREAM_LIB_PATH = PKG_DIR / "libidx_read_stream.so"

@@ -1,0 +1,694 @@
+// kv_attention.hip -- attention of one new token per row over the paged keys and
+// values by head (gfx950 kernels and C-ABI entry points declared in
+// include/kv_cache.h).
+//
+//   x_ip = scale * <q_i, k_p>,  z_i = sum_p exp(x_ip) (+ exp(sink_i)),
+//   out_i = sum_p exp(x_ip) v_p / z_i
+//
+// for the query heads i of a key head and its positions p.  A unit is (row, key
+// head, block of 16 * NT of its query heads): it reads every page of its own once.
+//
+// Work decomposition.  The pages of all units, one after the other, are cut into
+// even shares, one a workgroup, whatever the rows' lengths: a share's pieces are the
+// end of a unit, whole units and the start of one.  Whole units are finished by their
+// workgroup, the other pieces leave sums and outputs in float32, which a second
+// kernel joins.  Where there are far more units than workgroups, each unit is a
+// workgroup's and nothing is joined.
+//
+// A workgroup has four waves, which take tiles of kTile positions of a piece in
+// turn, each with LDS buffers of its own: keys and values arrive by DMA, the next
+// keys while the values are used and the next values while the keys are, so the
+// waves need no barrier until the piece ends.  The matrix units (16 x 16 x 32,
+// bf16) take
+//   scores   X = K Q^T:  a lane gets 4 positions of a head for each 16 of the tile;
+//   outputs  O^T += V^T P^T:  the lane's positions of two such blocks are its 8
+//            k-values, so P stays in registers; V^T comes out of LDS through the
+//            transposing reads in the same order.
+// Rounding: scores, exponentials, sums and outputs are float32; the products take
+// bf16 operands, which rounds the probability (times the value's e4m3 scale) once, by
+// 2^-8 of itself at most.  The denominator sums the unrounded probabilities.
+//
+// Running maximum: a head's reference moves, and sums and outputs are rescaled,
+// only when a lane's probabilities of a tile add up to more than kLimit.
+#include <type_traits>
+
+#include "kv_device.h"
+
+namespace {
+
+constexpr float kLimit = 256.0f;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kMinShare = 2;  // pages of a workgroup's share, at least
+
+struct Attend {
+  const uint8_t* q;     // bf16 [rows][heads][D]
+  const uint8_t* kv[2];
+  const uint8_t* ks[2];
+  Tables tables;
+  const int32_t* idx;   // [rows][kv_heads][k] (k >= 0)
+  const int32_t* sl;
+  const float* sinks;   // [heads] or NULL
+  uint8_t* out;         // bf16 [rows][heads][D]
+  float* lse;           // [rows][heads] or NULL
+  int32_t* prefix;      // [rows + 1]: pages of the rows before, of one unit each (balanced)
+  f32x2* ml;            // references and sums of the pieces: [2 * shares][16 * NT]
+  f32x4* part;          // their outputs
+  KvStrides s;
+  uint32_t pages_lim;
+  int32_t rows, heads, kv_heads, group, blocks, width, k;
+  int32_t shares;       // workgroups with a share; 0: a unit each
+  float scale2;         // scale * log2(e)
+};
+
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(x >> 32)) << 32 | (uint32_t)uniform((int32_t)x));
+}
+
+// 64 lanes x 16 bytes from base + off (off each lane's own) to LDS dst + 16 * lane.
+__device__ __forceinline__ void dma16_from(int64_t base, uint32_t off, uint32_t dst) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
+}
+
+template <int KEY, int DIM, int NT>
+struct Form {
+  static constexpr int kRowBytes = KEY == kFp8 ? DIM : 2 * DIM;  // of a position
+  static constexpr int kPerCu = NT * DIM > 256 || kRowBytes > 256 ? 1 : 2;
+  static constexpr int kWant = (kPerCu == 1 ? 16384 : 8192) / kRowBytes;
+  static constexpr int kTile = kWant < 32 || NT == 4 || (KEY == kFp8 && NT > 1) ? 32 : kWant > 64 ? 64 : kWant;
+  static constexpr int kBytes = kTile * kRowBytes;  // of a tile's keys, and of its values
+  static constexpr int kDmas = kBytes / 1024;
+  static constexpr int kScaleDmas = KEY == kFp8 ? kTile / 32 : 0;
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int kRowsPerLine = kRowBytes < 256 ? 256 / kRowBytes : 1;
+  static constexpr int kMask = (kChunks < 16 ? kChunks : 16) - 1;
+  static constexpr int kSteps = DIM / 32;   // of the scores' sums
+  static constexpr int kParts = DIM / 16;   // blocks of 16 values
+  static constexpr int kSubs = kTile / 16;  // blocks of 16 positions
+
+  // Chunk c (16 bytes) of position r stands at place c ^ key(r) of its LDS row, so
+  // that what 16 lanes (keys: one chunk of 16 positions) or 32 (values: one or two
+  // chunks of 16 or 8 positions) read at once lies in different banks.
+  static __device__ __forceinline__ constexpr int key_k(int r) { return (r / kRowsPerLine) & kMask; }
+  static __device__ __forceinline__ constexpr int key_v(int r) {
+    if (KEY == kBf16) return ((r / kRowsPerLine) << 1) & kMask;
+    return ((r / kRowsPerLine) & (kMask >> 1)) | ((r >> 4 & 1) ? (kMask + 1) / 2 : 0);
+  }
+};
+
+template <int KEY, int DIM, int NT>
+struct AttendShared {
+  using F = Form<KEY, DIM, NT>;
+  uint8_t tile[kWaves][2][F::kBytes];           // keys, values; at the end outputs
+  float scale[kWaves][2][KEY == kFp8 ? F::kTile : 4];
+  f32x2 ml[kWaves][16 * NT];
+  int32_t sums[kWaves];
+  int32_t start[3];
+};
+
+// The pages of a row's units.
+__device__ __forceinline__ int32_t live_pages(const Attend& a, int64_t b) {
+  const int64_t L = min((int64_t)max(a.sl[b], 0), (int64_t)a.width * kPage);
+  return (int32_t)((L + kPage - 1) / kPage);
+}
+__device__ __forceinline__ int32_t pages_of(const Attend& a, int64_t b) {
+  const int32_t c = live_pages(a, b);
+  return a.k >= 0 ? min(a.k, c) : c;
+}
+
+template <int KEY, int DIM, int NT>
+__global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_attention_kernel(Attend a) {
+  using F = Form<KEY, DIM, NT>;
+  constexpr int kTile = F::kTile, kRowBytes = F::kRowBytes, kSteps = F::kSteps, kParts = F::kParts, kSubs = F::kSubs;
+  constexpr int kTilesPerPage = kPage / kTile;
+  __shared__ __attribute__((aligned(1024))) AttendShared<KEY, DIM, NT> sh;
+  const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int32_t per_row = a.kv_heads * a.blocks;
+
+  // The workgroup's share: pages [at, end) of the units' in order, from page
+  // `page0` of unit `unit` of row `b`.
+  int64_t b;
+  int32_t unit, page0 = 0, count, at = 0, end;
+  if (a.shares == 0) {
+    b = blockIdx.x / (uint32_t)per_row;
+    unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
+    count = end = pages_of(a, b);
+  } else {
+    const int32_t per = (a.rows + kThreads - 1) / kThreads;
+    const int32_t r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+    int32_t own = 0;
+    for (int32_t r = r0; r < r1; ++r) own += pages_of(a, r);
+    int32_t upto = own;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int32_t v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 63) sh.sums[wave] = upto;
+    if (threadIdx.x == 0) sh.start[0] = -1;
+    __syncthreads();
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) upto += sh.sums[w];
+      total += sh.sums[w];
+    }
+    if (blockIdx.x == 0) {
+      int32_t p = upto - own;
+      for (int32_t r = r0; r < r1; ++r) {
+        a.prefix[r] = p;
+        p += pages_of(a, r);
+      }
+      if (threadIdx.x == 0) a.prefix[a.rows] = total;
+    }
+    total *= per_row;
+    const int32_t share = max((total + a.shares - 1) / a.shares, kMinShare);
+    at = (int32_t)min((int64_t)blockIdx.x * share, (int64_t)total);
+    end = min(at + share, total);
+    if (at >= end) return;
+    if (at < upto * per_row && at >= (upto - own) * per_row) {
+      int32_t p = (upto - own) * per_row, r = r0, c = pages_of(a, r);
+      while (at >= p + c * per_row) {
+        p += c * per_row;
+        c = pages_of(a, ++r);
+      }
+      sh.start[0] = r;
+      sh.start[1] = (at - p) / c;
+      sh.start[2] = (at - p) % c;
+    }
+    __syncthreads();
+    b = uniform(sh.start[0]);
+    unit = uniform(sh.start[1]);
+    page0 = uniform(sh.start[2]);
+    count = uniform(pages_of(a, b));
+  }
+
+  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[wave][0][0];
+  const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[wave][0][0];
+  const uint8_t* keys = sh.tile[wave][0];
+  const uint8_t* vals = sh.tile[wave][1];
+  // DMA i of a tile brings rows kRowsPerDma * i ..; the lane's source within it
+  constexpr int kRowsPerDma = 1024 / kRowBytes;
+  const int dr = lane / F::kChunks, dc = lane % F::kChunks;
+  const uint32_t from_k = dr * kRowBytes + 16 * (dc ^ F::key_k(dr)), from_v = dr * kRowBytes + 16 * (dc ^ F::key_v(dr));
+
+  int32_t slot = 0;  // of a piece that is not whole: the share's first, or its last
+  while (true) {
+    const int32_t pages = a.shares == 0 ? count : min(count - page0, end - at);
+    const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
+    const int32_t head0 = h * a.group + hb * 16 * NT;                 // of the row's
+    const int32_t heads = min(16 * NT, a.group - hb * 16 * NT);
+    const int32_t L = (int32_t)min((int64_t)max(a.sl[b], 0), (int64_t)a.width * kPage);
+    const int32_t live = (int32_t)(((int64_t)L + kPage - 1) / kPage);
+    bool table_ok;
+    const int32_t* tab = a.tables.of(b, table_ok);
+    const int32_t* list = a.k >= 0 ? a.idx + (b * a.kv_heads + h) * (int64_t)a.k : nullptr;
+
+    bf16x8 q[NT][kSteps];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = KEY == kFp8 ? 64 * (s / 2) + 16 * quad + 8 * (s & 1) : 32 * s + 8 * quad;
+        q[t][s] = (bf16x8)((__bf16)0.0f);
+        if (16 * t + n < heads)
+          q[t][s] = *reinterpret_cast<const bf16x8*>(a.q + ((b * a.heads + head0 + 16 * t + n) * DIM + d) * 2);
+      }
+
+    f32x4 acc[kParts][NT];
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[p][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    // of head 16 * t + n: reference, what a lane's probabilities may add up to by it
+    // (nothing, before the first), the lane's sum
+    float ref[NT], limit[NT], sum[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ref[t] = 0.0f, limit[t] = -1.0f, sum[t] = 0.0f;
+    bool bad = false;
+
+    // The wave's tiles: page `page` of the pool, positions 64 * j + first .. of the
+    // row, `left` of them live.
+    struct Tile {
+      int32_t page, first, left;
+    };
+    int32_t next = wave, ids_from = -64;  // next tile of the piece, first page whose id is in `ids`
+    int32_t ids = -2, ids_left = 0;       // page id (-1 outside the pool, -2 to skip) and live positions of page ids_from + lane
+    const int32_t tiles = pages * kTilesPerPage;
+    auto find = [&](Tile& t) -> bool {
+      for (; next < tiles; next += kWaves) {
+        const int32_t e = next / kTilesPerPage;
+        if (e >= ids_from + 64) {
+          ids_from = e / 64 * 64;
+          ids = -2;
+          ids_left = 0;
+          if (ids_from + lane < pages) {
+            const int32_t j = list ? list[page0 + ids_from + lane] : page0 + ids_from + lane;
+            if ((uint32_t)j < (uint32_t)live) {
+              const int32_t page = table_ok ? tab[j] : -1;
+              ids = (uint32_t)page < a.pages_lim ? page : -1;
+              ids_left = min(L - j * kPage, kPage);
+            }
+          }
+        }
+        const int32_t page = __builtin_amdgcn_readlane(ids, e - ids_from);
+        t.first = (next % kTilesPerPage) * kTile;
+        t.left = __builtin_amdgcn_readlane(ids_left, e - ids_from) - t.first;
+        if (page == -1) bad = true;
+        if (page < 0 || t.left <= 0) continue;
+        t.page = page;
+        next += kWaves;
+        return true;
+      }
+      return false;
+    };
+    auto fetch = [&](const Tile& t, auto which) {  // keys (with both scales) or values
+      constexpr int kWhich = decltype(which)::value;
+      const int64_t base = uniform64((int64_t)(uintptr_t)a.kv[kWhich] + t.page * a.s.kv_page + h * a.s.kv_head + t.first * kRowBytes);
+      if constexpr (KEY == kFp8 && kWhich == 0) {
+        const int64_t at_ = t.page * a.s.ks_page + h * a.s.ks_head + 4 * t.first;
+        if constexpr (kTile == 64) {
+          dma4(a.ks[0] + at_ + 4 * lane, lds_scale);
+          dma4(a.ks[1] + at_ + 4 * lane, lds_scale + 256);
+        } else {
+          dma4((lane < 32 ? a.ks[0] : a.ks[1]) + at_ + 4 * (lane & 31), lds_scale);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < F::kDmas; ++i) {
+        const int key = kWhich == 0 ? F::key_k(kRowsPerDma * i) : F::key_v(kRowsPerDma * i);
+        dma16_from(base, ((kWhich == 0 ? from_k : from_v) ^ (16 * key)) + 1024 * i, lds_tile + kWhich * F::kBytes + 1024 * i);
+      }
+    };
+    constexpr std::integral_constant<int, 0> kKeys{};
+    constexpr std::integral_constant<int, 1> kVals{};
+
+    Tile cur, nxt;
+    bool more = find(cur);
+    if (more) {
+      fetch(cur, kKeys);
+      fetch(cur, kVals);
+    }
+    while (more) {
+      const bool ahead = find(nxt);
+      // scores of the tile
+      wait_vm<F::kDmas>();
+      f32x4 x[kSubs][NT];
+      f32x4 ks[kSubs], vs[kSubs];
+#pragma unroll
+      for (int s = 0; s < kSubs; ++s) {
+        if constexpr (KEY == kFp8) {
+          ks[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][0][16 * s + 4 * quad]);
+          vs[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][1][16 * s + 4 * quad]);
+        }
+        if constexpr (NT * DIM > 128) __builtin_amdgcn_sched_barrier(0);  // (or all LDS reads go first, into registers there are not)
+        const int r = 16 * s + n;
+        const uint8_t* row = keys + r * kRowBytes;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) x[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < F::kChunks / 4; ++c) {
+          const u32x4 raw = *reinterpret_cast<const u32x4*>(row + 16 * ((4 * c + quad) ^ F::key_k(r)));
+          if constexpr (KEY == kFp8) {
+            const bf16x8 k0 = fp8x8_to_bf16x8(raw.x, raw.y), k1 = fp8x8_to_bf16x8(raw.z, raw.w);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[t][2 * c], x[s][t], 0, 0, 0);
+              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[t][2 * c + 1], x[s][t], 0, 0, 0);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, raw), q[t][c], x[s][t], 0, 0, 0);
+          }
+        }
+      }
+      // (the reads above are over: their products wait for them; the DMAs behind
+      // them overwrite what they read)
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (ahead) fetch(nxt, kKeys);
+
+      // probabilities
+      const bool partial = cur.left < kTile;
+      bf16x8 w[kSubs / 2][NT];
+      float part[NT];
+      auto weigh = [&]() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          part[t] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
+              const bool dead = partial && 16 * s + 4 * quad + e >= cur.left;
+              const float p = dead ? 0.0f : __builtin_amdgcn_exp2f(fmaf(x[s][t][e], by, -ref[t]));
+              part[t] += p;
+              w[s / 2][t][4 * (s & 1) + e] = (__bf16)(KEY == kFp8 ? (dead ? 0.0f : p * vs[s][e]) : p);
+            }
+        }
+      };
+      weigh();
+      bool over = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) over = over || part[t] > limit[t];
+      if (__ballot(over) != 0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
+              const bool dead = partial && 16 * s + 4 * quad + e >= cur.left;
+              top = fmaxf(top, dead ? -INFINITY : x[s][t][e] * by);
+            }
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const bool begun = limit[t] > 0.0f;
+          const bool moves = begun ? top > ref[t] : top > -INFINITY;
+          const float f = moves && begun ? __builtin_amdgcn_exp2f(ref[t] - top) : 1.0f;  // (before the first there is nothing)
+          if (moves) ref[t] = top, limit[t] = kLimit;
+          sum[t] *= f;
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) acc[p][t] *= f;
+        }
+        weigh();
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) sum[t] += part[t];
+
+      // outputs
+      if (ahead) wait_vm<F::kDmas + F::kScaleDmas>();
+      else wait_vm<0>();
+      if (partial) {  // values past the row's end: their probability is 0, theirs may be no number
+        for (int i = cur.left * F::kChunks + lane; i < kTile * F::kChunks; i += 64)
+          *reinterpret_cast<u32x4*>(sh.tile[wave][1] + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int i = 0; i < kSubs / 2; ++i) {
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          if constexpr (NT * DIM > 128)
+            if (p % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+          bf16x8 v;
+          if constexpr (KEY == kFp8) {
+            const int k = n >> 1, r = 32 * i + 16 * (k >> 2) + 4 * quad + (k & 3);
+            const v2i c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)(
+                vals + r * kRowBytes + 16 * (p ^ F::key_v(r)) + 8 * (n & 1)));
+            v = fp8x8_to_bf16x8((uint32_t)c.x, (uint32_t)c.y);
+          } else {
+            v4s u[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 32 * i + 16 * e + 4 * quad + (n >> 2), c = 2 * p + (n >> 1 & 1);
+              u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(
+                  vals + r * kRowBytes + 16 * (c ^ F::key_v(r)) + 8 * (n & 1)));
+            }
+            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u[0], u[1], 0, 1, 2, 3, 4, 5, 6, 7));
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) acc[p][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[i][t], acc[p][t], 0, 0, 0);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (ahead) fetch(nxt, kVals);
+      cur = nxt;
+      more = ahead;
+    }
+
+    // The waves' sums and outputs together.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float s = sum[t];
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (bad) s = __builtin_nanf("");
+      if (quad == 0) sh.ml[wave][16 * t + n] = (f32x2){s == 0.0f ? -INFINITY : ref[t], s};
+    }
+    barrier();
+    const bool whole = a.shares == 0 || pages == count;
+    const int64_t piece = 2 * (int64_t)blockIdx.x + slot;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f32x2 ml[kWaves];
+      float top = -INFINITY, total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        ml[w] = sh.ml[w][16 * t + n];
+        top = fmaxf(top, ml[w].x);
+      }
+      const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total = fmaf(ml[w].y, __builtin_amdgcn_exp2f(ml[w].x - base), total);
+      const float f = __builtin_amdgcn_exp2f(sh.ml[wave][16 * t + n].x - base);
+      f32x4* mine = reinterpret_cast<f32x4*>(sh.tile[wave][0]);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) mine[64 * p + lane] = acc[p][t] * f;
+      barrier();
+      const bool in = 16 * t + n < heads;
+      const int64_t head = b * a.heads + head0 + 16 * t + n;
+      Closing c = {1.0f, 1.0f, 0.0f};
+      if (whole) c = close_sum(top, total, a.sinks && in ? a.sinks[head0 + 16 * t + n] * kLog2e : -INFINITY);
+#pragma unroll
+      for (int p = wave; p < kParts; p += kWaves) {
+        f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) o += reinterpret_cast<const f32x4*>(sh.tile[w][0])[64 * p + lane];
+        if (whole) {
+          o = o * c.by * c.half * c.half;
+          if (in)
+            *reinterpret_cast<bf16x4*>(a.out + (head * DIM + 16 * p + 4 * quad) * 2) =
+                (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+        } else {
+          a.part[((piece * NT + t) * kParts + p) * 64 + lane] = o;
+        }
+      }
+      if (wave == 0 && quad == 0) {
+        if (!whole) a.ml[piece * 16 * NT + 16 * t + n] = (f32x2){top, total};
+        else if (a.lse && in) a.lse[head] = c.lse;
+      }
+      barrier();
+    }
+    if (a.shares == 0) return;
+    slot = 1;
+    at += pages;
+    if (at >= end) return;
+    page0 = 0;
+    if (++unit == per_row) {
+      unit = 0;
+      do count = uniform(pages_of(a, ++b));
+      while (count == 0);
+    }
+  }
+}
+
+// Joins the pieces of a unit, a wave 16 values of 16 heads; writes the units that
+// have no pages.  The pieces' order is fixed, so the result does not depend on
+// their timing.
+constexpr int kBatch = 8;
+
+template <int DIM, int NT>
+__global__ __launch_bounds__(64) void kv_join_kernel(Attend a) {
+  constexpr int kParts = DIM / 16;
+  const int lane = threadIdx.x, n = lane & 15, quad = lane >> 4;
+  const int32_t per_row = a.kv_heads * a.blocks;
+  const int32_t b = (int32_t)(blockIdx.x / (uint32_t)per_row), unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
+  const int t = (int)blockIdx.y / kParts, p = (int)blockIdx.y % kParts;
+  const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
+  const int32_t before = a.prefix[b], count = a.prefix[b + 1] - before, total_pages = a.prefix[a.rows] * per_row;
+  const int32_t share = max((total_pages + a.shares - 1) / a.shares, kMinShare);
+  const int32_t s = before * per_row + unit * count;  // the unit's pages: s .. s + count
+  const int32_t w0 = s / share, w1 = count > 0 ? (s + count - 1) / share : w0 - 1;
+  if (w0 == w1) return;  // whole
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, total = 0.0f;
+#pragma unroll 1
+  for (int32_t w = w0; w <= w1; w += kBatch) {
+    f32x2 ml[kBatch];
+    f32x4 v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = (f32x2){-INFINITY, 0.0f};
+      v[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      if (w + i <= w1) {
+        const int64_t piece = 2 * (int64_t)(w + i) + (w + i == w0 && s != w0 * share ? 1 : 0);
+        ml[i] = a.ml[piece * 16 * NT + 16 * t + n];
+        v[i] = a.part[((piece * NT + t) * kParts + p) * 64 + lane];
+      }
+    }
+    float to = top;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) to = fmaxf(to, ml[i].x);
+    const float base = to == -INFINITY ? 0.0f : to, by = __builtin_amdgcn_exp2f(top - base);
+    top = to;
+    total *= by;
+    o *= by;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float f = __builtin_amdgcn_exp2f(ml[i].x - base);
+      total = fmaf(ml[i].y, f, total);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = fmaf(v[i][e], f, o[e]);
+    }
+  }
+  const int32_t i = hb * 16 * NT + 16 * t + n;
+  if (i >= a.group) return;
+  const int32_t head = h * a.group + i;
+  const Closing c = close_sum(top, total, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+  o = o * c.by * c.half * c.half;
+  *reinterpret_cast<bf16x4*>(a.out + (((int64_t)b * a.heads + head) * DIM + 16 * p + 4 * quad) * 2) =
+      (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+  if (a.lse && p == 0 && quad == 0) a.lse[(int64_t)b * a.heads + head] = c.lse;
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+constexpr int64_t kMaxHeads = 8000000;  // of a call's rows together: a launch has less than 2^32 threads
+
+struct Split {
+  int nt, blocks, shares;  // head tiles of a unit, blocks of them a group, workgroups (0: a unit each)
+  int64_t bytes;
+};
+
+inline int64_t padded(int64_t n) { return (n + 255) / 256 * 256; }
+
+bool dims_ok(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t table_width, int32_t k) {
+  return rows >= 0 && num_heads >= 0 && kv_heads >= 0 && (kv_heads == 0 ? num_heads == 0 : num_heads % kv_heads == 0) &&
+         table_width >= 0 && table_width <= kMaxWidth && k >= -1 && (int64_t)rows * num_heads <= kMaxHeads;
+}
+
+// From the scalar arguments alone (the lengths are on the device).
+Split split_of(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
+  Split s = {1, 1, 0, 0};
+  if (rows == 0 || num_heads == 0) return s;
+  const int32_t group = num_heads / kv_heads;
+  const int most_nt = head_dim == 256 ? 2 : 4;
+  while (s.nt < most_nt && 16 * s.nt < group) s.nt *= 2;
+  s.blocks = (group + 16 * s.nt - 1) / (16 * s.nt);
+  const int64_t units = (int64_t)rows * kv_heads * s.blocks;
+  const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
+  const int64_t workgroups = 2 * device_cu_count();
+  if (units > 4 * workgroups || units * most > INT32_MAX / 2 || most <= kMinShare) return s;
+  const int64_t want = (units * most + kMinShare - 1) / kMinShare;
+  s.shares = (int)(want < workgroups ? want : workgroups);
+  if (s.shares < 1) s.shares = 1;
+  s.bytes = padded(4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.nt * 8) +
+            2 * (int64_t)s.shares * s.nt * head_dim * 64;
+  return s;
+}
+
+template <int KEY, int DIM, int NT>
+void launch(const Attend& a, const Split& split, hipStream_t stream) {
+  const uint32_t units = (uint32_t)((int64_t)a.rows * a.kv_heads * a.blocks);
+  kv_attention_kernel<KEY, DIM, NT><<<dim3(split.shares ? (uint32_t)split.shares : units), dim3(kThreads), 0, stream>>>(a);
+  if (split.shares) kv_join_kernel<DIM, NT><<<dim3(units, NT * DIM / 16), dim3(64), 0, stream>>>(a);
+}
+
+template <int KEY, int DIM>
+void launch_for(const Attend& a, const Split& split, hipStream_t stream) {
+  if (split.nt == 1) return launch<KEY, DIM, 1>(a, split, stream);
+  if (split.nt == 2) return launch<KEY, DIM, 2>(a, split, stream);
+  if constexpr (DIM <= 128) launch<KEY, DIM, 4>(a, split, stream);
+}
+
+template <int KEY>
+int kv_attention(const void* q, const void* k_pages, const void* v_pages, const float* kscale, const float* vscale,
+                 const int32_t* page_table, const int32_t* row_table, int32_t num_tables, const int32_t* page_idx,
+                 const int32_t* seqlens, const float* sinks, void* out, float* lse, int32_t rows, int32_t num_heads,
+                 int32_t kv_heads, int32_t head_dim, int32_t table_width, int64_t num_pages, const KvStrides& s,
+                 int64_t page_table_row_stride, int32_t k, float scale, void* workspace, int64_t workspace_bytes,
+                 hipStream_t stream) {
+  if (!head_dim_ok(head_dim) || (int64_t)num_heads > (int64_t)kMaxGroup * kv_heads) return IDX_ERR_UNSUPPORTED;
+  if (!dims_ok(rows, num_heads, kv_heads, table_width, k) || page_table_row_stride < 0 || num_tables < 0 ||
+      !(fabsf(scale * kLog2e) < INFINITY) || workspace_bytes < 0)
+    return IDX_ERR_SHAPE;
+  int st = validate_kv_strides(KEY, kv_heads, head_dim, num_pages, s);
+  if (st != IDX_OK || rows == 0 || num_heads == 0) return st;
+  if (!q || !seqlens || !out || (table_width > 0 && !page_table) || (k > 0 && !page_idx) || (k < 0 && page_idx))
+    return IDX_ERR_NULL;
+  st = validate_kv_pointers(KEY, kv_heads, k_pages, kscale, s);
+  if (st == IDX_OK) st = validate_kv_pointers(KEY, kv_heads, v_pages, vscale, s);
+  if (st != IDX_OK) return st;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(row_table, 4) || !aligned(page_idx, 4) ||
+      !aligned(seqlens, 4) || !aligned(sinks, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
+    return IDX_ERR_ALIGN;
+  const Split split = split_of(rows, num_heads, kv_heads, head_dim, table_width, k);
+  if (split.bytes > 0 && !workspace) return IDX_ERR_NULL;
+  if (workspace_bytes < split.bytes) return IDX_ERR_SHAPE;
+  Attend a;
+  a.q = static_cast<const uint8_t*>(q);
+  a.kv[0] = static_cast<const uint8_t*>(k_pages);
+  a.kv[1] = static_cast<const uint8_t*>(v_pages);
+  a.ks[0] = reinterpret_cast<const uint8_t*>(kscale);
+  a.ks[1] = reinterpret_cast<const uint8_t*>(vscale);
+  a.tables = {page_table, row_table, page_table_row_stride, num_tables};
+  a.idx = page_idx;
+  a.sl = seqlens;
+  a.sinks = sinks;
+  a.out = static_cast<uint8_t*>(out);
+  a.lse = lse;
+  uint8_t* space = static_cast<uint8_t*>(workspace);
+  a.prefix = reinterpret_cast<int32_t*>(space);
+  a.ml = reinterpret_cast<f32x2*>(space + padded(4 * ((int64_t)rows + 1)));
+  a.part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(a.ml) + padded(2 * (int64_t)split.shares * 16 * split.nt * 8));
+  a.s = s;
+  a.pages_lim = pages_limit(num_pages);
+  a.rows = rows;
+  a.heads = num_heads;
+  a.kv_heads = kv_heads;
+  a.group = num_heads / kv_heads;
+  a.blocks = split.blocks;
+  a.width = table_width;
+  a.k = k;
+  a.shares = split.shares;
+  a.scale2 = scale * kLog2e;
+  (void)hipGetLastError();  // start from a clean error state
+  if (head_dim == 64) launch_for<KEY, 64>(a, split, stream);
+  else if (head_dim == 128) launch_for<KEY, 128>(a, split, stream);
+  else launch_for<KEY, 256>(a, split, stream);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t idx_kv_attention_workspace(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim,
+                                   int32_t table_width, int32_t k) {
+  if (!head_dim_ok(head_dim) || !dims_ok(rows, num_heads, kv_heads, table_width, k) ||
+      (int64_t)num_heads > (int64_t)kMaxGroup * kv_heads)
+    return -1;
+  return split_of(rows, num_heads, kv_heads, head_dim, table_width, k).bytes;
+}
+
+int idx_kv_attention_fp8(const void* q, const void* k_pages, const void* v_pages, const float* kscale,
+                         const float* vscale, const int32_t* page_table, const int32_t* row_table,
+                         int32_t num_tables, const int32_t* page_idx, const int32_t* seqlens,
+                         const float* sinks, void* out, float* lse, int32_t rows, int32_t num_heads,
+                         int32_t kv_heads, int32_t head_dim, int32_t table_width, int64_t num_pages,
+                         int64_t kv_page_stride, int64_t kv_head_stride, int64_t kscale_page_stride,
+                         int64_t kscale_head_stride, int64_t page_table_row_stride, int32_t k, float scale,
+                         void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  return kv_attention<kFp8>(q, k_pages, v_pages, kscale, vscale, page_table, row_table, num_tables, page_idx, seqlens, sinks,
+                            out, lse, rows, num_heads, kv_heads, head_dim, table_width, num_pages,
+                            {kv_page_stride, kv_head_stride, kscale_page_stride, kscale_head_stride},
+                            page_table_row_stride, k, scale, workspace, workspace_bytes, stream);
+}
+
+int idx_kv_attention_bf16(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                          const int32_t* row_table, int32_t num_tables, const int32_t* page_idx,
+                          const int32_t* seqlens, const float* sinks, void* out, float* lse, int32_t rows,
+                          int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width,
+                          int64_t num_pages, int64_t kv_page_stride, int64_t kv_head_stride,
+                          int64_t page_table_row_stride, int32_t k, float scale, void* workspace,
+                          int64_t workspace_bytes, hipStream_t stream) {
+  return kv_attention<kBf16>(q, k_pages, v_pages, nullptr, nullptr, page_table, row_table, num_tables, page_idx, seqlens,
+                             sinks, out, lse, rows, num_heads, kv_heads, head_dim, table_width, num_pages,
+                             {kv_page_stride, kv_head_stride, 0, 0}, page_table_row_stride, k, scale, workspace,
+                             workspace_bytes, stream);
+}
+
+}  // extern "C"

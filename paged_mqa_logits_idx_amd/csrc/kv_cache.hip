@@ -1,0 +1,627 @@
+// kv_cache.hip -- page tables and slot maps of a batch, paged store of keys and
+// values, bounds of pages' keys and scores of pages by them (gfx950 kernels and
+// C-ABI entry points declared in include/kv_cache.h).
+#include <type_traits>
+
+#include "kv_device.h"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Page tables and slot maps.
+
+struct Plan {
+  const int32_t* cached;
+  const int32_t* added;
+  const int32_t* free_pages;
+  int32_t* pt;
+  int64_t* slots;
+  int64_t* positions;
+  int32_t* row_table;
+  int32_t* seqlens;
+  int64_t* starts;
+  int64_t* taken;
+  int64_t num_free, pt_stride, n;
+  int32_t requests, width;
+};
+
+// What a request has and gets.
+struct Request {
+  int64_t cached, added, low, need;  // positions, new ones, its pages so far, new ones
+};
+__device__ __forceinline__ Request request_of(const Plan& p, int32_t r) {
+  Request q;
+  q.cached = max(p.cached[r], 0);
+  q.added = max(p.added[r], 0);
+  q.low = (q.cached + kPage - 1) / kPage;
+  const int64_t high = min((q.cached + q.added + kPage - 1) / kPage, (int64_t)p.width);
+  q.need = max(high - q.low, (int64_t)0);
+  return q;
+}
+
+// Every workgroup adds up the requests by itself (they are few, and read from the
+// caches), so that one launch does it all: its threads have runs of `per` requests,
+// whose sums are scanned in LDS.  A token's request is found by halving over
+// the runs, then a walk along one; a new page's likewise.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void plan_kernel(Plan p) {
+  __shared__ int64_t tokens[THREADS + 1], pages[THREADS + 1];
+  __shared__ int64_t sums[2][THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t per = (p.requests + THREADS - 1) / THREADS;
+  const int32_t r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
+  int64_t t = 0, g = 0;
+  for (int32_t r = r0; r < r1; ++r) {
+    const Request q = request_of(p, r);
+    t += q.added;
+    g += q.need;
+  }
+  const int64_t own_t = t, own_g = g;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t a = __shfl_up((long long)t, d), b = __shfl_up((long long)g, d);
+    if (lane >= d) t += a, g += b;
+  }
+  if (lane == 63) sums[0][wave] = t, sums[1][wave] = g;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w)
+    if (w < wave) t += sums[0][w], g += sums[1][w];
+  tokens[tid] = t - own_t;
+  pages[tid] = g - own_g;
+  if (tid == THREADS - 1) tokens[THREADS] = t, pages[THREADS] = g;
+  __syncthreads();
+  const int64_t all_tokens = tokens[THREADS], all_pages = pages[THREADS];
+
+  if (blockIdx.x == 0) {
+    if (p.starts) {
+      int64_t at = tokens[tid];
+      for (int32_t r = r0; r < r1; ++r) {
+        p.starts[r] = at;
+        at += max(p.added[r], 0);
+      }
+      if (tid == 0) p.starts[p.requests] = all_tokens;
+    }
+    if (p.taken && tid == 0) *p.taken = all_pages;
+  }
+
+  const auto run_of = [&](const int64_t* from, int64_t x) {  // the last run that starts at or before x
+    int at = 0;
+#pragma unroll
+    for (int d = THREADS / 2; d > 0; d /= 2)
+      if (from[at + d] <= x) at += d;
+    return at;
+  };
+  const auto free_page = [&](int64_t i) { return i < p.num_free ? p.free_pages[i] : -1; };
+  const int64_t first = (int64_t)blockIdx.x * THREADS + tid, step = (int64_t)gridDim.x * THREADS;
+  for (int64_t row = first; row < p.n; row += step) {
+    int64_t slot = -1, position = 0;
+    int32_t request = 0, length = 0;
+    if (row < all_tokens) {
+      const int run = run_of(tokens, row);
+      int64_t start = tokens[run], base = pages[run];
+      request = run * per;
+      Request q = request_of(p, request);
+      while (row >= start + q.added) {
+        start += q.added;
+        base += q.need;
+        q = request_of(p, ++request);
+      }
+      position = q.cached + (row - start);
+      length = (int32_t)min(position + 1, (int64_t)INT32_MAX);
+      const int64_t j = position / kPage;
+      int32_t page = -1;
+      if (j < p.width) page = j < q.low ? p.pt[request * p.pt_stride + j] : free_page(base + j - q.low);
+      if (page >= 0) slot = (int64_t)page * kPage + position % kPage;
+    }
+    if (p.slots) p.slots[row] = slot;
+    if (p.positions) p.positions[row] = position;
+    if (p.row_table) p.row_table[row] = request;
+    if (p.seqlens) p.seqlens[row] = length;
+  }
+  for (int64_t i = first; i < all_pages; i += step) {
+    const int run = run_of(pages, i);
+    int64_t base = pages[run];
+    int32_t request = run * per;
+    Request q = request_of(p, request);
+    while (i >= base + q.need) {
+      base += q.need;
+      q = request_of(p, ++request);
+    }
+    p.pt[request * p.pt_stride + q.low + (i - base)] = free_page(i);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Store of keys and values.
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+struct Store {
+  const uint8_t* x[2];  // keys, values (bf16)
+  uint8_t* kv[2];
+  uint8_t* ks[2];
+  const int64_t* slots;
+  int64_t x_stride[2];  // bytes
+  int64_t vectors;      // tokens * heads, of each
+  int64_t pool_slots;   // 64 * pages
+  KvStrides s;
+  int32_t heads;
+};
+
+constexpr int kStoreSteps = 2;
+
+// A vector of D values is D/8 lanes' (16 bytes of bf16 each); a wave takes
+// kStoreSteps groups of 64*8/D neighbouring vectors of the keys and the same of
+// the values, all loads under way at once.
+template <int KEY, int LPV, bool FAR>
+__global__ __launch_bounds__(kThreads) void store_kv_kernel(Store p) {
+  constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kUnit = kStoreSteps * kVecs;
+  const int lane = threadIdx.x & 63, sub = lane % LPV, wave = threadIdx.x >> 6;
+  const int64_t step = (int64_t)gridDim.x * kWaves * kUnit;
+  for (int64_t v0 = ((int64_t)blockIdx.x * kWaves + wave) * kUnit; v0 < p.vectors; v0 += step) {
+    u32x4 raw[kStoreSteps][2];
+    int64_t slot[kStoreSteps];
+    int32_t head[kStoreSteps];
+#pragma unroll
+    for (int u = 0; u < kStoreSteps; ++u) {
+      const int64_t v = v0 + u * kVecs + lane / LPV;
+      slot[u] = -1;
+      head[u] = 0;
+      raw[u][0] = raw[u][1] = (u32x4){0u, 0u, 0u, 0u};
+      if (v < p.vectors) {
+        const int64_t t = p.vectors <= UINT32_MAX ? (uint32_t)v / (uint32_t)p.heads : v / p.heads;
+        head[u] = (int32_t)(v - t * p.heads);
+        slot[u] = p.slots[t];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          raw[u][w] = *reinterpret_cast<const u32x4*>(p.x[w] + t * p.x_stride[w] + ((int64_t)head[u] * kDim + 8 * sub) * 2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kStoreSteps; ++u) {
+      const bool ok = slot[u] >= 0 && slot[u] < p.pool_slots;
+      const int64_t page = ok ? slot[u] / kPage : 0, i = ok ? slot[u] % kPage : 0;
+      const int64_t at = page * p.s.kv_page + head[u] * p.s.kv_head;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if constexpr (KEY == kBf16) {
+          if (ok) put<FAR>(raw[u][w], p.kv[w] + at + (i * kDim + 8 * sub) * 2);
+        } else {
+          float v[8], scale;
+          bf16x8_to_float(raw[u][w], v);
+          const u32x2 codes = quantise<LPV>(v, 1.0f, ok, scale, [&](float (&f)[8]) { bf16x8_to_float(raw[u][w], f); });
+          if (ok) {
+            put<FAR>(codes, p.kv[w] + at + i * kDim + 8 * sub);
+            if (sub == 0) *reinterpret_cast<float*>(p.ks[w] + page * p.s.ks_page + head[u] * p.s.ks_head + 4 * i) = scale;
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Bounds of pages' keys.
+
+struct Bounds {
+  const uint8_t* kv;
+  const uint8_t* ks;
+  Tables tables;
+  const int32_t* first;  // or NULL
+  const int32_t* sl;
+  uint8_t* out;          // bf16 [pages][heads][2][D]
+  KvStrides s;
+  uint32_t pages_lim;
+  int32_t heads, width;
+};
+
+constexpr float kBf16Max = 3.3895313892515355e38f;
+
+// The bf16 next to v (finite: clamped) that is no less (UP) or no more.
+template <bool UP>
+__device__ __forceinline__ uint32_t outwards(float v) {
+  const uint32_t bits = __float_as_uint(__builtin_amdgcn_fmed3f(v, -kBf16Max, kBf16Max));
+  return ((bits >> 31 != 0) == UP ? bits : bits + 0xffffu) >> 16;
+}
+
+// A wave takes a page of a head: a lane 16 bytes of a position, 1024 bytes of the
+// block a load, all of the block's loads under way at once; then the lanes that
+// have the same values of other positions.
+template <int KEY, int DIM>
+__global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
+  constexpr int kPer = KEY == kFp8 ? 16 : 8;  // values of a lane
+  constexpr int LP = DIM / kPer, kLoads = LP, kStep = 64 / LP;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t b = blockIdx.y;
+  bool table_ok;
+  const int32_t* tab = p.tables.of(b, table_ok);
+  const int64_t L = min((int64_t)max(p.sl[b], 0), (int64_t)p.width * kPage);
+  const int64_t j0 = p.first ? max(p.first[b], 0) / kPage : 0, j1 = (L + kPage - 1) / kPage;
+  if (!table_ok || j0 >= j1) return;
+  const int64_t items = (j1 - j0) * p.heads;
+  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
+    const int64_t j = j0 + item / p.heads, h = item % p.heads;
+    const int32_t page = tab[j];
+    if ((uint32_t)page >= p.pages_lim) continue;
+    const int live = (int)min(L - j * kPage, (int64_t)kPage);
+    const uint8_t* block = p.kv + (int64_t)page * p.s.kv_page + h * p.s.kv_head;
+    const float* scales = reinterpret_cast<const float*>(p.ks + (int64_t)page * p.s.ks_page + h * p.s.ks_head);
+    u32x4 raw[kLoads];
+    float scale[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      raw[i] = *reinterpret_cast<const u32x4*>(block + 1024 * i + 16 * lane);
+      if constexpr (KEY == kFp8) scale[i] = scales[kStep * i + lane / LP];
+    }
+    float lo[kPer], hi[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) lo[e] = INFINITY, hi[e] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      float v[kPer];
+      if constexpr (KEY == kFp8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(raw[i][e], false), c = __builtin_amdgcn_cvt_pk_f32_fp8(raw[i][e], true);
+          v[4 * e] = a[0] * scale[i], v[4 * e + 1] = a[1] * scale[i];
+          v[4 * e + 2] = c[0] * scale[i], v[4 * e + 3] = c[1] * scale[i];
+        }
+      } else {
+        bf16x8_to_float(raw[i], v);
+      }
+      const bool dead = kStep * i + lane / LP >= live;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const float x = dead ? __builtin_nanf("") : v[e];
+        lo[e] = fminf(lo[e], x);
+        hi[e] = fmaxf(hi[e], x);
+      }
+    }
+#pragma unroll
+    for (int d = LP; d < 64; d *= 2) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        lo[e] = fminf(lo[e], __shfl_xor(lo[e], d));
+        hi[e] = fmaxf(hi[e], __shfl_xor(hi[e], d));
+      }
+    }
+    if (lane >= 2 * LP) continue;
+    const bool up = lane >= LP;
+    uint32_t word[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      uint32_t two[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool none = lo[e + k] > hi[e + k];
+        two[k] = none ? 0u : up ? outwards<true>(hi[e + k]) : outwards<false>(lo[e + k]);
+      }
+      word[e / 2] = two[0] | two[1] << 16;
+    }
+    uint8_t* to = p.out + (((int64_t)page * p.heads + h) * 2 * DIM + lane * kPer) * 2;
+#pragma unroll
+    for (int e = 0; e < kPer / 8; ++e)
+      *reinterpret_cast<u32x4*>(to + 16 * e) = (u32x4){word[4 * e], word[4 * e + 1], word[4 * e + 2], word[4 * e + 3]};
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Scores of pages.
+
+struct Scores {
+  const uint8_t* q;
+  const uint8_t* bounds;
+  Tables tables;
+  const int32_t* sl;
+  float* out;
+  int32_t* counts;  // or NULL
+  int64_t out_stride, blocks;
+  uint32_t pages_lim;
+  int32_t rows, heads, kv_heads, width, first, last;
+};
+
+constexpr int kScoreTiles = 2;                                // of 16 pages a wave
+constexpr int kScorePages = 16 * kScoreTiles * kWaves;        // pages of a workgroup
+
+// max(q lo, q hi) is q hi where q is positive and q lo where it is negative, so the
+// sum is a product of [min(q, 0), max(q, 0)] with [lo, hi]: bf16 matrix instructions
+// with exact products and float32 sums.  A wave takes 16 * kScoreTiles pages, whose
+// bounds a lane loads as the B operand (16 bytes of a page each), against 16 query
+// heads at a time; a lane then has 4 heads of a page.
+template <int DIM>
+__global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
+  constexpr int kSteps = DIM / 32;
+  const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t group = p.heads / p.kv_heads;
+  for (int64_t unit = blockIdx.x; unit < (int64_t)p.rows * p.kv_heads * p.blocks; unit += gridDim.x) {
+    const int64_t bh = unit / p.blocks, block = unit - bh * p.blocks;
+    const int64_t b = bh / p.kv_heads;
+    const int32_t h = (int32_t)(bh - b * p.kv_heads);
+    bool table_ok;
+    const int32_t* tab = p.tables.of(b, table_ok);
+    const int64_t L = min((int64_t)max(p.sl[b], 0), (int64_t)p.width * kPage);
+    const int32_t count = (int32_t)((L + kPage - 1) / kPage);
+    if (p.counts && block == 0 && threadIdx.x == 0) p.counts[bh] = count;
+    const int64_t j0 = block * kScorePages + wave * 16 * kScoreTiles + n;  // the lane's first page
+    float best[kScoreTiles];
+    if (j0 - n < count) {
+      bf16x8 side[kScoreTiles][2][kSteps];
+      bool ok[kScoreTiles];
+#pragma unroll
+      for (int t = 0; t < kScoreTiles; ++t) {
+        const int64_t j = j0 + 16 * t;
+        const int32_t page = j < count && table_ok ? tab[j] : -1;
+        ok[t] = (uint32_t)page < p.pages_lim;
+        const uint8_t* from = p.bounds + (((int64_t)(ok[t] ? page : 0) * p.kv_heads + h) * 2 * DIM + 8 * quad) * 2;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s)
+            side[t][w][s] = ok[t] ? *reinterpret_cast<const bf16x8*>(from + (w * DIM + 32 * s) * 2) : (bf16x8)((__bf16)0.0f);
+        best[t] = -INFINITY;
+      }
+      for (int32_t i0 = 0; i0 < group; i0 += 16) {
+        // (heads past the group's last are its last)
+        const uint8_t* from = p.q + ((b * p.heads + (int64_t)h * group + min(i0 + n, group - 1)) * DIM + 8 * quad) * 2;
+        f32x4 acc[kScoreTiles];
+#pragma unroll
+        for (int t = 0; t < kScoreTiles; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const u32x4 q = *reinterpret_cast<const u32x4*>(from + 64 * s);
+          u32x4 neg, pos;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t sign = (q[e] >> 15 & 0x00010001u) * 0xffffu;
+            neg[e] = q[e] & sign;
+            pos[e] = q[e] & ~sign;
+          }
+#pragma unroll
+          for (int t = 0; t < kScoreTiles; ++t) {
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, neg), side[t][0][s], acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), side[t][1][s], acc[t], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kScoreTiles; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) best[t] = __builtin_elementwise_maximum(best[t], acc[t][e]);  // (a NaN stays)
+      }
+#pragma unroll
+      for (int t = 0; t < kScoreTiles; ++t) {
+        best[t] = __builtin_elementwise_maximum(best[t], __shfl_xor(best[t], 16));
+        best[t] = __builtin_elementwise_maximum(best[t], __shfl_xor(best[t], 32));
+        if (!ok[t]) best[t] = __builtin_nanf("");
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kScoreTiles; ++t) {
+      const int64_t j = j0 + 16 * t;
+      float s = best[t];
+      if (j < p.first || j >= (int64_t)count - p.last) s = INFINITY;
+      if (j >= count) s = -INFINITY;
+      if (quad == t && j < p.width) p.out[bh * p.out_stride + j] = s;
+    }
+  }
+}
+static_assert(kScoreTiles <= 4);  // (a quad of lanes writes a tile)
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+template <class F>
+int for_dim(int32_t head_dim, F f) {
+  switch (head_dim) {
+    case 64: f(std::integral_constant<int, 64>{}); break;
+    case 128: f(std::integral_constant<int, 128>{}); break;
+    default: f(std::integral_constant<int, 256>{});
+  }
+  return launch_status();
+}
+
+template <int KEY>
+int store_kv(const void* keys, const void* values, const int64_t* slots, int64_t n, int32_t kv_heads,
+             int32_t head_dim, int64_t k_row_stride, int64_t v_row_stride, void* k_pages, void* v_pages,
+             float* kscale, float* vscale, int64_t num_pages, const KvStrides& s, hipStream_t stream) {
+  if (!head_dim_ok(head_dim)) return IDX_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 32;
+  if (n < 0 || kv_heads < 0 || n > ((int64_t)1 << 32) || k_row_stride < (int64_t)kv_heads * head_dim ||
+      v_row_stride < (int64_t)kv_heads * head_dim || k_row_stride > most || v_row_stride > most)
+    return IDX_ERR_SHAPE;
+  int st = validate_kv_strides(KEY, kv_heads, head_dim, num_pages, s);
+  if (st != IDX_OK || n == 0 || kv_heads == 0) return st;
+  if (!keys || !values || !slots) return IDX_ERR_NULL;
+  st = validate_kv_pointers(KEY, kv_heads, k_pages, kscale, s);
+  if (st == IDX_OK) st = validate_kv_pointers(KEY, kv_heads, v_pages, vscale, s);
+  if (st != IDX_OK) return st;
+  if (!aligned(keys, 16) || !aligned(values, 16) || k_row_stride % 8 != 0 || v_row_stride % 8 != 0 || !aligned(slots, 8))
+    return IDX_ERR_ALIGN;
+  Store p;
+  p.x[0] = static_cast<const uint8_t*>(keys);
+  p.x[1] = static_cast<const uint8_t*>(values);
+  p.kv[0] = static_cast<uint8_t*>(k_pages);
+  p.kv[1] = static_cast<uint8_t*>(v_pages);
+  p.ks[0] = reinterpret_cast<uint8_t*>(kscale);
+  p.ks[1] = reinterpret_cast<uint8_t*>(vscale);
+  p.slots = slots;
+  p.x_stride[0] = 2 * k_row_stride;
+  p.x_stride[1] = 2 * v_row_stride;
+  p.vectors = n * kv_heads;
+  p.pool_slots = num_pages * kPage;
+  p.s = s;
+  p.heads = kv_heads;
+  (void)hipGetLastError();  // start from a clean error state
+  return for_dim(head_dim, [&](auto dim) {
+    constexpr int LPV = decltype(dim)::value / 8, kUnit = kStoreSteps * kWaves * (64 / LPV);
+    const int64_t units = (p.vectors + kUnit - 1) / kUnit, cap = 16 * device_cu_count();
+    const dim3 grid((uint32_t)(units < cap ? units : cap));
+    if (is_far(p.vectors, LPV * (KEY == kFp8 ? 16 : 32)))
+      store_kv_kernel<KEY, LPV, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    else
+      store_kv_kernel<KEY, LPV, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+  });
+}
+
+// The checks that bounds and scores share of a row's pages.
+int validate_rows(int32_t rows, int32_t kv_heads, int32_t table_width, int32_t num_tables, int64_t page_table_row_stride) {
+  return rows < 0 || kv_heads < 0 || table_width < 0 || table_width > kMaxWidth || num_tables < 0 ||
+                 page_table_row_stride < 0 || (int64_t)rows * kv_heads > INT32_MAX
+             ? IDX_ERR_SHAPE
+             : IDX_OK;
+}
+
+template <int KEY>
+int page_bounds(const void* k_pages, const float* kscale, const int32_t* page_table, const int32_t* row_table,
+                int32_t num_tables, const int32_t* first, const int32_t* seqlens, void* bounds, int32_t rows,
+                int32_t kv_heads, int32_t head_dim, int32_t table_width, int64_t num_pages, const KvStrides& s,
+                int64_t page_table_row_stride, hipStream_t stream) {
+  if (!head_dim_ok(head_dim)) return IDX_ERR_UNSUPPORTED;
+  int st = validate_rows(rows, kv_heads, table_width, num_tables, page_table_row_stride);
+  if (st == IDX_OK) st = validate_kv_strides(KEY, kv_heads, head_dim, num_pages, s);
+  if (st != IDX_OK || rows == 0 || kv_heads == 0 || table_width == 0) return st;
+  if (!page_table || !seqlens || !bounds) return IDX_ERR_NULL;
+  st = validate_kv_pointers(KEY, kv_heads, k_pages, kscale, s);
+  if (st != IDX_OK) return st;
+  if (!aligned(page_table, 4) || !aligned(row_table, 4) || !aligned(first, 4) || !aligned(seqlens, 4) || !aligned(bounds, 16))
+    return IDX_ERR_ALIGN;
+  Bounds p;
+  p.kv = static_cast<const uint8_t*>(k_pages);
+  p.ks = reinterpret_cast<const uint8_t*>(kscale);
+  p.tables = {page_table, row_table, page_table_row_stride, num_tables};
+  p.first = first;
+  p.sl = seqlens;
+  p.out = static_cast<uint8_t*>(bounds);
+  p.s = s;
+  p.pages_lim = pages_limit(num_pages);
+  p.heads = kv_heads;
+  p.width = table_width;
+  (void)hipGetLastError();
+  int64_t x = ((int64_t)table_width * kv_heads + kWaves - 1) / kWaves;
+  const int64_t cap = (8 * (int64_t)device_cu_count() + rows - 1) / rows;
+  if (x > cap) x = cap;
+  return for_dim(head_dim, [&](auto dim) {
+    constexpr int kDim = decltype(dim)::value;
+    for (int64_t b = 0; b < rows; b += 65535) {  // (a grid's second side)
+      Bounds part = p;
+      part.sl = p.sl + b;
+      if (p.first) part.first = p.first + b;
+      if (row_table) part.tables.rt = row_table + b;
+      else part.tables.pt = page_table + b * page_table_row_stride;
+      const dim3 grid((uint32_t)x, (uint32_t)(rows - b < 65535 ? rows - b : 65535));
+      page_bounds_kernel<KEY, kDim><<<grid, dim3(kThreads), 0, stream>>>(part);
+    }
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+int idx_plan_batch(const int32_t* cached, const int32_t* added, int32_t requests, const int32_t* free_pages,
+                   int64_t num_free, int32_t* page_table, int32_t table_width, int64_t page_table_row_stride,
+                   int64_t n, int64_t* slots, int64_t* positions, int32_t* row_table, int32_t* seqlens,
+                   int64_t* starts, int64_t* taken, hipStream_t stream) {
+  if (requests < 0 || requests > 65536 || num_free < 0 || table_width < 0 || table_width > kMaxWidth || n < 0 ||
+      n > ((int64_t)1 << 40) || page_table_row_stride < 0 || (requests > 1 && page_table_row_stride < table_width))
+    return IDX_ERR_SHAPE;
+  if (n == 0 && requests == 0 && !starts && !taken) return IDX_OK;
+  if ((requests > 0 && (!cached || !added || (table_width > 0 && !page_table))) || (num_free > 0 && !free_pages))
+    return IDX_ERR_NULL;
+  if (!aligned(cached, 4) || !aligned(added, 4) || !aligned(free_pages, 4) || !aligned(page_table, 4) ||
+      !aligned(slots, 8) || !aligned(positions, 8) || !aligned(row_table, 4) || !aligned(seqlens, 4) ||
+      !aligned(starts, 8) || !aligned(taken, 8))
+    return IDX_ERR_ALIGN;
+  const Plan p = {cached, added, free_pages, page_table, slots, positions, row_table, seqlens, starts, taken,
+                  num_free, page_table_row_stride, n, requests, table_width};
+  (void)hipGetLastError();
+  const int threads = requests <= 256 ? 256 : 1024;
+  int64_t grid = (n + threads - 1) / threads;
+  if (grid < 1) grid = 1;
+  if (grid > 2 * device_cu_count()) grid = 2 * device_cu_count();
+  if (threads == 256) plan_kernel<256><<<dim3((uint32_t)grid), dim3(256), 0, stream>>>(p);
+  else plan_kernel<1024><<<dim3((uint32_t)grid), dim3(1024), 0, stream>>>(p);
+  return launch_status();
+}
+
+int idx_store_kv_fp8(const void* keys, const void* values, const int64_t* slots, int64_t n, int32_t kv_heads,
+                     int32_t head_dim, int64_t k_row_stride, int64_t v_row_stride, void* k_pages, void* v_pages,
+                     float* kscale, float* vscale, int64_t num_pages, int64_t kv_page_stride,
+                     int64_t kv_head_stride, int64_t kscale_page_stride, int64_t kscale_head_stride,
+                     hipStream_t stream) {
+  return store_kv<kFp8>(keys, values, slots, n, kv_heads, head_dim, k_row_stride, v_row_stride, k_pages, v_pages, kscale,
+                        vscale, num_pages, {kv_page_stride, kv_head_stride, kscale_page_stride, kscale_head_stride}, stream);
+}
+
+int idx_store_kv_bf16(const void* keys, const void* values, const int64_t* slots, int64_t n, int32_t kv_heads,
+                      int32_t head_dim, int64_t k_row_stride, int64_t v_row_stride, void* k_pages, void* v_pages,
+                      int64_t num_pages, int64_t kv_page_stride, int64_t kv_head_stride, hipStream_t stream) {
+  return store_kv<kBf16>(keys, values, slots, n, kv_heads, head_dim, k_row_stride, v_row_stride, k_pages, v_pages, nullptr,
+                         nullptr, num_pages, {kv_page_stride, kv_head_stride, 0, 0}, stream);
+}
+
+int idx_page_bounds_fp8(const void* k_pages, const float* kscale, const int32_t* page_table,
+                        const int32_t* row_table, int32_t num_tables, const int32_t* first,
+                        const int32_t* seqlens, void* bounds, int32_t rows, int32_t kv_heads, int32_t head_dim,
+                        int32_t table_width, int64_t num_pages, int64_t kv_page_stride, int64_t kv_head_stride,
+                        int64_t kscale_page_stride, int64_t kscale_head_stride, int64_t page_table_row_stride,
+                        hipStream_t stream) {
+  return page_bounds<kFp8>(k_pages, kscale, page_table, row_table, num_tables, first, seqlens, bounds, rows, kv_heads,
+                           head_dim, table_width, num_pages,
+                           {kv_page_stride, kv_head_stride, kscale_page_stride, kscale_head_stride},
+                           page_table_row_stride, stream);
+}
+
+int idx_page_bounds_bf16(const void* k_pages, const int32_t* page_table, const int32_t* row_table,
+                         int32_t num_tables, const int32_t* first, const int32_t* seqlens, void* bounds,
+                         int32_t rows, int32_t kv_heads, int32_t head_dim, int32_t table_width,
+                         int64_t num_pages, int64_t kv_page_stride, int64_t kv_head_stride,
+                         int64_t page_table_row_stride, hipStream_t stream) {
+  return page_bounds<kBf16>(k_pages, nullptr, page_table, row_table, num_tables, first, seqlens, bounds, rows, kv_heads,
+                            head_dim, table_width, num_pages, {kv_page_stride, kv_head_stride, 0, 0},
+                            page_table_row_stride, stream);
+}
+
+int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table, const int32_t* row_table,
+                    int32_t num_tables, const int32_t* seqlens, float* scores, int32_t* page_counts,
+                    int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width,
+                    int64_t num_pages, int64_t page_table_row_stride, int64_t score_stride, int32_t first_pages,
+                    int32_t last_pages, hipStream_t stream) {
+  if (!head_dim_ok(head_dim) || (int64_t)num_heads > (int64_t)kMaxGroup * kv_heads) return IDX_ERR_UNSUPPORTED;
+  const int st = validate_rows(rows, kv_heads, table_width, num_tables, page_table_row_stride);
+  if (st != IDX_OK) return st;
+  if (num_heads < 0 || (kv_heads > 0 && num_heads % kv_heads != 0) || num_pages < 0 || score_stride < table_width ||
+      score_stride > ((int64_t)1 << 32) || first_pages < 0 || last_pages < 0)
+    return IDX_ERR_SHAPE;
+  if (rows == 0 || kv_heads == 0 || num_heads == 0) return IDX_OK;
+  if (!q || !seqlens || (table_width > 0 && (!bounds || !page_table || !scores))) return IDX_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(page_table, 4) || !aligned(row_table, 4) ||
+      !aligned(seqlens, 4) || !aligned(scores, 4) || !aligned(page_counts, 4))
+    return IDX_ERR_ALIGN;
+  Scores p;
+  p.q = static_cast<const uint8_t*>(q);
+  p.bounds = static_cast<const uint8_t*>(bounds);
+  p.tables = {page_table, row_table, page_table_row_stride, num_tables};
+  p.sl = seqlens;
+  p.out = scores;
+  p.counts = page_counts;
+  p.out_stride = score_stride;
+  p.blocks = table_width > 0 ? (table_width + kScorePages - 1) / kScorePages : 1;
+  p.pages_lim = pages_limit(num_pages);
+  p.rows = rows;
+  p.heads = num_heads;
+  p.kv_heads = kv_heads;
+  p.width = table_width;
+  p.first = first_pages;
+  p.last = last_pages;
+  const int64_t units = (int64_t)rows * kv_heads * p.blocks, cap = (int64_t)1 << 20;
+  const dim3 grid((uint32_t)(units < cap ? units : cap));
+  (void)hipGetLastError();
+  return for_dim(head_dim, [&](auto dim) {
+    page_scores_kernel<decltype(dim)::value><<<grid, dim3(kThreads), 0, stream>>>(p);
+  });
+}
+
+}  // extern "C"
