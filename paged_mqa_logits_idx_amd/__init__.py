@@ -650,7 +650,7 @@ def _workspace(size, dims, dev, stream) -> torch.Tensor | None:
     device and stream."""
     if dev < 0:
         return None
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _workspace(size, dims, dev, stream)
     need = size(*dims)
@@ -750,32 +750,48 @@ def idx_latent_attention_bf16(q, kv_pages, page_table, topk_idx, seqlens, out, l
 # tensors [pages, kv_heads, 64, D], whose strides the kernels take.
 
 
-def _table(page_table, rows, row_table, dev):
-    """A page table's address, that of its rows' map, its width, tables and row stride."""
-    if page_table.dtype is not torch.int32:
-        raise ValueError(f"page_table must be torch.int32, got {page_table.dtype}")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must have two dims")
-    tables, width = page_table.shape
-    step, unit = page_table.stride()
+def _flat(name, x, dtype, n, dev) -> int:
+    """Address of a contiguous tensor of this type and ``n`` elements on device ``dev``."""
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.numel() != n:
+        raise ValueError(f"{name} must be of {n} elements, got {list(x.shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if x.get_device() != dev:
+        raise _elsewhere(name, x, dev)
+    return x.data_ptr()
+
+
+def _grid(name, x, dev):
+    """Address, rows, columns and row stride of an int32 table."""
+    if x.dtype is not torch.int32:
+        raise ValueError(f"{name} must be torch.int32, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dims")
+    (rows, width), (step, unit) = x.shape, x.stride()
     if unit != 1 and width > 1:
-        raise ValueError("page_table must be unit-stride along its last dim")
-    if page_table.get_device() != dev:
-        raise _elsewhere("page_table", page_table, dev)
-    which = None
+        raise ValueError(f"{name} must be unit-stride along its last dim")
+    if x.get_device() != dev:
+        raise _elsewhere(name, x, dev)
+    return x.data_ptr(), rows, width, step
+
+
+def _table(page_table, rows, row_table, dev):
+    """A page table's address, that of its rows' map, tables, width and row stride."""
+    at, tables, width, step = _grid("page_table", page_table, dev)
     if row_table is not None:
-        which = _dense("row_table", row_table, torch.int32, (rows,), dev)
-    elif tables == 1:
+        return at, _flat("row_table", row_table, torch.int32, rows, dev), tables, width, step
+    if tables == 1:
         step = 0
     elif tables < rows:
         raise ValueError(f"page_table holds {tables} tables for {rows} rows")
-    return page_table.data_ptr(), which, width, tables, step
+    return at, None, 0, width, step
 
 
-def _blocks(name, pool, dtypes, last, dev, like=None):
+def _blocks(name, pool, dtypes, last, dev):
     """Address, page stride and head stride (bytes) of a pool's blocks: [pages,
-    heads, *last], dense behind its first two dims; ``like``: a tensor that it
-    must agree with."""
+    heads, *last], dense behind its first two dims."""
     shape = pool.shape
     if pool.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {pool.dtype}")
@@ -786,41 +802,40 @@ def _blocks(name, pool, dtypes, last, dev, like=None):
         raise ValueError(f"{name} must be dense behind its first two dims")
     if pool.get_device() != dev:
         raise _elsewhere(name, pool, dev)
-    if like is not None and (shape[:2] != like.shape[:2] or pool.dtype is not like.dtype):
-        raise ValueError(f"{name} must be of the keys' pages, heads and type")
+    block = last[0] * last[1] if len(last) == 2 else last[0]
     size = pool.element_size()
-    block = 1
-    for n in last:
-        block *= n
     return pool.data_ptr(), (step[0] if shape[0] > 1 else max(step[0], block)) * size, step[1] * size
+
+
+def _alike(name, pool, first, dev) -> int:
+    """Address of a pool of the same type, shape and strides as the one before."""
+    if pool.dtype is not first.dtype or pool.shape != first.shape:
+        raise ValueError(f"{name} must be {first.dtype} {list(first.shape)}, as the one before it")
+    if pool.stride() != first.stride():
+        raise ValueError(f"{name} must have the strides of the one before it")
+    if pool.get_device() != dev:
+        raise _elsewhere(name, pool, dev)
+    return pool.data_ptr()
 
 
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 _BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
 
 
 def _kv_pools(fp8, k_pages, v_pages, scales, dim, dev):
-    """Addresses of the pools ([keys, values, their scales]) and their strides."""
-    block = (PAGE_POSITIONS, dim)
-    kv, page, head = _blocks("k_pages", k_pages, _FP8 if fp8 else _BF16, block, dev)
-    where, strides = [kv], [page, head]
-    if v_pages is not None:
-        v, *same = _blocks("v_pages", v_pages, _FP8 if fp8 else _BF16, block, dev, k_pages)
-        if same != strides:
-            raise ValueError("k_pages and v_pages must have the same strides")
-        where.append(v)
-    if fp8:
-        first = None
-        for name, scale in zip(("kscale", "vscale"), scales):
-            s, *same = _blocks(name, scale, (torch.float32,), (PAGE_POSITIONS,), dev)
-            if scale.shape[:2] != k_pages.shape[:2]:
-                raise ValueError(f"{name} must be of the keys' pages and heads")
-            if first is not None and same != first:
-                raise ValueError("kscale and vscale must have the same strides")
-            first = same
-            where.append(s)
-        strides += first
-    return where, strides
+    """Addresses of the pools (keys, values, their scales) and their strides."""
+    kv, page, head = _blocks("k_pages", k_pages, _FP8 if fp8 else _BF16, (PAGE_POSITIONS, dim), dev)
+    where = (kv,) if v_pages is None else (kv, _alike("v_pages", v_pages, k_pages, dev))
+    if not fp8:
+        return where, (page, head)
+    kscale = scales[0]
+    at, *strides = _blocks("kscale", kscale, _F32, (PAGE_POSITIONS,), dev)
+    if kscale.shape[:2] != k_pages.shape[:2]:
+        raise ValueError("kscale must be of the keys' pages and heads")
+    if v_pages is None:
+        return where + (at,), (page, head, *strides)
+    return where + (at, _alike("vscale", scales[1], kscale, dev)), (page, head, *strides)
 
 
 def _num_pages(num_pages, pool):
@@ -844,45 +859,35 @@ def idx_plan_batch(cached, added, free_pages, page_table, slots=None, positions=
     length 0), ``starts`` int64 [requests + 1] each request's first row, ``taken``
     int64 [1] the pages asked for.  Those that are None are not written.
     """
-    dev = cached.get_device()
-    requests = cached.shape[0] if cached.dim() == 1 else -1
-    have = _dense("cached", cached, torch.int32, (requests,), dev)
-    more = _dense("added", added, torch.int32, (requests,), dev)
+    dev, requests = cached.get_device(), cached.numel()
+    have = _flat("cached", cached, torch.int32, requests, dev)
+    more = _flat("added", added, torch.int32, requests, dev)
     num_free = free_pages.numel()
-    free = _dense("free_pages", free_pages, torch.int32, (num_free,), dev)
-    if page_table.dim() != 2 or page_table.shape[0] != requests:
-        raise ValueError(f"page_table must be [{requests}, width], got {list(page_table.shape)}")
-    if page_table.dtype is not torch.int32:
-        raise ValueError(f"page_table must be torch.int32, got {page_table.dtype}")
-    width = page_table.shape[1]
-    step, unit = page_table.stride()
-    if unit != 1 and width > 1:
-        raise ValueError("page_table must be unit-stride along its last dim")
-    if page_table.get_device() != dev:
-        raise _elsewhere("page_table", page_table, dev)
-    n, rows = None, []
-    for name, x, dtype in (("slots", slots, torch.int64), ("positions", positions, torch.int64),
-                           ("row_table", row_table, torch.int32), ("seqlens", seqlens, torch.int32)):
-        if x is None:
-            rows.append(None)
-            continue
-        n = x.numel() if n is None else n
-        rows.append(_dense(name, x, dtype, (n,), dev))
-    begin = None if starts is None else _dense("starts", starts, torch.int64, (requests + 1,), dev)
-    count = None if taken is None else _dense("taken", taken, torch.int64, (1,), dev)
-    return _launch(_lib.idx_plan_batch, dev, stream, check, have, more, requests, free, num_free, page_table.data_ptr(),
-                   width, step if requests > 1 else width, n or 0, *rows, begin, count)
+    free = _flat("free_pages", free_pages, torch.int32, num_free, dev)
+    table, tables, width, step = _grid("page_table", page_table, dev)
+    if tables != requests:
+        raise ValueError(f"page_table holds {tables} tables for {requests} requests")
+    first = slots if slots is not None else positions if positions is not None else row_table if row_table is not None else seqlens
+    n = 0 if first is None else first.numel()
+    rows = (None if slots is None else _flat("slots", slots, torch.int64, n, dev),
+            None if positions is None else _flat("positions", positions, torch.int64, n, dev),
+            None if row_table is None else _flat("row_table", row_table, torch.int32, n, dev),
+            None if seqlens is None else _flat("seqlens", seqlens, torch.int32, n, dev),
+            None if starts is None else _flat("starts", starts, torch.int64, requests + 1, dev),
+            None if taken is None else _flat("taken", taken, torch.int64, 1, dev))
+    return _launch(_lib.idx_plan_batch, dev, stream, check, have, more, requests, free, num_free, table, width,
+                   step if requests > 1 else width, n, *rows)
 
 
 def _store_kv(fn, fp8, keys, values, slots, k_pages, v_pages, scales, num_pages, stream, check):
     k_step, dev = _rows("keys", keys, 3), keys.get_device()
-    v_step = _rows("values", values, 3)
-    n, heads, dim = keys.shape
-    if values.shape != keys.shape:
-        raise ValueError(f"values must be {list(keys.shape)}, got {list(values.shape)}")
+    v_step, shape = _rows("values", values, 3), keys.shape
+    n, heads, dim = shape
+    if values.shape != shape:
+        raise ValueError(f"values must be {list(shape)}, got {list(values.shape)}")
     if values.get_device() != dev:
         raise _elsewhere("values", values, dev)
-    at = _dense("slots", slots, torch.int64, (n,), dev)
+    at = _flat("slots", slots, torch.int64, n, dev)
     where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
     if k_pages.shape[1] != heads:
         raise ValueError(f"k_pages must have {heads} heads, got {k_pages.shape[1]}")
@@ -912,18 +917,19 @@ def idx_store_kv_bf16(keys, values, slots, k_pages, v_pages, *, num_pages=None, 
 
 def _page_bounds(fn, fp8, k_pages, kscale, page_table, seqlens, bounds, first, row_table, num_pages, stream, check):
     dev = seqlens.get_device()
-    rows = seqlens.shape[0] if seqlens.dim() == 1 else -1
-    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
-    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
-    dim = k_pages.shape[-1]
+    rows = seqlens.numel()
+    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
+    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
+    shape, near = k_pages.shape, bounds.shape
+    dim = shape[-1]
     where, strides = _kv_pools(fp8, k_pages, None, (kscale,), dim, dev)
-    heads, pages = k_pages.shape[1], _num_pages(num_pages, k_pages)
-    if bounds.dim() != 4 or bounds.shape[0] < pages:
-        raise ValueError(f"bounds must be [{pages}, {heads}, 2, {dim}], got {list(bounds.shape)}")
-    to = _dense("bounds", bounds, torch.bfloat16, (bounds.shape[0], heads, 2, dim), dev)
-    begin = None if first is None else _dense("first", first, torch.int32, (rows,), dev)
-    return _launch(fn, dev, stream, check, *where, table, which, 0 if which is None else tables, begin, lengths, to, rows,
-                   heads, dim, width, pages, *strides, step)
+    heads, pages = shape[1], _num_pages(num_pages, k_pages)
+    if len(near) != 4 or near[0] < pages or near[1:] != (heads, 2, dim):
+        raise ValueError(f"bounds must be [{pages}, {heads}, 2, {dim}], got {list(near)}")
+    to = _flat("bounds", bounds, torch.bfloat16, bounds.numel(), dev)
+    begin = None if first is None else _flat("first", first, torch.int32, rows, dev)
+    return _launch(fn, dev, stream, check, *where, table, which, tables, begin, lengths, to, rows, heads, dim, width, pages,
+                   *strides, step)
 
 
 def idx_page_bounds_fp8(k_pages, kscale, page_table, seqlens, bounds, *, first=None, row_table=None, num_pages=None,
@@ -957,16 +963,15 @@ def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *,
     ``scores.flatten(0, 1)`` and ``page_counts.flatten()`` are what
     :func:`idx_topk_logits` selects pages from (score rows a multiple of 4 apart).
     """
-    dev, shape = q.get_device(), q.shape
-    if len(shape) != 3 or bounds.dim() != 4:
-        raise ValueError(f"q must be [rows, heads, D] and bounds [pages, kv_heads, 2, D], got {list(shape)} and "
-                         f"{list(bounds.shape)}")
+    dev, shape, near = q.get_device(), q.shape, bounds.shape
+    if len(shape) != 3 or len(near) != 4 or near[2] != 2 or near[3] != shape[2]:
+        raise ValueError(f"q must be [rows, heads, D] and bounds [pages, kv_heads, 2, D], got {list(shape)} and {list(near)}")
     rows, heads, dim = shape
-    pages, kv_heads = bounds.shape[:2]
-    from_q = _dense("q", q, torch.bfloat16, shape, dev)
-    near = _dense("bounds", bounds, torch.bfloat16, (pages, kv_heads, 2, dim), dev)
-    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
-    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
+    pages, kv_heads = near[:2]
+    from_q = _flat("q", q, torch.bfloat16, rows * heads * dim, dev)
+    at = _flat("bounds", bounds, torch.bfloat16, bounds.numel(), dev)
+    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
+    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
     if scores.dtype is not torch.float32:
         raise ValueError(f"scores must be torch.float32, got {scores.dtype}")
     if scores.shape != (rows, kv_heads, width):
@@ -977,10 +982,9 @@ def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *,
     apart = head if kv_heads > 1 else row if rows > 1 else width
     if (unit != 1 and width > 1) or (rows > 1 and kv_heads > 1 and row != kv_heads * head):
         raise ValueError("scores must be unit-stride along its last dim, its rows evenly apart")
-    counts = None if page_counts is None else _dense("page_counts", page_counts, torch.int32, (rows, kv_heads), dev)
-    return _launch(_lib.idx_page_scores, dev, stream, check, from_q, near, table, which, 0 if which is None else tables,
-                   lengths, scores.data_ptr(), counts, rows, heads, kv_heads, dim, width, pages, step, apart, first_pages,
-                   last_pages)
+    counts = None if page_counts is None else _flat("page_counts", page_counts, torch.int32, rows * kv_heads, dev)
+    return _launch(_lib.idx_page_scores, dev, stream, check, from_q, at, table, which, tables, lengths, scores.data_ptr(),
+                   counts, rows, heads, kv_heads, dim, width, pages, step, apart, first_pages, last_pages)
 
 
 def idx_kv_attention_workspace(rows, num_heads, kv_heads, head_dim, table_width, k=None) -> int:
@@ -995,25 +999,22 @@ def _kv_attention(fn, fp8, q, k_pages, v_pages, scales, page_table, page_idx, se
     if len(shape) != 3 or out.shape != shape:
         raise ValueError(f"q and out must be [rows, heads, D], got {list(shape)} and {list(out.shape)}")
     rows, heads, dim = shape
-    from_q = _dense("q", q, torch.bfloat16, shape, dev)
-    to = _dense("out", out, torch.bfloat16, shape, dev)
+    size = rows * heads * dim
+    from_q = _flat("q", q, torch.bfloat16, size, dev)
+    to = _flat("out", out, torch.bfloat16, size, dev)
     where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
     kv_heads = k_pages.shape[1]
-    table, which, width, tables, step = _table(page_table, rows, row_table, dev)
-    lengths = _dense("seqlens", seqlens, torch.int32, (rows,), dev)
+    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
+    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
     idx = sink = log = None
     k = -1
     if page_idx is not None:
-        if page_idx.dim() == 2 and page_idx.shape[0] == rows * kv_heads:  # (as the top-k's rows)
-            k = page_idx.shape[1]
-            idx = _dense("page_idx", page_idx, torch.int32, (rows * kv_heads, k), dev)
-        else:
-            k = page_idx.shape[-1] if page_idx.dim() == 3 else 0
-            idx = _dense("page_idx", page_idx, torch.int32, (rows, kv_heads, k), dev)
+        k = page_idx.shape[-1]
+        idx = _flat("page_idx", page_idx, torch.int32, rows * kv_heads * k, dev)
     if sinks is not None:
-        sink = _dense("sinks", sinks, torch.float32, (heads,), dev)
+        sink = _flat("sinks", sinks, torch.float32, heads, dev)
     if lse is not None:
-        log = _dense("lse", lse, torch.float32, (rows, heads), dev)
+        log = _flat("lse", lse, torch.float32, rows * heads, dev)
     if workspace is None:
         workspace = _workspace(_lib.idx_kv_attention_workspace, (rows, heads, kv_heads, dim, width, k), dev, stream)
     elif not workspace.is_contiguous():
@@ -1021,9 +1022,8 @@ def _kv_attention(fn, fp8, q, k_pages, v_pages, scales, page_table, page_idx, se
     elif workspace.get_device() != dev:
         raise _elsewhere("workspace", workspace, dev)
     space, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    return _launch(fn, dev, stream, check, from_q, *where, table, which, 0 if which is None else tables, idx, lengths, sink,
-                   to, log, rows, heads, kv_heads, dim, width, _num_pages(num_pages, k_pages), *strides, step, k, scale,
-                   space, nbytes)
+    return _launch(fn, dev, stream, check, from_q, *where, table, which, tables, idx, lengths, sink, to, log, rows, heads,
+                   kv_heads, dim, width, _num_pages(num_pages, k_pages), *strides, step, k, scale, space, nbytes)
 
 
 def idx_kv_attention_fp8(q, k_pages, v_pages, kscale, vscale, page_table, page_idx, seqlens, out, lse=None, *, scale,

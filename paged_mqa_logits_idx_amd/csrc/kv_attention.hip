@@ -102,17 +102,21 @@ struct AttendShared {
   float scale[kWaves][2][KEY == kFp8 ? F::kTile : 4];
   f32x2 ml[kWaves][16 * NT];
   int32_t sums[kWaves];
-  int32_t start[3];
+  int32_t start[2];
 };
 
-// The pages of a row's units.
-__device__ __forceinline__ int32_t live_pages(const Attend& a, int64_t b) {
-  const int64_t L = min((int64_t)max(a.sl[b], 0), (int64_t)a.width * kPage);
-  return (int32_t)((L + kPage - 1) / kPage);
+// A row's length, and the pages of its units.
+__device__ __forceinline__ int32_t length_of(const Attend& a, int64_t b) {
+  return min(max(a.sl[b], 0), a.width * kPage);
 }
-__device__ __forceinline__ int32_t pages_of(const Attend& a, int64_t b) {
-  const int32_t c = live_pages(a, b);
+__device__ __forceinline__ int32_t pages_of(const Attend& a, int32_t L) {
+  const int32_t c = (int32_t)(((uint32_t)L + kPage - 1) / kPage);
   return a.k >= 0 ? min(a.k, c) : c;
+}
+
+// The pages of a workgroup's share.
+__device__ __forceinline__ int32_t share_pages(int32_t total, int32_t shares) {
+  return max((int32_t)(((uint32_t)total + (uint32_t)shares - 1) / (uint32_t)shares), kMinShare);
 }
 
 template <int KEY, int DIM, int NT>
@@ -128,59 +132,83 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
   // The workgroup's share: pages [at, end) of the units' in order, from page
   // `page0` of unit `unit` of row `b`.
   int64_t b;
-  int32_t unit, page0 = 0, count, at = 0, end;
+  int32_t unit, page0 = 0, count, at = 0, end, L;
   if (a.shares == 0) {
     b = blockIdx.x / (uint32_t)per_row;
     unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
-    count = end = pages_of(a, b);
+    L = length_of(a, b);
+    count = end = pages_of(a, L);
   } else {
-    const int32_t per = (a.rows + kThreads - 1) / kThreads;
-    const int32_t r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
-    int32_t own = 0;
-    for (int32_t r = r0; r < r1; ++r) own += pages_of(a, r);
-    int32_t upto = own;
+    const auto share_of = [&](int32_t total) {
+      const int32_t share = share_pages(total, a.shares);
+      at = (int32_t)min((int64_t)blockIdx.x * share, (int64_t)total);
+      end = min(at + share, total);
+    };
+    if (a.rows <= 64) {  // every wave by itself, a lane a row
+      const int32_t mine = lane < a.rows ? length_of(a, lane) : 0, own = pages_of(a, mine);
+      int32_t upto = own;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int32_t v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
-    if (lane == 63) sh.sums[wave] = upto;
-    if (threadIdx.x == 0) sh.start[0] = -1;
-    __syncthreads();
-    int32_t total = 0;
+      for (int d = 1; d < 64; d *= 2) {
+        const int32_t v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+      }
+      if (blockIdx.x == 0 && wave == 0) {
+        if (lane < a.rows) a.prefix[lane] = upto - own;
+        if (lane == 63) a.prefix[a.rows] = upto;
+      }
+      share_of(__builtin_amdgcn_readlane(upto, 63) * per_row);
+      if (at >= end) return;
+      const int row = __builtin_ctzll(__ballot(upto * per_row > at));
+      b = row;
+      count = __builtin_amdgcn_readlane(own, row);
+      L = __builtin_amdgcn_readlane(mine, row);
+      page0 = at - (__builtin_amdgcn_readlane(upto, row) - count) * per_row;
+    } else {
+      const int32_t per = (a.rows + kThreads - 1) / kThreads;
+      const int32_t r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+      int32_t own = 0;
+      for (int32_t r = r0; r < r1; ++r) own += pages_of(a, length_of(a, r));
+      int32_t upto = own;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) upto += sh.sums[w];
-      total += sh.sums[w];
-    }
-    if (blockIdx.x == 0) {
-      int32_t p = upto - own;
-      for (int32_t r = r0; r < r1; ++r) {
-        a.prefix[r] = p;
-        p += pages_of(a, r);
+      for (int d = 1; d < 64; d *= 2) {
+        const int32_t v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
       }
-      if (threadIdx.x == 0) a.prefix[a.rows] = total;
-    }
-    total *= per_row;
-    const int32_t share = max((total + a.shares - 1) / a.shares, kMinShare);
-    at = (int32_t)min((int64_t)blockIdx.x * share, (int64_t)total);
-    end = min(at + share, total);
-    if (at >= end) return;
-    if (at < upto * per_row && at >= (upto - own) * per_row) {
-      int32_t p = (upto - own) * per_row, r = r0, c = pages_of(a, r);
-      while (at >= p + c * per_row) {
-        p += c * per_row;
-        c = pages_of(a, ++r);
+      if (lane == 63) sh.sums[wave] = upto;
+      __syncthreads();
+      int32_t total = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) upto += sh.sums[w];
+        total += sh.sums[w];
       }
-      sh.start[0] = r;
-      sh.start[1] = (at - p) / c;
-      sh.start[2] = (at - p) % c;
+      if (blockIdx.x == 0) {
+        int32_t p = upto - own;
+        for (int32_t r = r0; r < r1; ++r) {
+          a.prefix[r] = p;
+          p += pages_of(a, length_of(a, r));
+        }
+        if (threadIdx.x == 0) a.prefix[a.rows] = total;
+      }
+      share_of(total * per_row);
+      if (at >= end) return;
+      if (at < upto * per_row && at >= (upto - own) * per_row) {
+        int32_t p = (upto - own) * per_row, r = r0, c = pages_of(a, length_of(a, r));
+        while (at >= p + c * per_row) {
+          p += c * per_row;
+          c = pages_of(a, length_of(a, ++r));
+        }
+        sh.start[0] = r;
+        sh.start[1] = at - p;
+      }
+      __syncthreads();
+      b = uniform(sh.start[0]);
+      page0 = uniform(sh.start[1]);
+      L = uniform(length_of(a, b));
+      count = pages_of(a, L);
     }
-    __syncthreads();
-    b = uniform(sh.start[0]);
-    unit = uniform(sh.start[1]);
-    page0 = uniform(sh.start[2]);
-    count = uniform(pages_of(a, b));
+    unit = page0 / count;
+    page0 -= unit * count;
   }
 
   const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[wave][0][0];
@@ -198,8 +226,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
     const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
     const int32_t head0 = h * a.group + hb * 16 * NT;                 // of the row's
     const int32_t heads = min(16 * NT, a.group - hb * 16 * NT);
-    const int32_t L = (int32_t)min((int64_t)max(a.sl[b], 0), (int64_t)a.width * kPage);
-    const int32_t live = (int32_t)(((int64_t)L + kPage - 1) / kPage);
+    const int32_t live = (int32_t)(((uint32_t)L + kPage - 1) / kPage);
     bool table_ok;
     const int32_t* tab = a.tables.of(b, table_ok);
     const int32_t* list = a.k >= 0 ? a.idx + (b * a.kv_heads + h) * (int64_t)a.k : nullptr;
@@ -478,69 +505,101 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
     page0 = 0;
     if (++unit == per_row) {
       unit = 0;
-      do count = uniform(pages_of(a, ++b));
-      while (count == 0);
+      do {
+        L = uniform(length_of(a, ++b));
+        count = pages_of(a, L);
+      } while (count == 0);
     }
   }
 }
 
-// Joins the pieces of a unit, a wave 16 values of 16 heads; writes the units that
-// have no pages.  The pieces' order is fixed, so the result does not depend on
-// their timing.
-constexpr int kBatch = 8;
-
-template <int DIM, int NT>
-__global__ __launch_bounds__(64) void kv_join_kernel(Attend a) {
-  constexpr int kParts = DIM / 16;
-  const int lane = threadIdx.x, n = lane & 15, quad = lane >> 4;
+// Joins the pieces of a unit, and writes the units that have no pages: blocks of 16
+// values of 16 heads, kParts * NT of them a unit.  Many units: a workgroup a unit, its
+// waves take the blocks in turn.  FEW: a workgroup a block, its waves take the pieces in
+// turn and join what they have through LDS.  The order is fixed, so the result
+// does not depend on the pieces' timing.
+template <int DIM, int NT, bool FEW>
+__global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
+  constexpr int kParts = DIM / 16, kBatch = FEW ? 16 : 4, kEvery = FEW ? kWaves : 1;
+  __shared__ f32x4 outs[FEW ? kWaves : 1][64];
+  __shared__ f32x2 mls[FEW ? kWaves : 1][16];
+  const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
+  const int wave = uniform(threadIdx.x >> 6);
   const int32_t per_row = a.kv_heads * a.blocks;
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)per_row), unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
-  const int t = (int)blockIdx.y / kParts, p = (int)blockIdx.y % kParts;
   const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
-  const int32_t before = a.prefix[b], count = a.prefix[b + 1] - before, total_pages = a.prefix[a.rows] * per_row;
-  const int32_t share = max((total_pages + a.shares - 1) / a.shares, kMinShare);
+  const int32_t before = a.prefix[b], count = a.prefix[b + 1] - before;
+  const int32_t share = share_pages(a.prefix[a.rows] * per_row, a.shares);
   const int32_t s = before * per_row + unit * count;  // the unit's pages: s .. s + count
   const int32_t w0 = s / share, w1 = count > 0 ? (s + count - 1) / share : w0 - 1;
   if (w0 == w1) return;  // whole
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  float top = -INFINITY, total = 0.0f;
+  for (int block = FEW ? (int)blockIdx.y : wave; block < NT * kParts; block += FEW ? NT * kParts : kWaves) {
+    const int t = block / kParts, p = block % kParts;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float top = -INFINITY, total = 0.0f;
 #pragma unroll 1
-  for (int32_t w = w0; w <= w1; w += kBatch) {
-    f32x2 ml[kBatch];
-    f32x4 v[kBatch];
+    for (int32_t w = FEW ? w0 + wave : w0; w <= w1; w += kBatch * kEvery) {
+      f32x2 ml[kBatch];
+      f32x4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      ml[i] = (f32x2){-INFINITY, 0.0f};
-      v[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      if (w + i <= w1) {
-        const int64_t piece = 2 * (int64_t)(w + i) + (w + i == w0 && s != w0 * share ? 1 : 0);
-        ml[i] = a.ml[piece * 16 * NT + 16 * t + n];
-        v[i] = a.part[((piece * NT + t) * kParts + p) * 64 + lane];
+      for (int i = 0; i < kBatch; ++i) {
+        const int32_t x = w + i * kEvery;
+        ml[i] = (f32x2){-INFINITY, 0.0f};
+        v[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        if (x <= w1) {
+          const int64_t piece = 2 * (int64_t)x + (x == w0 && s != w0 * share ? 1 : 0);
+          ml[i] = a.ml[piece * 16 * NT + 16 * t + n];
+          v[i] = a.part[((piece * NT + t) * kParts + p) * 64 + lane];
+        }
+      }
+      float to = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) to = fmaxf(to, ml[i].x);
+      const float base = to == -INFINITY ? 0.0f : to, by = __builtin_amdgcn_exp2f(top - base);
+      top = to;
+      total *= by;
+      o *= by;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - base);
+        total = fmaf(ml[i].y, f, total);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(v[i][e], f, o[e]);
       }
     }
-    float to = top;
+    if constexpr (FEW) {
+      outs[wave][lane] = o;
+      if (quad == 0) mls[wave][n] = (f32x2){top, total};
+      __syncthreads();
+      if (wave != 0) return;
+      f32x2 ml[kWaves];
+      top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) to = fmaxf(to, ml[i].x);
-    const float base = to == -INFINITY ? 0.0f : to, by = __builtin_amdgcn_exp2f(top - base);
-    top = to;
-    total *= by;
-    o *= by;
+      for (int w = 0; w < kWaves; ++w) {
+        ml[w] = mls[w][n];
+        top = fmaxf(top, ml[w].x);
+      }
+      const float base = top == -INFINITY ? 0.0f : top;
+      o = (f32x4){0.f, 0.f, 0.f, 0.f};
+      total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float f = __builtin_amdgcn_exp2f(ml[i].x - base);
-      total = fmaf(ml[i].y, f, total);
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w].x - base);
+        total = fmaf(ml[w].y, f, total);
+        const f32x4 v = outs[w][lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = fmaf(v[i][e], f, o[e]);
+        for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], f, o[e]);
+      }
     }
+    const int32_t i = hb * 16 * NT + 16 * t + n;
+    if (i >= a.group) continue;
+    const int32_t head = h * a.group + i;
+    const Closing c = close_sum(top, total, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
+    o = o * c.by * c.half * c.half;
+    *reinterpret_cast<bf16x4*>(a.out + (((int64_t)b * a.heads + head) * DIM + 16 * p + 4 * quad) * 2) =
+        (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+    if (a.lse && p == 0 && quad == 0) a.lse[(int64_t)b * a.heads + head] = c.lse;
   }
-  const int32_t i = hb * 16 * NT + 16 * t + n;
-  if (i >= a.group) return;
-  const int32_t head = h * a.group + i;
-  const Closing c = close_sum(top, total, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
-  o = o * c.by * c.half * c.half;
-  *reinterpret_cast<bf16x4*>(a.out + (((int64_t)b * a.heads + head) * DIM + 16 * p + 4 * quad) * 2) =
-      (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-  if (a.lse && p == 0 && quad == 0) a.lse[(int64_t)b * a.heads + head] = c.lse;
 }
 
 // ---------------------------------------------------------------------------
@@ -584,7 +643,9 @@ template <int KEY, int DIM, int NT>
 void launch(const Attend& a, const Split& split, hipStream_t stream) {
   const uint32_t units = (uint32_t)((int64_t)a.rows * a.kv_heads * a.blocks);
   kv_attention_kernel<KEY, DIM, NT><<<dim3(split.shares ? (uint32_t)split.shares : units), dim3(kThreads), 0, stream>>>(a);
-  if (split.shares) kv_join_kernel<DIM, NT><<<dim3(units, NT * DIM / 16), dim3(64), 0, stream>>>(a);
+  if (split.shares == 0) return;
+  if (split.shares >= 8 * (int64_t)units) kv_join_kernel<DIM, NT, true><<<dim3(units, NT * DIM / 16), dim3(kThreads), 0, stream>>>(a);
+  else kv_join_kernel<DIM, NT, false><<<dim3(units), dim3(kThreads), 0, stream>>>(a);
 }
 
 template <int KEY, int DIM>

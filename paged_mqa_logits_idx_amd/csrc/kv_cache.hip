@@ -226,6 +226,20 @@ __device__ __forceinline__ uint32_t outwards(float v) {
   return ((bits >> 31 != 0) == UP ? bits : bits + 0xffffu) >> 16;
 }
 
+// f over the lanes whose number is the same modulo LP, in all of them: turns of a row
+// of 16 as operands of the arithmetic itself, then rows and halves of the wave.
+template <int LP, class F>
+__device__ __forceinline__ float fold_apart(float v, F f) {
+  if constexpr (LP <= 4) v = f(v, row_lane<0x124>(v));  // row_ror 4
+  if constexpr (LP <= 8) v = f(v, row_lane<0x128>(v));  // row_ror 8
+  if constexpr (LP <= 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // A wave takes a page of a head: a lane 16 bytes of a position, 1024 bytes of the
 // block a load, all of the block's loads under way at once; then the lanes that
 // have the same values of other positions.
@@ -234,15 +248,16 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
   constexpr int kPer = KEY == kFp8 ? 16 : 8;  // values of a lane
   constexpr int LP = DIM / kPer, kLoads = LP, kStep = 64 / LP;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t b = blockIdx.y;
+  const int64_t b = blockIdx.x;
   bool table_ok;
   const int32_t* tab = p.tables.of(b, table_ok);
   const int64_t L = min((int64_t)max(p.sl[b], 0), (int64_t)p.width * kPage);
   const int64_t j0 = p.first ? max(p.first[b], 0) / kPage : 0, j1 = (L + kPage - 1) / kPage;
   if (!table_ok || j0 >= j1) return;
   const int64_t items = (j1 - j0) * p.heads;
-  for (int64_t item = (int64_t)blockIdx.x * kWaves + wave; item < items; item += (int64_t)gridDim.x * kWaves) {
-    const int64_t j = j0 + item / p.heads, h = item % p.heads;
+  for (int64_t item = (int64_t)blockIdx.y * kWaves + wave; item < items; item += (int64_t)gridDim.y * kWaves) {
+    const int64_t over = items <= UINT32_MAX ? (uint32_t)item / (uint32_t)p.heads : item / p.heads;
+    const int64_t j = j0 + over, h = item - over * p.heads;
     const int32_t page = tab[j];
     if ((uint32_t)page >= p.pages_lim) continue;
     const int live = (int)min(L - j * kPage, (int64_t)kPage);
@@ -280,12 +295,9 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
       }
     }
 #pragma unroll
-    for (int d = LP; d < 64; d *= 2) {
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        lo[e] = fminf(lo[e], __shfl_xor(lo[e], d));
-        hi[e] = fmaxf(hi[e], __shfl_xor(hi[e], d));
-      }
+    for (int e = 0; e < kPer; ++e) {
+      lo[e] = fold_apart<LP>(lo[e], [](float a, float b) { return fminf(a, b); });
+      hi[e] = fold_apart<LP>(hi[e], [](float a, float b) { return fmaxf(a, b); });
     }
     if (lane >= 2 * LP) continue;
     const bool up = lane >= LP;
@@ -322,92 +334,107 @@ struct Scores {
   int32_t rows, heads, kv_heads, width, first, last;
 };
 
-constexpr int kScoreTiles = 2;                                // of 16 pages a wave
-constexpr int kScorePages = 16 * kScoreTiles * kWaves;        // pages of a workgroup
+constexpr int kScoreTiles = 2;  // a wave's of a unit
 
 // max(q lo, q hi) is q hi where q is positive and q lo where it is negative, so the
 // sum is a product of [min(q, 0), max(q, 0)] with [lo, hi]: bf16 matrix instructions
-// with exact products and float32 sums.  A wave takes 16 * kScoreTiles pages, whose
-// bounds a lane loads as the B operand (16 bytes of a page each), against 16 query
-// heads at a time; a lane then has 4 heads of a page.
+// with exact products and float32 sums.  A row's tiles are 16 pages of a head, heads
+// first, whose bounds stand side by side; a unit is kScoreTiles * kWaves of them.  A
+// lane loads 16 bytes of a page each as the B operand, against 16 query heads at a
+// time, and then has 4 heads of a page.  Workgroups go round the units, the next
+// one's page ids on their way while one is worked on.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
   constexpr int kSteps = DIM / 32;
   const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t group = p.heads / p.kv_heads;
-  for (int64_t unit = blockIdx.x; unit < (int64_t)p.rows * p.kv_heads * p.blocks; unit += gridDim.x) {
-    const int64_t bh = unit / p.blocks, block = unit - bh * p.blocks;
-    const int64_t b = bh / p.kv_heads;
-    const int32_t h = (int32_t)(bh - b * p.kv_heads);
+  const int64_t units = (int64_t)p.rows * p.blocks;
+  struct Unit {
+    int64_t b;
+    int32_t count;             // live pages of the row
+    int32_t head[kScoreTiles], j[kScoreTiles], page[kScoreTiles];  // the lane's (page -1: none)
+  };
+  const auto ask = [&](int64_t unit) {
+    Unit u;
+    u.b = units <= UINT32_MAX ? (uint32_t)unit / (uint32_t)p.blocks : unit / p.blocks;
+    const int32_t L = p.sl[u.b];
     bool table_ok;
-    const int32_t* tab = p.tables.of(b, table_ok);
-    const int64_t L = min((int64_t)max(p.sl[b], 0), (int64_t)p.width * kPage);
-    const int32_t count = (int32_t)((L + kPage - 1) / kPage);
-    if (p.counts && block == 0 && threadIdx.x == 0) p.counts[bh] = count;
-    const int64_t j0 = block * kScorePages + wave * 16 * kScoreTiles + n;  // the lane's first page
-    float best[kScoreTiles];
-    if (j0 - n < count) {
-      bf16x8 side[kScoreTiles][2][kSteps];
-      bool ok[kScoreTiles];
+    const int32_t* tab = p.tables.of(u.b, table_ok);
+#pragma unroll
+    for (int t = 0; t < kScoreTiles; ++t) {
+      const int64_t tile = (unit - u.b * p.blocks) * (kScoreTiles * kWaves) + kScoreTiles * wave + t;
+      const int32_t at = (int32_t)((uint32_t)tile / (uint32_t)p.kv_heads);
+      u.head[t] = (int32_t)tile - at * p.kv_heads;
+      u.j[t] = 16 * at + n;
+      u.page[t] = u.j[t] < p.width && table_ok ? tab[u.j[t]] : -1;  // (before the length is there)
+    }
+    u.count = min((max(L, 0) - 1) / kPage + (L > 0), p.width);
+    return u;
+  };
+  Unit next = ask(blockIdx.x);
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const Unit u = next;
+    const bool any = u.j[0] - n < u.count;  // (a wave's later tiles are no earlier)
+    u32x4 q[kScoreTiles][kSteps];
+    bf16x8 side[kScoreTiles][2][kSteps];
+    bool ok[kScoreTiles];
+    // query heads 16 * i of a tile's key head (past the group's last: its last)
+    const auto queries = [&](int t, int32_t i) {
+      return p.q + ((u.b * p.heads + (int64_t)u.head[t] * group + min(i + n, group - 1)) * DIM + 8 * quad) * 2;
+    };
+    if (any) {
 #pragma unroll
       for (int t = 0; t < kScoreTiles; ++t) {
-        const int64_t j = j0 + 16 * t;
-        const int32_t page = j < count && table_ok ? tab[j] : -1;
-        ok[t] = (uint32_t)page < p.pages_lim;
-        const uint8_t* from = p.bounds + (((int64_t)(ok[t] ? page : 0) * p.kv_heads + h) * 2 * DIM + 8 * quad) * 2;
+        ok[t] = (uint32_t)u.page[t] < p.pages_lim && u.j[t] < u.count;
+        const uint8_t* from = p.bounds + (((int64_t)(ok[t] ? u.page[t] : 0) * p.kv_heads + u.head[t]) * 2 * DIM + 8 * quad) * 2;
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int s = 0; s < kSteps; ++s)
             side[t][w][s] = ok[t] ? *reinterpret_cast<const bf16x8*>(from + (w * DIM + 32 * s) * 2) : (bf16x8)((__bf16)0.0f);
-        best[t] = -INFINITY;
-      }
-      for (int32_t i0 = 0; i0 < group; i0 += 16) {
-        // (heads past the group's last are its last)
-        const uint8_t* from = p.q + ((b * p.heads + (int64_t)h * group + min(i0 + n, group - 1)) * DIM + 8 * quad) * 2;
-        f32x4 acc[kScoreTiles];
 #pragma unroll
-        for (int t = 0; t < kScoreTiles; ++t) acc[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const u32x4 q = *reinterpret_cast<const u32x4*>(from + 64 * s);
-          u32x4 neg, pos;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t sign = (q[e] >> 15 & 0x00010001u) * 0xffffu;
-            neg[e] = q[e] & sign;
-            pos[e] = q[e] & ~sign;
-          }
-#pragma unroll
-          for (int t = 0; t < kScoreTiles; ++t) {
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, neg), side[t][0][s], acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), side[t][1][s], acc[t], 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < kScoreTiles; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) best[t] = __builtin_elementwise_maximum(best[t], acc[t][e]);  // (a NaN stays)
-      }
-#pragma unroll
-      for (int t = 0; t < kScoreTiles; ++t) {
-        best[t] = __builtin_elementwise_maximum(best[t], __shfl_xor(best[t], 16));
-        best[t] = __builtin_elementwise_maximum(best[t], __shfl_xor(best[t], 32));
-        if (!ok[t]) best[t] = __builtin_nanf("");
+        for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(queries(t, 0) + 64 * s);
       }
     }
+    if (unit + gridDim.x < units) next = ask(unit + gridDim.x);
 #pragma unroll
     for (int t = 0; t < kScoreTiles; ++t) {
-      const int64_t j = j0 + 16 * t;
-      float s = best[t];
-      if (j < p.first || j >= (int64_t)count - p.last) s = INFINITY;
-      if (j >= count) s = -INFINITY;
-      if (quad == t && j < p.width) p.out[bh * p.out_stride + j] = s;
+      float best = -INFINITY;
+      if (any) {
+        for (int32_t i = 0;;) {
+          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            u32x4 neg, pos;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t sign = (q[t][s][e] >> 15 & 0x00010001u) * 0xffffu;
+              neg[e] = q[t][s][e] & sign;
+              pos[e] = q[t][s][e] & ~sign;
+            }
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, neg), side[t][0][s], acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), side[t][1][s], acc, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) best = __builtin_elementwise_maximum(best, acc[e]);  // (a NaN stays)
+          i += 16;
+          if (i >= group) break;
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(queries(t, i) + 64 * s);
+        }
+        best = __builtin_elementwise_maximum(best, __shfl_xor(best, 16));
+        best = __builtin_elementwise_maximum(best, __shfl_xor(best, 32));
+        if (!ok[t]) best = __builtin_nanf("");
+      }
+      if (u.j[t] < p.first || u.j[t] >= (int64_t)u.count - p.last) best = INFINITY;
+      if (u.j[t] >= u.count) best = -INFINITY;
+      const int64_t row = u.b * p.kv_heads + u.head[t];
+      if (quad == 0 && u.j[t] < p.width) p.out[row * p.out_stride + u.j[t]] = best;
+      if (p.counts && quad == 0 && u.j[t] == 0) p.counts[row] = u.count;
     }
   }
 }
-static_assert(kScoreTiles <= 4);  // (a quad of lanes writes a tile)
 
 // ---------------------------------------------------------------------------
 // Host side.
@@ -499,20 +526,13 @@ int page_bounds(const void* k_pages, const float* kscale, const int32_t* page_ta
   p.heads = kv_heads;
   p.width = table_width;
   (void)hipGetLastError();
-  int64_t x = ((int64_t)table_width * kv_heads + kWaves - 1) / kWaves;
+  // (rows first: what a row has of a decode step is its first workgroups', which so are
+  // all dies')
+  int64_t y = ((int64_t)table_width * kv_heads + kWaves - 1) / kWaves;
   const int64_t cap = (8 * (int64_t)device_cu_count() + rows - 1) / rows;
-  if (x > cap) x = cap;
+  if (y > cap) y = cap;
   return for_dim(head_dim, [&](auto dim) {
-    constexpr int kDim = decltype(dim)::value;
-    for (int64_t b = 0; b < rows; b += 65535) {  // (a grid's second side)
-      Bounds part = p;
-      part.sl = p.sl + b;
-      if (p.first) part.first = p.first + b;
-      if (row_table) part.tables.rt = row_table + b;
-      else part.tables.pt = page_table + b * page_table_row_stride;
-      const dim3 grid((uint32_t)x, (uint32_t)(rows - b < 65535 ? rows - b : 65535));
-      page_bounds_kernel<KEY, kDim><<<grid, dim3(kThreads), 0, stream>>>(part);
-    }
+    page_bounds_kernel<KEY, decltype(dim)::value><<<dim3((uint32_t)rows, (uint32_t)y), dim3(kThreads), 0, stream>>>(p);
   });
 }
 
@@ -608,7 +628,8 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
   p.out = scores;
   p.counts = page_counts;
   p.out_stride = score_stride;
-  p.blocks = table_width > 0 ? (table_width + kScorePages - 1) / kScorePages : 1;
+  // (a table without columns has tiles for the counts)
+  p.blocks = ((int64_t)(table_width > 0 ? (table_width + 15) / 16 : 1) * kv_heads + kScoreTiles * kWaves - 1) / (kScoreTiles * kWaves);
   p.pages_lim = pages_limit(num_pages);
   p.rows = rows;
   p.heads = num_heads;
@@ -616,7 +637,8 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
   p.width = table_width;
   p.first = first_pages;
   p.last = last_pages;
-  const int64_t units = (int64_t)rows * kv_heads * p.blocks, cap = (int64_t)1 << 20;
+  if (p.blocks > INT32_MAX / (kScoreTiles * kWaves)) return IDX_ERR_SHAPE;
+  const int64_t units = (int64_t)rows * p.blocks, cap = 4 * device_cu_count();
   const dim3 grid((uint32_t)(units < cap ? units : cap));
   (void)hipGetLastError();
   return for_dim(head_dim, [&](auto dim) {

@@ -188,8 +188,8 @@ def attend(**kw):
 @pytest.mark.parametrize("kw,text", [
     (dict(q=zeros(2, 8, 128, dtype=F32)), "q must be torch.bfloat16"), (dict(out=zeros(2, 8, 64)), "q and out"),
     (dict(q=zeros(2, 1024)), "q and out"), (dict(k_pages=zeros(3, 2, 64, 128, dtype=U8)), "k_pages must be torch.bfloat16"),
-    (dict(k_pages=zeros(3, 2, 64, 64)), "k_pages must be"), (dict(v_pages=zeros(3, 1, 64, 128)), "v_pages must be of"),
-    (dict(v_pages=zeros(3, 4, 64, 128)[:, ::2]), "same strides"), (dict(k_pages=zeros(3, 2, 128, 64).transpose(2, 3)), "dense"),
+    (dict(k_pages=zeros(3, 2, 64, 64)), "k_pages must be"), (dict(v_pages=zeros(3, 1, 64, 128)), "v_pages must be torch.bfloat16"),
+    (dict(v_pages=zeros(3, 4, 64, 128)[:, ::2]), "v_pages must have the strides"), (dict(k_pages=zeros(3, 2, 128, 64).transpose(2, 3)), "dense"),
     (dict(page_table=zeros(2, 4, dtype=I64)), "page_table must be torch.int32"), (dict(page_table=zeros(3, 4, dtype=I32)[:, ::2]), "unit-stride"),
     (dict(q=zeros(3, 8, 128), out=zeros(3, 8, 128), seqlens=zeros(3, dtype=I32)), "2 tables for 3 rows"),
     (dict(seqlens=zeros(3, dtype=I32)), "seqlens must be"), (dict(page_idx=zeros(2, 2, 4, dtype=I64)), "page_idx must be torch.int32"),
@@ -205,7 +205,7 @@ def test_binding_refusals_attention(kw, text):
 
 @pytest.mark.parametrize("kw,text", [
     (dict(cached=zeros(2, dtype=I64)), "cached must be torch.int32"), (dict(added=zeros(3, dtype=I32)), "added must be"),
-    (dict(page_table=zeros(3, 4, dtype=I32)), "page_table must be"), (dict(page_table=zeros(2, 4, dtype=I64)), "page_table must be torch.int32"),
+    (dict(page_table=zeros(3, 4, dtype=I32)), "3 tables for 2 requests"), (dict(page_table=zeros(2, 4, dtype=I64)), "page_table must be torch.int32"),
     (dict(page_table=zeros(2, 8, dtype=I32)[:, ::2]), "unit-stride"), (dict(slots=zeros(4, dtype=I32)), "slots must be torch.int64"),
     (dict(seqlens=zeros(5, dtype=I32)), "seqlens must be"), (dict(starts=zeros(2, dtype=I64)), "starts must be"),
     (dict(taken=zeros(1, dtype=I32)), "taken must be"), (dict(free_pages=zeros(4, dtype=I64)), "free_pages must be"),
@@ -227,8 +227,8 @@ def test_binding_refusals_plan(kw, text):
     (dict(keys=zeros(4, 2, 128, dtype=F32)), "keys must be torch.bfloat16"), (dict(slots=zeros(4, dtype=I32)), "slots must be"),
     (dict(k_pages=zeros(3, 4, 64, 128, dtype=U8), v_pages=zeros(3, 4, 64, 128, dtype=U8), kscale=zeros(3, 4, 64, dtype=F32),
           vscale=zeros(3, 4, 64, dtype=F32)), "k_pages must have 2 heads"),
-    (dict(kscale=zeros(3, 2, 64)), "kscale must be torch.float32"), (dict(vscale=zeros(2, 2, 64, dtype=F32)), "vscale must be of"),
-    (dict(vscale=zeros(3, 2, 128, dtype=F32)[..., :64]), "same strides"), (dict(num_pages=4), "holds 3 pages"),
+    (dict(kscale=zeros(3, 2, 64)), "kscale must be torch.float32"), (dict(vscale=zeros(2, 2, 64, dtype=F32)), "vscale must be torch.float32"),
+    (dict(vscale=zeros(3, 2, 128, dtype=F32)[..., :64]), "vscale must have the strides"), (dict(num_pages=4), "holds 3 pages"),
     (dict(), "must be device tensors"),
 ])
 def test_binding_refusals_store(kw, text):
@@ -257,7 +257,7 @@ def test_binding_refusals_bounds(kw, text):
 
 
 @pytest.mark.parametrize("kw,text", [
-    (dict(q=zeros(2, 1024)), "q must be"), (dict(bounds=zeros(3, 2, 128)), "q must be"), (dict(bounds=zeros(3, 2, 2, 64)), "bounds must be"),
+    (dict(q=zeros(2, 1024)), "q must be"), (dict(bounds=zeros(3, 2, 128)), "q must be"), (dict(bounds=zeros(3, 2, 2, 64)), "q must be"),
     (dict(scores=zeros(2, 2, 4)), "scores must be torch.float32"), (dict(scores=zeros(2, 2, 5, dtype=F32)), "scores must be"),
     (dict(scores=zeros(2, 2, 8, dtype=F32)[..., ::2]), "unit-stride"), (dict(scores=zeros(4, 2, 4, dtype=F32)[::2]), "evenly apart"),
     (dict(page_counts=zeros(2, dtype=I32)), "page_counts must be"), (dict(), "must be device tensors"),
