@@ -619,8 +619,20 @@ bool dims_ok(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t table_wi
          table_width >= 0 && table_width <= kMaxWidth && k >= -1 && (int64_t)rows * num_heads <= kMaxHeads;
 }
 
+// Workgroups of a form that a CU holds.
+int per_cu(int key, int32_t head_dim, int nt) {
+  const auto of = [&](auto d, auto n) {
+    return key == kFp8 ? Form<kFp8, decltype(d)::value, decltype(n)::value>::kPerCu : Form<kBf16, decltype(d)::value, decltype(n)::value>::kPerCu;
+  };
+  const auto with = [&](auto d) {
+    return nt == 1 ? of(d, std::integral_constant<int, 1>{}) : nt == 2 ? of(d, std::integral_constant<int, 2>{}) : of(d, std::integral_constant<int, 4>{});
+  };
+  return head_dim == 64 ? with(std::integral_constant<int, 64>{}) : head_dim == 128 ? with(std::integral_constant<int, 128>{})
+                                                                                   : with(std::integral_constant<int, 256>{});
+}
+
 // From the scalar arguments alone (the lengths are on the device).
-Split split_of(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
+Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
   Split s = {1, 1, 0, 0};
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
@@ -629,7 +641,7 @@ Split split_of(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_d
   s.blocks = (group + 16 * s.nt - 1) / (16 * s.nt);
   const int64_t units = (int64_t)rows * kv_heads * s.blocks;
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
-  const int64_t workgroups = 2 * device_cu_count();
+  const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.nt) * device_cu_count();
   if (units > 4 * workgroups || units * most > INT32_MAX / 2 || most <= kMinShare) return s;
   const int64_t want = (units * most + kMinShare - 1) / kMinShare;
   s.shares = (int)(want < workgroups ? want : workgroups);
@@ -676,7 +688,7 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(page_table, 4) || !aligned(row_table, 4) || !aligned(page_idx, 4) ||
       !aligned(seqlens, 4) || !aligned(sinks, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
     return IDX_ERR_ALIGN;
-  const Split split = split_of(rows, num_heads, kv_heads, head_dim, table_width, k);
+  const Split split = split_of(KEY, rows, num_heads, kv_heads, head_dim, table_width, k);
   if (split.bytes > 0 && !workspace) return IDX_ERR_NULL;
   if (workspace_bytes < split.bytes) return IDX_ERR_SHAPE;
   Attend a;
@@ -722,7 +734,10 @@ int64_t idx_kv_attention_workspace(int32_t rows, int32_t num_heads, int32_t kv_h
   if (!head_dim_ok(head_dim) || !dims_ok(rows, num_heads, kv_heads, table_width, k) ||
       (int64_t)num_heads > (int64_t)kMaxGroup * kv_heads)
     return -1;
-  return split_of(rows, num_heads, kv_heads, head_dim, table_width, k).bytes;
+  // (either key type's call may be made with it)
+  const int64_t one = split_of(kFp8, rows, num_heads, kv_heads, head_dim, table_width, k).bytes;
+  const int64_t two = split_of(kBf16, rows, num_heads, kv_heads, head_dim, table_width, k).bytes;
+  return one > two ? one : two;
 }
 
 int idx_kv_attention_fp8(const void* q, const void* k_pages, const void* v_pages, const float* kscale,

@@ -213,7 +213,7 @@ struct Bounds {
   const int32_t* sl;
   uint8_t* out;          // bf16 [pages][heads][2][D]
   KvStrides s;
-  uint32_t pages_lim;
+  uint32_t pages_lim, side;  // side: a row's workgroups that stand together
   int32_t heads, width;
 };
 
@@ -248,14 +248,14 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
   constexpr int kPer = KEY == kFp8 ? 16 : 8;  // values of a lane
   constexpr int LP = DIM / kPer, kLoads = LP, kStep = 64 / LP;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t b = blockIdx.x;
+  const int64_t b = blockIdx.x / p.side, first = ((int64_t)blockIdx.y * p.side + blockIdx.x % p.side) * kWaves + wave;
   bool table_ok;
   const int32_t* tab = p.tables.of(b, table_ok);
   const int64_t L = min((int64_t)max(p.sl[b], 0), (int64_t)p.width * kPage);
   const int64_t j0 = p.first ? max(p.first[b], 0) / kPage : 0, j1 = (L + kPage - 1) / kPage;
   if (!table_ok || j0 >= j1) return;
   const int64_t items = (j1 - j0) * p.heads;
-  for (int64_t item = (int64_t)blockIdx.y * kWaves + wave; item < items; item += (int64_t)gridDim.y * kWaves) {
+  for (int64_t item = first; item < items; item += (int64_t)gridDim.y * p.side * kWaves) {
     const int64_t over = items <= UINT32_MAX ? (uint32_t)item / (uint32_t)p.heads : item / p.heads;
     const int64_t j = j0 + over, h = item - over * p.heads;
     const int32_t page = tab[j];
@@ -334,15 +334,12 @@ struct Scores {
   int32_t rows, heads, kv_heads, width, first, last;
 };
 
-constexpr int kScoreTiles = 2;  // a wave's of a unit
-
 // max(q lo, q hi) is q hi where q is positive and q lo where it is negative, so the
 // sum is a product of [min(q, 0), max(q, 0)] with [lo, hi]: bf16 matrix instructions
 // with exact products and float32 sums.  A row's tiles are 16 pages of a head, heads
-// first, whose bounds stand side by side; a unit is kScoreTiles * kWaves of them.  A
-// lane loads 16 bytes of a page each as the B operand, against 16 query heads at a
-// time, and then has 4 heads of a page.  Workgroups go round the units, the next
-// one's page ids on their way while one is worked on.
+// first, whose bounds stand side by side; a wave takes one.  A lane loads 16 bytes of a
+// page each as the B operand, against 16 query heads at a time, and then has 4 heads
+// of a page.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
   constexpr int kSteps = DIM / 32;
@@ -350,89 +347,61 @@ __global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t group = p.heads / p.kv_heads;
   const int64_t units = (int64_t)p.rows * p.blocks;
-  struct Unit {
-    int64_t b;
-    int32_t count;             // live pages of the row
-    int32_t head[kScoreTiles], j[kScoreTiles], page[kScoreTiles];  // the lane's (page -1: none)
-  };
-  const auto ask = [&](int64_t unit) {
-    Unit u;
-    u.b = units <= UINT32_MAX ? (uint32_t)unit / (uint32_t)p.blocks : unit / p.blocks;
-    const int32_t L = p.sl[u.b];
-    bool table_ok;
-    const int32_t* tab = p.tables.of(u.b, table_ok);
-#pragma unroll
-    for (int t = 0; t < kScoreTiles; ++t) {
-      const int64_t tile = (unit - u.b * p.blocks) * (kScoreTiles * kWaves) + kScoreTiles * wave + t;
-      const int32_t at = (int32_t)((uint32_t)tile / (uint32_t)p.kv_heads);
-      u.head[t] = (int32_t)tile - at * p.kv_heads;
-      u.j[t] = 16 * at + n;
-      u.page[t] = u.j[t] < p.width && table_ok ? tab[u.j[t]] : -1;  // (before the length is there)
-    }
-    u.count = min((max(L, 0) - 1) / kPage + (L > 0), p.width);
-    return u;
-  };
-  Unit next = ask(blockIdx.x);
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const Unit u = next;
-    const bool any = u.j[0] - n < u.count;  // (a wave's later tiles are no earlier)
-    u32x4 q[kScoreTiles][kSteps];
-    bf16x8 side[kScoreTiles][2][kSteps];
-    bool ok[kScoreTiles];
-    // query heads 16 * i of a tile's key head (past the group's last: its last)
-    const auto queries = [&](int t, int32_t i) {
-      return p.q + ((u.b * p.heads + (int64_t)u.head[t] * group + min(i + n, group - 1)) * DIM + 8 * quad) * 2;
+    const int64_t b = units <= UINT32_MAX ? (uint32_t)unit / (uint32_t)p.blocks : unit / p.blocks;
+    const uint32_t tile = (uint32_t)(unit - b * p.blocks) * kWaves + wave, at = tile / (uint32_t)p.kv_heads;
+    const int32_t h = (int32_t)(tile - at * (uint32_t)p.kv_heads), j = (int32_t)(16 * at) + n;
+    const int32_t L = p.sl[b];
+    bool table_ok;
+    const int32_t* tab = p.tables.of(b, table_ok);
+    const int32_t page = j < p.width && table_ok ? tab[j] : -1;  // (before the length is there)
+    const int32_t count = min((max(L, 0) - 1) / kPage + (L > 0), p.width);
+    const int64_t row = b * p.kv_heads + h;
+    u32x4 q[kSteps];  // of 16 query heads (past the group's last: its last)
+    const auto queries = [&](int32_t i) {
+      const uint8_t* from = p.q + ((b * p.heads + (int64_t)h * group + min(i + n, group - 1)) * DIM + 8 * quad) * 2;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4*>(from + 64 * s);
     };
-    if (any) {
+    float best = -INFINITY;
+    if (j - n < count) {
+      queries(0);
+      const bool ok = (uint32_t)page < p.pages_lim && j < count;
+      bf16x8 side[2][kSteps];
+      const uint8_t* from = p.bounds + (((int64_t)(ok ? page : 0) * p.kv_heads + h) * 2 * DIM + 8 * quad) * 2;
 #pragma unroll
-      for (int t = 0; t < kScoreTiles; ++t) {
-        ok[t] = (uint32_t)u.page[t] < p.pages_lim && u.j[t] < u.count;
-        const uint8_t* from = p.bounds + (((int64_t)(ok[t] ? u.page[t] : 0) * p.kv_heads + u.head[t]) * 2 * DIM + 8 * quad) * 2;
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
+        for (int s = 0; s < kSteps; ++s)
+          side[w][s] = ok ? *reinterpret_cast<const bf16x8*>(from + (w * DIM + 32 * s) * 2) : (bf16x8)((__bf16)0.0f);
+      for (int32_t i = 0;;) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s)
-            side[t][w][s] = ok[t] ? *reinterpret_cast<const bf16x8*>(from + (w * DIM + 32 * s) * 2) : (bf16x8)((__bf16)0.0f);
+        for (int s = 0; s < kSteps; ++s) {
+          u32x4 neg, pos;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(queries(t, 0) + 64 * s);
-      }
-    }
-    if (unit + gridDim.x < units) next = ask(unit + gridDim.x);
-#pragma unroll
-    for (int t = 0; t < kScoreTiles; ++t) {
-      float best = -INFINITY;
-      if (any) {
-        for (int32_t i = 0;;) {
-          f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            u32x4 neg, pos;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t sign = (q[t][s][e] >> 15 & 0x00010001u) * 0xffffu;
-              neg[e] = q[t][s][e] & sign;
-              pos[e] = q[t][s][e] & ~sign;
-            }
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, neg), side[t][0][s], acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), side[t][1][s], acc, 0, 0, 0);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t sign = (q[s][e] >> 15 & 0x00010001u) * 0xffffu;
+            neg[e] = q[s][e] & sign;
+            pos[e] = q[s][e] & ~sign;
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) best = __builtin_elementwise_maximum(best, acc[e]);  // (a NaN stays)
-          i += 16;
-          if (i >= group) break;
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const u32x4*>(queries(t, i) + 64 * s);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, neg), side[0][s], acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, pos), side[1][s], acc, 0, 0, 0);
         }
-        best = __builtin_elementwise_maximum(best, __shfl_xor(best, 16));
-        best = __builtin_elementwise_maximum(best, __shfl_xor(best, 32));
-        if (!ok[t]) best = __builtin_nanf("");
+#pragma unroll
+        for (int e = 0; e < 4; ++e) best = __builtin_elementwise_maximum(best, acc[e]);  // (a NaN stays)
+        i += 16;
+        if (i >= group) break;
+        queries(i);
       }
-      if (u.j[t] < p.first || u.j[t] >= (int64_t)u.count - p.last) best = INFINITY;
-      if (u.j[t] >= u.count) best = -INFINITY;
-      const int64_t row = u.b * p.kv_heads + u.head[t];
-      if (quad == 0 && u.j[t] < p.width) p.out[row * p.out_stride + u.j[t]] = best;
-      if (p.counts && quad == 0 && u.j[t] == 0) p.counts[row] = u.count;
+      best = __builtin_elementwise_maximum(best, __shfl_xor(best, 16));
+      best = __builtin_elementwise_maximum(best, __shfl_xor(best, 32));
+      if (!ok) best = __builtin_nanf("");
     }
+    if (j < p.first || j >= (int64_t)count - p.last) best = INFINITY;
+    if (j >= count) best = -INFINITY;
+    if (quad == 0 && j < p.width) p.out[row * p.out_stride + j] = best;
+    if (p.counts && quad == 0 && j == 0) p.counts[row] = count;
   }
 }
 
@@ -526,13 +495,14 @@ int page_bounds(const void* k_pages, const float* kscale, const int32_t* page_ta
   p.heads = kv_heads;
   p.width = table_width;
   (void)hipGetLastError();
-  // (rows first: what a row has of a decode step is its first workgroups', which so are
-  // all dies')
-  int64_t y = ((int64_t)table_width * kv_heads + kWaves - 1) / kWaves;
-  const int64_t cap = (8 * (int64_t)device_cu_count() + rows - 1) / rows;
+  // The workgroups of one page of a row, then those of the next row: what the rows have
+  // of a decode step so is all dies', and neighbours read neighbouring blocks.
+  p.side = (uint32_t)((kv_heads + kWaves - 1) / kWaves);
+  int64_t y = table_width;
+  const int64_t cap = (8 * (int64_t)device_cu_count() + (int64_t)rows * p.side - 1) / ((int64_t)rows * p.side);
   if (y > cap) y = cap;
   return for_dim(head_dim, [&](auto dim) {
-    page_bounds_kernel<KEY, decltype(dim)::value><<<dim3((uint32_t)rows, (uint32_t)y), dim3(kThreads), 0, stream>>>(p);
+    page_bounds_kernel<KEY, decltype(dim)::value><<<dim3((uint32_t)rows * p.side, (uint32_t)y), dim3(kThreads), 0, stream>>>(p);
   });
 }
 
@@ -629,7 +599,8 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
   p.counts = page_counts;
   p.out_stride = score_stride;
   // (a table without columns has tiles for the counts)
-  p.blocks = ((int64_t)(table_width > 0 ? (table_width + 15) / 16 : 1) * kv_heads + kScoreTiles * kWaves - 1) / (kScoreTiles * kWaves);
+  p.blocks = ((int64_t)(table_width > 0 ? (table_width + 15) / 16 : 1) * kv_heads + kWaves - 1) / kWaves;
+  if (p.blocks > INT32_MAX / kWaves) return IDX_ERR_SHAPE;
   p.pages_lim = pages_limit(num_pages);
   p.rows = rows;
   p.heads = num_heads;
@@ -637,8 +608,7 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
   p.width = table_width;
   p.first = first_pages;
   p.last = last_pages;
-  if (p.blocks > INT32_MAX / (kScoreTiles * kWaves)) return IDX_ERR_SHAPE;
-  const int64_t units = (int64_t)rows * p.blocks, cap = 4 * device_cu_count();
+  const int64_t units = (int64_t)rows * p.blocks, cap = (int64_t)1 << 20;
   const dim3 grid((uint32_t)(units < cap ? units : cap));
   (void)hipGetLastError();
   return for_dim(head_dim, [&](auto dim) {
