@@ -65,8 +65,11 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
 }
 
 // 64 lanes x 16 bytes from base + off (off each lane's own) to LDS dst + 16 * lane.
+// (s_nop: a scalar that a vector instruction has written, as base's halves are, can be
+// read by a memory instruction five states on; the compiler counts them for its own
+// instructions, not for those in assembly.)
 __device__ __forceinline__ void dma16_from(int64_t base, uint32_t off, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
 }
 
 template <int KEY, int DIM, int NT>
@@ -78,6 +81,8 @@ struct Form {
   static constexpr int kBytes = kTile * kRowBytes;  // of a tile's keys, and of its values
   static constexpr int kDmas = kBytes / 1024;
   static constexpr int kScaleDmas = KEY == kFp8 ? kTile / 32 : 0;
+  static constexpr int kFit = (kPerCu == 1 ? 131072 : 65536) / (2 * kWaves * kBytes);
+  static constexpr int kDepth = kFit > 4 ? 4 : kFit;  // tiles of a wave on their way or in use
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kRowsPerLine = kRowBytes < 256 ? 256 / kRowBytes : 1;
   static constexpr int kMask = (kChunks < 16 ? kChunks : 16) - 1;
@@ -98,8 +103,8 @@ struct Form {
 template <int KEY, int DIM, int NT>
 struct AttendShared {
   using F = Form<KEY, DIM, NT>;
-  uint8_t tile[kWaves][2][F::kBytes];           // keys, values; at the end outputs
-  float scale[kWaves][2][KEY == kFp8 ? F::kTile : 4];
+  uint8_t tile[kWaves][F::kDepth][2][F::kBytes];  // keys, values; at the end outputs
+  float scale[kWaves][F::kDepth][2][KEY == kFp8 ? F::kTile : 4];
   f32x2 ml[kWaves][16 * NT];
   int32_t sums[kWaves];
   int32_t start[2];
@@ -133,9 +138,15 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
   // `page0` of unit `unit` of row `b`.
   int64_t b;
   int32_t unit, page0 = 0, count, at = 0, end, L;
+  int32_t early_j = 0, early_page = 0;  // of a unit's first 64 pages, looked up before the row's length is there
   if (a.shares == 0) {
     b = blockIdx.x / (uint32_t)per_row;
     unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
+    bool ok;
+    const int32_t* tab = a.tables.of(b, ok);
+    early_j = lane;
+    if (a.k >= 0) early_j = lane < a.k ? a.idx[(b * a.kv_heads + unit / a.blocks) * (int64_t)a.k + lane] : -1;
+    early_page = (uint32_t)early_j < (uint32_t)a.width && ok ? tab[early_j] : -1;
     L = length_of(a, b);
     count = end = pages_of(a, L);
   } else {
@@ -211,10 +222,8 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
     page0 -= unit * count;
   }
 
-  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[wave][0][0];
-  const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[wave][0][0];
-  const uint8_t* keys = sh.tile[wave][0];
-  const uint8_t* vals = sh.tile[wave][1];
+  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[wave][0][0][0];
+  const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[wave][0][0][0];
   // DMA i of a tile brings rows kRowsPerDma * i ..; the lane's source within it
   constexpr int kRowsPerDma = 1024 / kRowBytes;
   const int dr = lane / F::kChunks, dc = lane % F::kChunks;
@@ -254,13 +263,13 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
     for (int t = 0; t < NT; ++t) ref[t] = 0.0f, limit[t] = -1.0f, sum[t] = 0.0f;
     bool bad = false;
 
-    // The wave's tiles: page `page` of the pool, positions 64 * j + first .. of the
-    // row, `left` of them live.
+    // The wave's tiles: page `page` of the pool, positions `first` .. of it, `left` of
+    // them live.
     struct Tile {
       int32_t page, first, left;
     };
-    int32_t next = wave, ids_from = -64;  // next tile of the piece, first page whose id is in `ids`
-    int32_t ids = -2, ids_left = 0;       // page id (-1 outside the pool, -2 to skip) and live positions of page ids_from + lane
+    int32_t next = wave;                  // next tile of the piece
+    int32_t ids_from = -64, ids, ids_left;  // lane: page id (-1 outside the pool, -2 to skip) and live positions of page ids_from + lane
     const int32_t tiles = pages * kTilesPerPage;
     auto find = [&](Tile& t) -> bool {
       for (; next < tiles; next += kWaves) {
@@ -270,9 +279,10 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
           ids = -2;
           ids_left = 0;
           if (ids_from + lane < pages) {
-            const int32_t j = list ? list[page0 + ids_from + lane] : page0 + ids_from + lane;
+            const bool early = a.shares == 0 && e < 64;
+            const int32_t j = early ? early_j : list ? list[page0 + ids_from + lane] : page0 + ids_from + lane;
             if ((uint32_t)j < (uint32_t)live) {
-              const int32_t page = table_ok ? tab[j] : -1;
+              const int32_t page = early ? early_page : table_ok ? tab[j] : -1;
               ids = (uint32_t)page < a.pages_lim ? page : -1;
               ids_left = min(L - j * kPage, kPage);
             }
@@ -289,44 +299,65 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
       }
       return false;
     };
-    auto fetch = [&](const Tile& t, auto which) {  // keys (with both scales) or values
+    auto fetch = [&](const Tile& t, int place, auto which) {  // keys (with both scales) or values
       constexpr int kWhich = decltype(which)::value;
       const int64_t base = uniform64((int64_t)(uintptr_t)a.kv[kWhich] + t.page * a.s.kv_page + h * a.s.kv_head + t.first * kRowBytes);
       if constexpr (KEY == kFp8 && kWhich == 0) {
         const int64_t at_ = t.page * a.s.ks_page + h * a.s.ks_head + 4 * t.first;
+        const uint32_t to = lds_scale + place * 8 * kTile;
         if constexpr (kTile == 64) {
-          dma4(a.ks[0] + at_ + 4 * lane, lds_scale);
-          dma4(a.ks[1] + at_ + 4 * lane, lds_scale + 256);
+          dma4(a.ks[0] + at_ + 4 * lane, to);
+          dma4(a.ks[1] + at_ + 4 * lane, to + 256);
         } else {
-          dma4((lane < 32 ? a.ks[0] : a.ks[1]) + at_ + 4 * (lane & 31), lds_scale);
+          dma4((lane < 32 ? a.ks[0] : a.ks[1]) + at_ + 4 * (lane & 31), to);
         }
       }
+      const uint32_t to = lds_tile + (2 * place + kWhich) * F::kBytes;
 #pragma unroll
       for (int i = 0; i < F::kDmas; ++i) {
         const int key = kWhich == 0 ? F::key_k(kRowsPerDma * i) : F::key_v(kRowsPerDma * i);
-        dma16_from(base, ((kWhich == 0 ? from_k : from_v) ^ (16 * key)) + 1024 * i, lds_tile + kWhich * F::kBytes + 1024 * i);
+        dma16_from(base, ((kWhich == 0 ? from_k : from_v) ^ (16 * key)) + 1024 * i, to + 1024 * i);
       }
     };
     constexpr std::integral_constant<int, 0> kKeys{};
     constexpr std::integral_constant<int, 1> kVals{};
 
-    Tile cur, nxt;
-    bool more = find(cur);
-    if (more) {
-      fetch(cur, kKeys);
-      fetch(cur, kVals);
-    }
-    while (more) {
-      const bool ahead = find(nxt);
+    // Operations of a wave complete in order: a tile's keys or values have arrived
+    // when no more are outstanding than were issued after them, those of the `after`
+    // tiles behind it among them.
+    auto wait_behind = [&](int after, auto extra) {
+      constexpr int kTileOps = 2 * F::kDmas + F::kScaleDmas, kMore = decltype(extra)::value;
+      if (F::kDepth > 3 && after >= 3) wait_vm<3 * kTileOps + kMore>();
+      else if (F::kDepth > 2 && after == 2) wait_vm<2 * kTileOps + kMore>();
+      else if (F::kDepth > 1 && after == 1) wait_vm<kTileOps + kMore>();
+      else wait_vm<kMore>();
+    };
+    static_assert(3 * (2 * F::kDmas + F::kScaleDmas) + F::kDmas + F::kScaleDmas <= 63 || F::kDepth < 4);
+
+    Tile ring[F::kDepth];  // the tiles on their way, the next to be used first
+    int have = 0, place = 0;
+#pragma unroll
+    for (int i = 0; i < F::kDepth; ++i)
+      if (have == i && find(ring[i])) {
+        fetch(ring[i], i, kKeys);
+        fetch(ring[i], i, kVals);
+        ++have;
+      }
+    while (have > 0) {
+      const int32_t left = ring[0].left;
+      const uint8_t* keys = sh.tile[wave][place][0];
+      uint8_t* vals = sh.tile[wave][place][1];
+      Tile nxt;
+      const bool ahead = have == F::kDepth && find(nxt);
       // scores of the tile
-      wait_vm<F::kDmas>();
+      wait_behind(have - 1, std::integral_constant<int, F::kDmas>{});
       f32x4 x[kSubs][NT];
       f32x4 ks[kSubs], vs[kSubs];
 #pragma unroll
       for (int s = 0; s < kSubs; ++s) {
         if constexpr (KEY == kFp8) {
-          ks[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][0][16 * s + 4 * quad]);
-          vs[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][1][16 * s + 4 * quad]);
+          ks[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][0][16 * s + 4 * quad]);
+          vs[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][1][16 * s + 4 * quad]);
         }
         if constexpr (NT * DIM > 128) __builtin_amdgcn_sched_barrier(0);  // (or all LDS reads go first, into registers there are not)
         const int r = 16 * s + n;
@@ -353,10 +384,10 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
       // (the reads above are over: their products wait for them; the DMAs behind
       // them overwrite what they read)
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ahead) fetch(nxt, kKeys);
+      if (ahead) fetch(nxt, place, kKeys);
 
       // probabilities
-      const bool partial = cur.left < kTile;
+      const bool partial = left < kTile;
       bf16x8 w[kSubs / 2][NT];
       float part[NT];
       auto weigh = [&]() {
@@ -368,7 +399,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
-              const bool dead = partial && 16 * s + 4 * quad + e >= cur.left;
+              const bool dead = partial && 16 * s + 4 * quad + e >= left;
               const float p = dead ? 0.0f : __builtin_amdgcn_exp2f(fmaf(x[s][t][e], by, -ref[t]));
               part[t] += p;
               w[s / 2][t][4 * (s & 1) + e] = (__bf16)(KEY == kFp8 ? (dead ? 0.0f : p * vs[s][e]) : p);
@@ -388,7 +419,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
-              const bool dead = partial && 16 * s + 4 * quad + e >= cur.left;
+              const bool dead = partial && 16 * s + 4 * quad + e >= left;
               top = fmaxf(top, dead ? -INFINITY : x[s][t][e] * by);
             }
           top = fmaxf(top, __shfl_xor(top, 16));
@@ -407,11 +438,11 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
       for (int t = 0; t < NT; ++t) sum[t] += part[t];
 
       // outputs
-      if (ahead) wait_vm<F::kDmas + F::kScaleDmas>();
-      else wait_vm<0>();
+      if (ahead) wait_behind(F::kDepth - 1, std::integral_constant<int, F::kDmas + F::kScaleDmas>{});
+      else wait_behind(have - 1, std::integral_constant<int, 0>{});
       if (partial) {  // values past the row's end: their probability is 0, theirs may be no number
-        for (int i = cur.left * F::kChunks + lane; i < kTile * F::kChunks; i += 64)
-          *reinterpret_cast<u32x4*>(sh.tile[wave][1] + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
+        for (int i = left * F::kChunks + lane; i < kTile * F::kChunks; i += 64)
+          *reinterpret_cast<u32x4*>(vals + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
       }
 #pragma unroll
       for (int i = 0; i < kSubs / 2; ++i) {
@@ -440,9 +471,12 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ahead) fetch(nxt, kVals);
-      cur = nxt;
-      more = ahead;
+      if (ahead) fetch(nxt, place, kVals);
+#pragma unroll
+      for (int i = 0; i + 1 < F::kDepth; ++i) ring[i] = ring[i + 1];
+      ring[F::kDepth - 1] = nxt;
+      have -= ahead ? 0 : 1;
+      place = place + 1 == F::kDepth ? 0 : place + 1;
     }
 
     // The waves' sums and outputs together.
@@ -470,7 +504,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) total = fmaf(ml[w].y, __builtin_amdgcn_exp2f(ml[w].x - base), total);
       const float f = __builtin_amdgcn_exp2f(sh.ml[wave][16 * t + n].x - base);
-      f32x4* mine = reinterpret_cast<f32x4*>(sh.tile[wave][0]);
+      f32x4* mine = reinterpret_cast<f32x4*>(sh.tile[wave][0][0]);
 #pragma unroll
       for (int p = 0; p < kParts; ++p) mine[64 * p + lane] = acc[p][t] * f;
       barrier();
@@ -482,7 +516,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
       for (int p = wave; p < kParts; p += kWaves) {
         f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) o += reinterpret_cast<const f32x4*>(sh.tile[w][0])[64 * p + lane];
+        for (int w = 0; w < kWaves; ++w) o += reinterpret_cast<const f32x4*>(sh.tile[w][0][0])[64 * p + lane];
         if (whole) {
           o = o * c.by * c.half * c.half;
           if (in)
@@ -643,6 +677,8 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
   const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.nt) * device_cu_count();
   if (units > 4 * workgroups || units * most > INT32_MAX / 2 || most <= kMinShare) return s;
+  const int64_t last = units % workgroups, page_bytes = (int64_t)2 * kPage * head_dim * (key == kFp8 ? 1 : 2);
+  if (k >= 0 && (last == 0 || (2 * workgroups - 5 * last) * most * page_bytes < 5 * workgroups * 43008)) return s;
   const int64_t want = (units * most + kMinShare - 1) / kMinShare;
   s.shares = (int)(want < workgroups ? want : workgroups);
   if (s.shares < 1) s.shares = 1;
