@@ -6,20 +6,24 @@
 //   out_i = sum_p exp(x_ip) v_p / z_i
 //
 // for the query heads i of a key head and its positions p.  A unit is (row, key
-// head, block of 16 * NT of its query heads): it reads every page of its own once.
+// head, block of 16 * HW of its query heads): it reads every page of its own once.
 //
 // Work decomposition.  The pages of all units, one after the other, are cut into
 // even shares, one a workgroup, whatever the rows' lengths: a share's pieces are the
 // end of a unit, whole units and the start of one.  Whole units are finished by their
 // workgroup, the other pieces leave sums and outputs in float32, which a second
-// kernel joins.  Where there are far more units than workgroups, each unit is a
+// kernel joins.  Where units fill the device evenly by themselves, each is a
 // workgroup's and nothing is joined.
 //
-// A workgroup has four waves, which take tiles of kTile positions of a piece in
-// turn, each with LDS buffers of its own: keys and values arrive by DMA, the next
-// keys while the values are used and the next values while the keys are, so the
-// waves need no barrier until the piece ends.  The matrix units (16 x 16 x 32,
-// bf16) take
+// A workgroup has four waves: HW of them have 16 query heads each, and 4 / HW groups of
+// such take tiles of kTile positions of a piece in turn.  Keys and values arrive by
+// DMA, in LDS places of a group's own.  Up to 16 heads (HW 1): a wave by itself, the
+// next keys arrive while the values are used and the next values while the keys
+// are, and no wave waits for another until the piece ends.  More heads: the waves of
+// a group read the same tiles, bring a part of each, and meet once a tile, while
+// later ones are on their way.  (Waves with 64 heads of their own had 500 registers
+// and 28 KB of code: 64 rows of up to 8192 positions of one key head took them 63 us,
+// in e4m3 61, where these take 58 and 43.)  The matrix units (16 x 16 x 32, bf16) take
 //   scores   X = K Q^T:  a lane gets 4 positions of a head for each 16 of the tile;
 //   outputs  O^T += V^T P^T:  the lane's positions of two such blocks are its 8
 //            k-values, so P stays in registers; V^T comes out of LDS through the
@@ -29,14 +33,16 @@
 // 2^-8 of itself at most.  The denominator sums the unrounded probabilities.
 //
 // Running maximum: a head's reference moves, and sums and outputs are rescaled,
-// only when a lane's probabilities of a tile add up to more than kLimit.
+// only where a tile's maximum exceeds it by more than kLazy: probabilities reach 2^8
+// instead of 1, which costs no precision, and most tiles rescale nothing.
 #include <type_traits>
 
 #include "kv_device.h"
 
 namespace {
 
-constexpr float kLimit = 256.0f;
+constexpr float kLazy = 8.0f;     // base-2 logits that a tile's maximum exceeds its reference by where that moves
+constexpr float kNone = -3e38f;   // a reference before the first
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kMinShare = 2;  // pages of a workgroup's share, at least
 
@@ -51,7 +57,7 @@ struct Attend {
   uint8_t* out;         // bf16 [rows][heads][D]
   float* lse;           // [rows][heads] or NULL
   int32_t* prefix;      // [rows + 1]: pages of the rows before, of one unit each (balanced)
-  f32x2* ml;            // references and sums of the pieces: [2 * shares][16 * NT]
+  f32x2* ml;            // references and sums of the pieces: [2 * shares][16 * HW]
   f32x4* part;          // their outputs
   KvStrides s;
   uint32_t pages_lim;
@@ -64,6 +70,17 @@ __device__ __forceinline__ int64_t uniform64(int64_t x) {
   return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(x >> 32)) << 32 | (uint32_t)uniform((int32_t)x));
 }
 
+// The same value, of which the compiler knows nothing: what is made of it is made
+// here, not kept in registers from before a loop.
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) v2i lds_v2i;
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
 // 64 lanes x 16 bytes from base + off (off each lane's own) to LDS dst + 16 * lane.
 // (s_nop: a scalar that a vector instruction has written, as base's halves are, can be
 // read by a memory instruction five states on; the compiler counts them for its own
@@ -72,17 +89,19 @@ __device__ __forceinline__ void dma16_from(int64_t base, uint32_t off, uint32_t 
   asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
 }
 
-template <int KEY, int DIM, int NT>
+template <int KEY, int DIM, int HW>
 struct Form {
   static constexpr int kRowBytes = KEY == kFp8 ? DIM : 2 * DIM;  // of a position
-  static constexpr int kPerCu = NT * DIM > 256 || kRowBytes > 256 ? 1 : 2;
-  static constexpr int kWant = (kPerCu == 1 ? 16384 : 8192) / kRowBytes;
-  static constexpr int kTile = kWant < 32 || NT == 4 || (KEY == kFp8 && NT > 1) ? 32 : kWant > 64 ? 64 : kWant;
+  static constexpr int kGroups = kWaves / HW;
+  static constexpr int kTile = 8192 / kRowBytes < 32 ? 32 : 8192 / kRowBytes > 64 ? 64 : 8192 / kRowBytes;
   static constexpr int kBytes = kTile * kRowBytes;  // of a tile's keys, and of its values
-  static constexpr int kDmas = kBytes / 1024;
+  // A CU's LDS is two workgroups', or one's where half of it has too few places.
+  static constexpr int kLeast = (HW > 1 ? 2 : 1) * kGroups * 2 * kBytes;
+  static constexpr int kPerCu = kLeast > 65536 ? 1 : 2;
+  static constexpr int kFit = 131072 / kPerCu / (kGroups * 2 * kBytes);
+  static constexpr int kPlaces = HW == 1 ? 1 : kFit > 4 ? 4 : kFit;  // tiles of a group in use or on their way
+  static constexpr int kDmas = kBytes / 1024 / HW;  // a wave's, of a tile's keys, and of its values
   static constexpr int kScaleDmas = KEY == kFp8 ? kTile / 32 : 0;
-  static constexpr int kFit = (kPerCu == 1 ? 131072 : 65536) / (2 * kWaves * kBytes);
-  static constexpr int kDepth = kFit > 4 ? 4 : kFit;  // tiles of a wave on their way or in use
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kRowsPerLine = kRowBytes < 256 ? 256 / kRowBytes : 1;
   static constexpr int kMask = (kChunks < 16 ? kChunks : 16) - 1;
@@ -100,12 +119,12 @@ struct Form {
   }
 };
 
-template <int KEY, int DIM, int NT>
+template <int KEY, int DIM, int HW>
 struct AttendShared {
-  using F = Form<KEY, DIM, NT>;
-  uint8_t tile[kWaves][F::kDepth][2][F::kBytes];  // keys, values; at the end outputs
-  float scale[kWaves][F::kDepth][2][KEY == kFp8 ? F::kTile : 4];
-  f32x2 ml[kWaves][16 * NT];
+  using F = Form<KEY, DIM, HW>;
+  uint8_t tile[F::kGroups][F::kPlaces][2][F::kBytes];  // keys, values; at the end outputs
+  float scale[kWaves][F::kPlaces][2][KEY == kFp8 ? F::kTile : 4];  // (each wave brings its own)
+  f32x2 ml[kWaves][16];
   int32_t sums[kWaves];
   int32_t start[2];
 };
@@ -124,14 +143,14 @@ __device__ __forceinline__ int32_t share_pages(int32_t total, int32_t shares) {
   return max((int32_t)(((uint32_t)total + (uint32_t)shares - 1) / (uint32_t)shares), kMinShare);
 }
 
-template <int KEY, int DIM, int NT>
-__global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_attention_kernel(Attend a) {
-  using F = Form<KEY, DIM, NT>;
+template <int KEY, int DIM, int HW>
+__global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_attention_kernel(Attend a) {
+  using F = Form<KEY, DIM, HW>;
   constexpr int kTile = F::kTile, kRowBytes = F::kRowBytes, kSteps = F::kSteps, kParts = F::kParts, kSubs = F::kSubs;
   constexpr int kTilesPerPage = kPage / kTile;
-  __shared__ __attribute__((aligned(1024))) AttendShared<KEY, DIM, NT> sh;
+  __shared__ __attribute__((aligned(1024))) AttendShared<KEY, DIM, HW> sh;
   const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
-  const int wave = uniform(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6), hw = wave % HW, group = wave / HW;
   const int32_t per_row = a.kv_heads * a.blocks;
 
   // The workgroup's share: pages [at, end) of the units' in order, from page
@@ -222,82 +241,75 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
     page0 -= unit * count;
   }
 
-  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[wave][0][0][0];
+  const uint32_t lds_tile = (uint32_t)(uintptr_t)(lds_u8*)&sh.tile[group][0][0][0];
   const uint32_t lds_scale = (uint32_t)(uintptr_t)(lds_u8*)&sh.scale[wave][0][0][0];
-  // DMA i of a tile brings rows kRowsPerDma * i ..; the lane's source within it
+  // DMA i of a wave brings rows dr + kRowsPerDma * i of a tile; the lane's source
   constexpr int kRowsPerDma = 1024 / kRowBytes;
-  const int dr = lane / F::kChunks, dc = lane % F::kChunks;
+  const int dr = hw * (kTile / HW) + lane / F::kChunks, dc = lane % F::kChunks;
   const uint32_t from_k = dr * kRowBytes + 16 * (dc ^ F::key_k(dr)), from_v = dr * kRowBytes + 16 * (dc ^ F::key_v(dr));
+  // Where the lane reads of a tile: keys, chunk `quad` of position n; values, of its
+  // first block of 16, chunks 0 (and 1) of position vr.  Other chunks are this place
+  // with bits of the chunk turned over, other positions (16 and 32 on have the same
+  // keys) a sum.
+  const int vr = KEY == kFp8 ? 16 * (n >> 3) + 4 * quad + (n >> 1 & 3) : 4 * quad + (n >> 2);
+  const uint32_t lane_k = lds_tile + n * kRowBytes + 16 * (quad ^ F::key_k(n));
+  const uint32_t lane_v = lds_tile + F::kBytes + vr * kRowBytes + 16 * ((KEY == kFp8 ? 0 : n >> 1 & 1) ^ F::key_v(vr)) + 8 * (n & 1);
 
   int32_t slot = 0;  // of a piece that is not whole: the share's first, or its last
   while (true) {
     const int32_t pages = a.shares == 0 ? count : min(count - page0, end - at);
     const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
-    const int32_t head0 = h * a.group + hb * 16 * NT;                 // of the row's
-    const int32_t heads = min(16 * NT, a.group - hb * 16 * NT);
+    const int32_t head0 = h * a.group + 16 * (hb * HW + hw);        // the wave's first, of the row's
+    const int32_t heads = min(16, a.group - 16 * (hb * HW + hw));    // (may be less than one)
     const int32_t live = (int32_t)(((uint32_t)L + kPage - 1) / kPage);
     bool table_ok;
     const int32_t* tab = a.tables.of(b, table_ok);
     const int32_t* list = a.k >= 0 ? a.idx + (b * a.kv_heads + h) * (int64_t)a.k : nullptr;
 
-    bf16x8 q[NT][kSteps];
+    bf16x8 q[kSteps];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const int d = KEY == kFp8 ? 64 * (s / 2) + 16 * quad + 8 * (s & 1) : 32 * s + 8 * quad;
-        q[t][s] = (bf16x8)((__bf16)0.0f);
-        if (16 * t + n < heads)
-          q[t][s] = *reinterpret_cast<const bf16x8*>(a.q + ((b * a.heads + head0 + 16 * t + n) * DIM + d) * 2);
-      }
+    for (int s = 0; s < kSteps; ++s) {
+      const int d = KEY == kFp8 ? 64 * (s / 2) + 16 * quad + 8 * (s & 1) : 32 * s + 8 * quad;
+      q[s] = (bf16x8)((__bf16)0.0f);
+      if (n < heads) q[s] = *reinterpret_cast<const bf16x8*>(a.q + ((b * a.heads + head0 + n) * DIM + d) * 2);
+    }
 
-    f32x4 acc[kParts][NT];
+    f32x4 acc[kParts];
 #pragma unroll
-    for (int p = 0; p < kParts; ++p)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[p][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    // of head 16 * t + n: reference, what a lane's probabilities may add up to by it
-    // (nothing, before the first), the lane's sum
-    float ref[NT], limit[NT], sum[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ref[t] = 0.0f, limit[t] = -1.0f, sum[t] = 0.0f;
+    for (int p = 0; p < kParts; ++p) acc[p] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    float ref = kNone, sum = 0.0f;  // of head n: reference, the lane's sum
     bool bad = false;
 
-    // The wave's tiles: page `page` of the pool, positions `first` .. of it, `left` of
-    // them live.
+    // The group's tiles: page `page` of the pool, positions `first` .. of it, `left` of
+    // them live (none: nothing to be read).
     struct Tile {
       int32_t page, first, left;
     };
-    int32_t next = wave;                  // next tile of the piece
     int32_t ids_from = -64, ids, ids_left;  // lane: page id (-1 outside the pool, -2 to skip) and live positions of page ids_from + lane
     const int32_t tiles = pages * kTilesPerPage;
-    auto find = [&](Tile& t) -> bool {
-      for (; next < tiles; next += kWaves) {
-        const int32_t e = next / kTilesPerPage;
-        if (e >= ids_from + 64) {
-          ids_from = e / 64 * 64;
-          ids = -2;
-          ids_left = 0;
-          if (ids_from + lane < pages) {
-            const bool early = a.shares == 0 && e < 64;
-            const int32_t j = early ? early_j : list ? list[page0 + ids_from + lane] : page0 + ids_from + lane;
-            if ((uint32_t)j < (uint32_t)live) {
-              const int32_t page = early ? early_page : table_ok ? tab[j] : -1;
-              ids = (uint32_t)page < a.pages_lim ? page : -1;
-              ids_left = min(L - j * kPage, kPage);
-            }
+    auto look = [&](int32_t tile, Tile& t) -> bool {
+      t.left = 0;
+      if (tile >= tiles) return false;
+      const int32_t e = tile / kTilesPerPage;
+      if (e >= ids_from + 64) {
+        ids_from = e / 64 * 64;
+        ids = -2;
+        ids_left = 0;
+        if (ids_from + lane < pages) {
+          const bool early = a.shares == 0 && e < 64;
+          const int32_t j = early ? early_j : list ? list[page0 + ids_from + lane] : page0 + ids_from + lane;
+          if ((uint32_t)j < (uint32_t)live) {
+            const int32_t page = early ? early_page : table_ok ? tab[j] : -1;
+            ids = (uint32_t)page < a.pages_lim ? page : -1;
+            ids_left = min(L - j * kPage, kPage);
           }
         }
-        const int32_t page = __builtin_amdgcn_readlane(ids, e - ids_from);
-        t.first = (next % kTilesPerPage) * kTile;
-        t.left = __builtin_amdgcn_readlane(ids_left, e - ids_from) - t.first;
-        if (page == -1) bad = true;
-        if (page < 0 || t.left <= 0) continue;
-        t.page = page;
-        next += kWaves;
-        return true;
       }
-      return false;
+      t.page = __builtin_amdgcn_readlane(ids, e - ids_from);
+      t.first = (tile % kTilesPerPage) * kTile;
+      if (t.page == -1) bad = true;
+      if (t.page >= 0) t.left = max(__builtin_amdgcn_readlane(ids_left, e - ids_from) - t.first, 0);
+      return t.left > 0;
     };
     auto fetch = [&](const Tile& t, int place, auto which) {  // keys (with both scales) or values
       constexpr int kWhich = decltype(which)::value;
@@ -312,226 +324,235 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
           dma4((lane < 32 ? a.ks[0] : a.ks[1]) + at_ + 4 * (lane & 31), to);
         }
       }
-      const uint32_t to = lds_tile + (2 * place + kWhich) * F::kBytes;
+      const uint32_t to = lds_tile + (2 * place + kWhich) * F::kBytes + hw * (F::kBytes / HW);
+      const uint32_t from = here(kWhich == 0 ? from_k : from_v);
 #pragma unroll
       for (int i = 0; i < F::kDmas; ++i) {
         const int key = kWhich == 0 ? F::key_k(kRowsPerDma * i) : F::key_v(kRowsPerDma * i);
-        dma16_from(base, ((kWhich == 0 ? from_k : from_v) ^ (16 * key)) + 1024 * i, to + 1024 * i);
+        dma16_from(base, (from ^ (16 * key)) + 1024 * i, to + 1024 * i);
       }
     };
     constexpr std::integral_constant<int, 0> kKeys{};
     constexpr std::integral_constant<int, 1> kVals{};
 
-    // Operations of a wave complete in order: a tile's keys or values have arrived
-    // when no more are outstanding than were issued after them, those of the `after`
-    // tiles behind it among them.
-    auto wait_behind = [&](int after, auto extra) {
-      constexpr int kTileOps = 2 * F::kDmas + F::kScaleDmas, kMore = decltype(extra)::value;
-      if (F::kDepth > 3 && after >= 3) wait_vm<3 * kTileOps + kMore>();
-      else if (F::kDepth > 2 && after == 2) wait_vm<2 * kTileOps + kMore>();
-      else if (F::kDepth > 1 && after == 1) wait_vm<kTileOps + kMore>();
-      else wait_vm<kMore>();
-    };
-    static_assert(3 * (2 * F::kDmas + F::kScaleDmas) + F::kDmas + F::kScaleDmas <= 63 || F::kDepth < 4);
-
-    Tile ring[F::kDepth];  // the tiles on their way, the next to be used first
-    int have = 0, place = 0;
-#pragma unroll
-    for (int i = 0; i < F::kDepth; ++i)
-      if (have == i && find(ring[i])) {
-        fetch(ring[i], i, kKeys);
-        fetch(ring[i], i, kVals);
-        ++have;
-      }
-    while (have > 0) {
-      const int32_t left = ring[0].left;
-      const uint8_t* keys = sh.tile[wave][place][0];
-      uint8_t* vals = sh.tile[wave][place][1];
-      Tile nxt;
-      const bool ahead = have == F::kDepth && find(nxt);
-      // scores of the tile
-      wait_behind(have - 1, std::integral_constant<int, F::kDmas>{});
-      f32x4 x[kSubs][NT];
-      f32x4 ks[kSubs], vs[kSubs];
+    f32x4 x[kSubs];        // of a tile's positions 16 * s + 4 * quad .. and head n: scores, then base-2 logits
+    f32x4 ks[kSubs], vs[kSubs];
+    bf16x8 w[kSubs / 2];   // probabilities
+    auto score = [&](int place) {
+      const uint32_t from = here(lane_k + place * 2 * F::kBytes);
 #pragma unroll
       for (int s = 0; s < kSubs; ++s) {
         if constexpr (KEY == kFp8) {
           ks[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][0][16 * s + 4 * quad]);
           vs[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][1][16 * s + 4 * quad]);
         }
-        if constexpr (NT * DIM > 128) __builtin_amdgcn_sched_barrier(0);  // (or all LDS reads go first, into registers there are not)
-        const int r = 16 * s + n;
-        const uint8_t* row = keys + r * kRowBytes;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) x[s][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        x[s] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < F::kChunks / 4; ++c) {
-          const u32x4 raw = *reinterpret_cast<const u32x4*>(row + 16 * ((4 * c + quad) ^ F::key_k(r)));
+          const u32x4 raw = *(lds_u32x4*)(uintptr_t)((from ^ (64 * c)) + 16 * s * kRowBytes);
           if constexpr (KEY == kFp8) {
-            const bf16x8 k0 = fp8x8_to_bf16x8(raw.x, raw.y), k1 = fp8x8_to_bf16x8(raw.z, raw.w);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[t][2 * c], x[s][t], 0, 0, 0);
-              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[t][2 * c + 1], x[s][t], 0, 0, 0);
-            }
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(raw.x, raw.y), q[2 * c], x[s], 0, 0, 0);
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(raw.z, raw.w), q[2 * c + 1], x[s], 0, 0, 0);
           } else {
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-              x[s][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, raw), q[t][c], x[s][t], 0, 0, 0);
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, raw), q[c], x[s], 0, 0, 0);
           }
         }
       }
-      // (the reads above are over: their products wait for them; the DMAs behind
-      // them overwrite what they read)
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ahead) fetch(nxt, place, kKeys);
-
-      // probabilities
-      const bool partial = left < kTile;
-      bf16x8 w[kSubs / 2][NT];
-      float part[NT];
-      auto weigh = [&]() {
+    };
+    auto weigh = [&](int32_t left) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          part[t] = 0.0f;
+      for (int s = 0; s < kSubs; ++s) x[s] *= KEY == kFp8 ? ks[s] * a.scale2 : (f32x4){a.scale2, a.scale2, a.scale2, a.scale2};
+      if (left < kTile) {  // past the row's end: no logit, and values of no weight, whatever is there
 #pragma unroll
-          for (int s = 0; s < kSubs; ++s)
+        for (int s = 0; s < kSubs; ++s)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
-              const bool dead = partial && 16 * s + 4 * quad + e >= left;
-              const float p = dead ? 0.0f : __builtin_amdgcn_exp2f(fmaf(x[s][t][e], by, -ref[t]));
-              part[t] += p;
-              w[s / 2][t][4 * (s & 1) + e] = (__bf16)(KEY == kFp8 ? (dead ? 0.0f : p * vs[s][e]) : p);
-            }
-        }
-      };
-      weigh();
-      bool over = false;
+          for (int e = 0; e < 4; ++e) {
+            const bool dead = 16 * s + 4 * quad + e >= left;
+            x[s][e] = dead ? -INFINITY : x[s][e];
+            if constexpr (KEY == kFp8) vs[s][e] = dead ? 0.0f : vs[s][e];
+          }
+      }
+      float top = x[0][0];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) over = over || part[t] > limit[t];
-      if (__ballot(over) != 0) {
+      for (int s = 0; s < kSubs; ++s)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float top = -INFINITY;
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, x[s][e]);
+      if (__ballot(top > ref + kLazy) != 0) {
+        float m = fmaxf(top, __shfl_xor(top, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        m = fmaxf(m, ref);
+        const float f = __builtin_amdgcn_exp2f(ref - m);
+        ref = m;
+        sum *= f;
 #pragma unroll
-          for (int s = 0; s < kSubs; ++s)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float by = KEY == kFp8 ? a.scale2 * ks[s][e] : a.scale2;
-              const bool dead = partial && 16 * s + 4 * quad + e >= left;
-              top = fmaxf(top, dead ? -INFINITY : x[s][t][e] * by);
-            }
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const bool begun = limit[t] > 0.0f;
-          const bool moves = begun ? top > ref[t] : top > -INFINITY;
-          const float f = moves && begun ? __builtin_amdgcn_exp2f(ref[t] - top) : 1.0f;  // (before the first there is nothing)
-          if (moves) ref[t] = top, limit[t] = kLimit;
-          sum[t] *= f;
-#pragma unroll
-          for (int p = 0; p < kParts; ++p) acc[p][t] *= f;
-        }
-        weigh();
+        for (int p = 0; p < kParts; ++p) acc[p] *= f;
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) sum[t] += part[t];
-
-      // outputs
-      if (ahead) wait_behind(F::kDepth - 1, std::integral_constant<int, F::kDmas + F::kScaleDmas>{});
-      else wait_behind(have - 1, std::integral_constant<int, 0>{});
-      if (partial) {  // values past the row's end: their probability is 0, theirs may be no number
+      for (int s = 0; s < kSubs; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = __builtin_amdgcn_exp2f(x[s][e] - ref);
+          sum += p;
+          w[s / 2][4 * (s & 1) + e] = (__bf16)(KEY == kFp8 ? p * vs[s][e] : p);
+        }
+    };
+    auto add = [&](int place, int32_t left) {
+      if (left < kTile) {  // (their probability is 0, they may be no numbers)
         for (int i = left * F::kChunks + lane; i < kTile * F::kChunks; i += 64)
-          *reinterpret_cast<u32x4*>(vals + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
+          *reinterpret_cast<u32x4*>(sh.tile[group][place][1] + 16 * i) = (u32x4){0u, 0u, 0u, 0u};
       }
+      const uint32_t from = here(lane_v + place * 2 * F::kBytes);
 #pragma unroll
       for (int i = 0; i < kSubs / 2; ++i) {
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
-          if constexpr (NT * DIM > 128)
-            if (p % 2 == 0) __builtin_amdgcn_sched_barrier(0);
           bf16x8 v;
           if constexpr (KEY == kFp8) {
-            const int k = n >> 1, r = 32 * i + 16 * (k >> 2) + 4 * quad + (k & 3);
-            const v2i c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)(
-                vals + r * kRowBytes + 16 * (p ^ F::key_v(r)) + 8 * (n & 1)));
+            const v2i c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(uintptr_t)((from ^ (16 * p)) + 32 * i * kRowBytes));
             v = fp8x8_to_bf16x8((uint32_t)c.x, (uint32_t)c.y);
           } else {
             v4s u[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = 32 * i + 16 * e + 4 * quad + (n >> 2), c = 2 * p + (n >> 1 & 1);
-              u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(
-                  vals + r * kRowBytes + 16 * (c ^ F::key_v(r)) + 8 * (n & 1)));
-            }
+            for (int e = 0; e < 2; ++e)
+              u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)((from ^ (32 * p)) + (32 * i + 16 * e) * kRowBytes));
             v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u[0], u[1], 0, 1, 2, 3, 4, 5, 6, 7));
           }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) acc[p][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[i][t], acc[p][t], 0, 0, 0);
+          acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[i], acc[p], 0, 0, 0);
         }
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ahead) fetch(nxt, place, kVals);
+    };
+    // What a wave has read from LDS is there: DMAs may overwrite it.
+    auto reads_done = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+
+    // Operations of a wave complete in order: what it waits for has arrived when no more
+    // are outstanding than were issued after it.
+    if constexpr (HW == 1) {
+      int32_t next = wave;
+      auto find = [&](Tile& t) {
+        bool found = false;
+        for (; next < tiles && !found; next += kWaves) found = look(next, t);
+        return found;
+      };
+      Tile cur, nxt;
+      bool more = find(cur);
+      if (more) {
+        fetch(cur, 0, kKeys);
+        fetch(cur, 0, kVals);
+      }
+      while (more) {
+        const bool ahead = find(nxt);
+        wait_vm<F::kDmas>();
+        score(0);
+        reads_done();
+        if (ahead) fetch(nxt, 0, kKeys);
+        weigh(cur.left);
+        if (ahead) wait_vm<F::kDmas + F::kScaleDmas>();
+        else wait_vm<0>();
+        add(0, cur.left);
+        reads_done();
+        if (ahead) fetch(nxt, 0, kVals);
+        cur = nxt;
+        more = ahead;
+      }
+    } else {
+      // Tile r of a group goes to place r % kPlaces.  When the waves meet for it, their
+      // parts have arrived and all are done with tile r - 1, whose place the next takes.
+      constexpr int kBehind = F::kPlaces - 1, kOps = 2 * F::kDmas + F::kScaleDmas;  // tiles on their way, operations of each
+      static_assert(kBehind >= 1 && kBehind <= 3 && 2 * kOps <= 63);
+      const int32_t rounds = (tiles + F::kGroups - 1) / F::kGroups;
+      int32_t lefts[kBehind];  // of the tiles on their way, the next one's first
+      Tile t;
+#pragma unroll 1
+      for (int r = 0; r < kBehind; ++r) {
+        if (look(r * F::kGroups + group, t)) {
+          fetch(t, r, kKeys);
+          fetch(t, r, kVals);
+        }
 #pragma unroll
-      for (int i = 0; i + 1 < F::kDepth; ++i) ring[i] = ring[i + 1];
-      ring[F::kDepth - 1] = nxt;
-      have -= ahead ? 0 : 1;
-      place = place + 1 == F::kDepth ? 0 : place + 1;
+        for (int i = 0; i + 1 < kBehind; ++i) lefts[i] = lefts[i + 1];
+        lefts[kBehind - 1] = t.left;
+      }
+      int place = 0;
+#pragma unroll 1
+      for (int32_t r = 0; r < rounds; ++r) {
+        const int32_t left = lefts[0];
+        int after = 0;
+#pragma unroll
+        for (int i = 1; i < kBehind; ++i) after += lefts[i] > 0 ? 1 : 0;
+        if (kBehind > 2 && after == 2) wait_vm<2 * kOps>();
+        else if (kBehind > 1 && after == 1) wait_vm<kOps>();
+        else wait_vm<0>();
+        barrier();
+        const int last = place == 0 ? F::kPlaces - 1 : place - 1;
+        if (look((r + kBehind) * F::kGroups + group, t)) {
+          fetch(t, last, kKeys);
+          fetch(t, last, kVals);
+        }
+        score(place);
+        weigh(left);
+        add(place, left);
+#pragma unroll
+        for (int i = 0; i + 1 < kBehind; ++i) lefts[i] = lefts[i + 1];
+        lefts[kBehind - 1] = t.left;
+        place = place + 1 == F::kPlaces ? 0 : place + 1;
+      }
     }
 
-    // The waves' sums and outputs together.
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float s = sum[t];
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (bad) s = __builtin_nanf("");
-      if (quad == 0) sh.ml[wave][16 * t + n] = (f32x2){s == 0.0f ? -INFINITY : ref[t], s};
-    }
-    barrier();
+    // The groups' sums and outputs together, blocks of 16 values as they stand in the
+    // registers, through the tiles' places.
     const bool whole = a.shares == 0 || pages == count;
-    const int64_t piece = 2 * (int64_t)blockIdx.x + slot;
+    const int64_t head = b * a.heads + head0, piece = 2 * (int64_t)blockIdx.x + slot;
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (bad) sum = __builtin_nanf("");
+    float top = sum == 0.0f ? -INFINITY : ref, total = sum;
+    if constexpr (F::kGroups > 1) {
+      static_assert(kWaves * 64 * DIM <= (int)sizeof(sh.tile));
+      if (quad == 0) sh.ml[wave][n] = (f32x2){top, total};
+      barrier();
+      f32x2 ml[F::kGroups];
+      top = -INFINITY;
+      total = 0.0f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f32x2 ml[kWaves];
-      float top = -INFINITY, total = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        ml[w] = sh.ml[w][16 * t + n];
-        top = fmaxf(top, ml[w].x);
+      for (int g = 0; g < F::kGroups; ++g) {
+        ml[g] = sh.ml[g * HW + hw][n];
+        top = fmaxf(top, ml[g].x);
       }
       const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) total = fmaf(ml[w].y, __builtin_amdgcn_exp2f(ml[w].x - base), total);
-      const float f = __builtin_amdgcn_exp2f(sh.ml[wave][16 * t + n].x - base);
-      f32x4* mine = reinterpret_cast<f32x4*>(sh.tile[wave][0][0]);
+      for (int g = 0; g < F::kGroups; ++g) total = fmaf(ml[g].y, __builtin_amdgcn_exp2f(ml[g].x - base), total);
+      const float f = __builtin_amdgcn_exp2f(sh.ml[wave][n].x - base);
+      f32x4* to = reinterpret_cast<f32x4*>(&sh.tile[0][0][0][0]) + wave * kParts * 64 + lane;
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) mine[64 * p + lane] = acc[p][t] * f;
-      barrier();
-      const bool in = 16 * t + n < heads;
-      const int64_t head = b * a.heads + head0 + 16 * t + n;
-      Closing c = {1.0f, 1.0f, 0.0f};
-      if (whole) c = close_sum(top, total, a.sinks && in ? a.sinks[head0 + 16 * t + n] * kLog2e : -INFINITY);
-#pragma unroll
-      for (int p = wave; p < kParts; p += kWaves) {
-        f32x4 o = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) o += reinterpret_cast<const f32x4*>(sh.tile[w][0][0])[64 * p + lane];
-        if (whole) {
-          o = o * c.by * c.half * c.half;
-          if (in)
-            *reinterpret_cast<bf16x4*>(a.out + (head * DIM + 16 * p + 4 * quad) * 2) =
-                (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
-        } else {
-          a.part[((piece * NT + t) * kParts + p) * 64 + lane] = o;
-        }
-      }
-      if (wave == 0 && quad == 0) {
-        if (!whole) a.ml[piece * 16 * NT + 16 * t + n] = (f32x2){top, total};
-        else if (a.lse && in) a.lse[head] = c.lse;
-      }
-      barrier();
+      for (int p = 0; p < kParts; ++p) to[64 * p] = acc[p] * f;
     }
+    Closing c = {1.0f, 1.0f, 0.0f};
+    if (whole) c = close_sum(top, total, a.sinks && n < heads ? a.sinks[head0 + n] * kLog2e : -INFINITY);
+    if (group == 0 && quad == 0) {
+      if (!whole) a.ml[(piece * HW + hw) * 16 + n] = (f32x2){top, total};
+      else if (a.lse && n < heads) a.lse[head + n] = c.lse;
+    }
+    if constexpr (F::kGroups > 1) barrier();
+#pragma unroll
+    for (int i = 0; i < kParts / F::kGroups; ++i) {
+      const int p = F::kGroups * i + group;
+      f32x4 o = acc[i];
+      if constexpr (F::kGroups > 1) {
+        const f32x4* from = reinterpret_cast<const f32x4*>(&sh.tile[0][0][0][0]) + (hw * kParts + p) * 64 + lane;
+        o = from[0];
+#pragma unroll
+        for (int g = 1; g < F::kGroups; ++g) o += from[g * HW * kParts * 64];
+      }
+      if (whole) {
+        o = o * c.by * c.half * c.half;
+        if (n < heads)
+          *reinterpret_cast<bf16x4*>(a.out + ((head + n) * DIM + 16 * p + 4 * quad) * 2) =
+              (bf16x4){(__bf16)o[0], (__bf16)o[1], (__bf16)o[2], (__bf16)o[3]};
+      } else {
+        a.part[((piece * HW + hw) * kParts + p) * 64 + lane] = o;
+      }
+    }
+    barrier();  // (LDS is the next piece's)
     if (a.shares == 0) return;
     slot = 1;
     at += pages;
@@ -548,11 +569,11 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, NT>::kPerCu)) void kv_att
 }
 
 // Joins the pieces of a unit, and writes the units that have no pages: blocks of 16
-// values of 16 heads, kParts * NT of them a unit.  Many units: a workgroup a unit, its
-// waves take the blocks in turn.  FEW: a workgroup a block, its waves take the pieces in
+// values of 16 heads, kParts * HW of them a unit.  The waves of a unit's workgroups take
+// the blocks in turn.  FEW units: a workgroup a block, its waves take the pieces in
 // turn and join what they have through LDS.  The order is fixed, so the result
 // does not depend on the pieces' timing.
-template <int DIM, int NT, bool FEW>
+template <int DIM, int HW, bool FEW>
 __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
   constexpr int kParts = DIM / 16, kBatch = FEW ? 16 : 4, kEvery = FEW ? kWaves : 1;
   __shared__ f32x4 outs[FEW ? kWaves : 1][64];
@@ -567,7 +588,8 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
   const int32_t s = before * per_row + unit * count;  // the unit's pages: s .. s + count
   const int32_t w0 = s / share, w1 = count > 0 ? (s + count - 1) / share : w0 - 1;
   if (w0 == w1) return;  // whole
-  for (int block = FEW ? (int)blockIdx.y : wave; block < NT * kParts; block += FEW ? NT * kParts : kWaves) {
+  for (int block = FEW ? (int)blockIdx.y : (int)blockIdx.y * kWaves + wave; block < HW * kParts;
+       block += FEW ? HW * kParts : (int)gridDim.y * kWaves) {
     const int t = block / kParts, p = block % kParts;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
     float top = -INFINITY, total = 0.0f;
@@ -582,8 +604,8 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
         v[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
         if (x <= w1) {
           const int64_t piece = 2 * (int64_t)x + (x == w0 && s != w0 * share ? 1 : 0);
-          ml[i] = a.ml[piece * 16 * NT + 16 * t + n];
-          v[i] = a.part[((piece * NT + t) * kParts + p) * 64 + lane];
+          ml[i] = a.ml[piece * 16 * HW + 16 * t + n];
+          v[i] = a.part[((piece * HW + t) * kParts + p) * 64 + lane];
         }
       }
       float to = top;
@@ -625,7 +647,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
         for (int e = 0; e < 4; ++e) o[e] = fmaf(v[e], f, o[e]);
       }
     }
-    const int32_t i = hb * 16 * NT + 16 * t + n;
+    const int32_t i = hb * 16 * HW + 16 * t + n;
     if (i >= a.group) continue;
     const int32_t head = h * a.group + i;
     const Closing c = close_sum(top, total, a.sinks ? a.sinks[head] * kLog2e : -INFINITY);
@@ -642,7 +664,7 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
 constexpr int64_t kMaxHeads = 8000000;  // of a call's rows together: a launch has less than 2^32 threads
 
 struct Split {
-  int nt, blocks, shares;  // head tiles of a unit, blocks of them a group, workgroups (0: a unit each)
+  int hw, blocks, shares;  // waves of 16 heads of a unit, blocks of them a group, workgroups (0: a unit each)
   int64_t bytes;
 };
 
@@ -654,12 +676,12 @@ bool dims_ok(int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t table_wi
 }
 
 // Workgroups of a form that a CU holds.
-int per_cu(int key, int32_t head_dim, int nt) {
+int per_cu(int key, int32_t head_dim, int hw) {
   const auto of = [&](auto d, auto n) {
     return key == kFp8 ? Form<kFp8, decltype(d)::value, decltype(n)::value>::kPerCu : Form<kBf16, decltype(d)::value, decltype(n)::value>::kPerCu;
   };
   const auto with = [&](auto d) {
-    return nt == 1 ? of(d, std::integral_constant<int, 1>{}) : nt == 2 ? of(d, std::integral_constant<int, 2>{}) : of(d, std::integral_constant<int, 4>{});
+    return hw == 1 ? of(d, std::integral_constant<int, 1>{}) : hw == 2 ? of(d, std::integral_constant<int, 2>{}) : of(d, std::integral_constant<int, 4>{});
   };
   return head_dim == 64 ? with(std::integral_constant<int, 64>{}) : head_dim == 128 ? with(std::integral_constant<int, 128>{})
                                                                                    : with(std::integral_constant<int, 256>{});
@@ -670,37 +692,40 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   Split s = {1, 1, 0, 0};
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
-  const int most_nt = head_dim == 256 ? 2 : 4;
-  while (s.nt < most_nt && 16 * s.nt < group) s.nt *= 2;
-  s.blocks = (group + 16 * s.nt - 1) / (16 * s.nt);
+  while (s.hw < kWaves && 16 * s.hw < group) s.hw *= 2;
+  s.blocks = (group + 16 * s.hw - 1) / (16 * s.hw);
   const int64_t units = (int64_t)rows * kv_heads * s.blocks;
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
-  const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.nt) * device_cu_count();
+  const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.hw) * device_cu_count();
   if (units > 4 * workgroups || units * most > INT32_MAX / 2 || most <= kMinShare) return s;
   const int64_t last = units % workgroups, page_bytes = (int64_t)2 * kPage * head_dim * (key == kFp8 ? 1 : 2);
   if (k >= 0 && (last == 0 || (2 * workgroups - 5 * last) * most * page_bytes < 5 * workgroups * 43008)) return s;
   const int64_t want = (units * most + kMinShare - 1) / kMinShare;
   s.shares = (int)(want < workgroups ? want : workgroups);
   if (s.shares < 1) s.shares = 1;
-  s.bytes = padded(4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.nt * 8) +
-            2 * (int64_t)s.shares * s.nt * head_dim * 64;
+  s.bytes = padded(4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.hw * 8) +
+            2 * (int64_t)s.shares * s.hw * head_dim * 64;
   return s;
 }
 
-template <int KEY, int DIM, int NT>
+template <int KEY, int DIM, int HW>
 void launch(const Attend& a, const Split& split, hipStream_t stream) {
   const uint32_t units = (uint32_t)((int64_t)a.rows * a.kv_heads * a.blocks);
-  kv_attention_kernel<KEY, DIM, NT><<<dim3(split.shares ? (uint32_t)split.shares : units), dim3(kThreads), 0, stream>>>(a);
+  kv_attention_kernel<KEY, DIM, HW><<<dim3(split.shares ? (uint32_t)split.shares : units), dim3(kThreads), 0, stream>>>(a);
   if (split.shares == 0) return;
-  if (split.shares >= 8 * (int64_t)units) kv_join_kernel<DIM, NT, true><<<dim3(units, NT * DIM / 16), dim3(kThreads), 0, stream>>>(a);
-  else kv_join_kernel<DIM, NT, false><<<dim3(units), dim3(kThreads), 0, stream>>>(a);
+  if (split.shares >= 8 * (int64_t)units) kv_join_kernel<DIM, HW, true><<<dim3(units, HW * DIM / 16), dim3(kThreads), 0, stream>>>(a);
+  else {
+    uint32_t y = 512 / units;
+    if (y > HW * DIM / 16 / kWaves) y = HW * DIM / 16 / kWaves;
+    kv_join_kernel<DIM, HW, false><<<dim3(units, y < 1 ? 1 : y), dim3(kThreads), 0, stream>>>(a);
+  }
 }
 
 template <int KEY, int DIM>
 void launch_for(const Attend& a, const Split& split, hipStream_t stream) {
-  if (split.nt == 1) return launch<KEY, DIM, 1>(a, split, stream);
-  if (split.nt == 2) return launch<KEY, DIM, 2>(a, split, stream);
-  if constexpr (DIM <= 128) launch<KEY, DIM, 4>(a, split, stream);
+  if (split.hw == 1) return launch<KEY, DIM, 1>(a, split, stream);
+  if (split.hw == 2) return launch<KEY, DIM, 2>(a, split, stream);
+  launch<KEY, DIM, 4>(a, split, stream);
 }
 
 template <int KEY>
@@ -742,7 +767,7 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   uint8_t* space = static_cast<uint8_t*>(workspace);
   a.prefix = reinterpret_cast<int32_t*>(space);
   a.ml = reinterpret_cast<f32x2*>(space + padded(4 * ((int64_t)rows + 1)));
-  a.part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(a.ml) + padded(2 * (int64_t)split.shares * 16 * split.nt * 8));
+  a.part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(a.ml) + padded(2 * (int64_t)split.shares * 16 * split.hw * 8));
   a.s = s;
   a.pages_lim = pages_limit(num_pages);
   a.rows = rows;
