@@ -1,7 +1,8 @@
 """Python binding of the paged MQA-logits indexer library (libidx_paged_mqa.so).
 
 Argument marshalling only: every step of the computation runs in the library's
-HIP kernels.  The functions carry the C-ABI names and argument order; they
+HIP kernels (the marshalling of the newer functions is compiled, csrc/binding.cpp).
+The functions carry the C-ABI names and argument order; they
 accept torch device tensors (or raw device addresses as ints) and pass their
 addresses and sizes through ctypes.  torch supplies device memory and streams.
 
@@ -14,6 +15,12 @@ import ctypes
 from pathlib import Path
 
 import torch  # loads the HIP runtime the library binds to (same soname)
+
+try:
+    from . import _binding  # compiled with the library
+except ImportError as e:
+    raise ImportError(f"{Path(__file__).resolve().parent / '_binding.so'}: {e}; build it first "
+                      "(python paged_mqa_logits_idx_amd/_build.py)") from e
 
 LIB_PATH = Path(__file__).resolve().parent / "libidx_paged_mqa.so"
 
@@ -747,104 +754,32 @@ def idx_latent_attention_bf16(q, kv_pages, page_table, topk_idx, seqlens, out, l
 
 
 # --- the cache of keys and values by head (include/kv_cache.h).  Its pools are
-# tensors [pages, kv_heads, 64, D], whose strides the kernels take.
+# tensors [pages, kv_heads, 64, D], whose strides the kernels take.  The marshalling
+# of these calls is compiled (csrc/binding.cpp).
 
 
-def _flat(name, x, dtype, n, dev) -> int:
-    """Address of a contiguous tensor of this type and ``n`` elements on device ``dev``."""
-    if x.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.numel() != n:
-        raise ValueError(f"{name} must be of {n} elements, got {list(x.shape)}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if x.get_device() != dev:
-        raise _elsewhere(name, x, dev)
-    return x.data_ptr()
+def _make_workspace(nbytes, stream) -> torch.Tensor:
+    """A workspace from torch's allocator on a stream that is not the current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raise ValueError("a call on a raw stream handle needs its own workspace")
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-def _grid(name, x, dev):
-    """Address, rows, columns and row stride of an int32 table."""
-    if x.dtype is not torch.int32:
-        raise ValueError(f"{name} must be torch.int32, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name} must have two dims")
-    (rows, width), (step, unit) = x.shape, x.stride()
-    if unit != 1 and width > 1:
-        raise ValueError(f"{name} must be unit-stride along its last dim")
-    if x.get_device() != dev:
-        raise _elsewhere(name, x, dev)
-    return x.data_ptr(), rows, width, step
+_binding.bind(_make_workspace, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+    "idx_plan_batch", "idx_store_kv_fp8", "idx_store_kv_bf16", "idx_page_bounds_fp8", "idx_page_bounds_bf16",
+    "idx_page_scores", "idx_kv_attention_fp8", "idx_kv_attention_bf16", "idx_kv_attention_workspace")))
 
 
-def _table(page_table, rows, row_table, dev):
-    """A page table's address, that of its rows' map, tables, width and row stride."""
-    at, tables, width, step = _grid("page_table", page_table, dev)
-    if row_table is not None:
-        return at, _flat("row_table", row_table, torch.int32, rows, dev), tables, width, step
-    if tables == 1:
-        step = 0
-    elif tables < rows:
-        raise ValueError(f"page_table holds {tables} tables for {rows} rows")
-    return at, None, 0, width, step
+def _handle(stream) -> int | None:
+    return None if stream is None else _stream_handle(stream, None)
 
 
-def _blocks(name, pool, dtypes, last, dev):
-    """Address, page stride and head stride (bytes) of a pool's blocks: [pages,
-    heads, *last], dense behind its first two dims."""
-    shape = pool.shape
-    if pool.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {pool.dtype}")
-    if len(shape) != 2 + len(last) or shape[2:] != last:
-        raise ValueError(f"{name} must be [pages, kv_heads, {', '.join(str(n) for n in last)}], got {list(shape)}")
-    step = pool.stride()
-    if step[-1] != 1 or (len(last) == 2 and step[2] != last[1]):
-        raise ValueError(f"{name} must be dense behind its first two dims")
-    if pool.get_device() != dev:
-        raise _elsewhere(name, pool, dev)
-    block = last[0] * last[1] if len(last) == 2 else last[0]
-    size = pool.element_size()
-    return pool.data_ptr(), (step[0] if shape[0] > 1 else max(step[0], block)) * size, step[1] * size
-
-
-def _alike(name, pool, first, dev) -> int:
-    """Address of a pool of the same type, shape and strides as the one before."""
-    if pool.dtype is not first.dtype or pool.shape != first.shape:
-        raise ValueError(f"{name} must be {first.dtype} {list(first.shape)}, as the one before it")
-    if pool.stride() != first.stride():
-        raise ValueError(f"{name} must have the strides of the one before it")
-    if pool.get_device() != dev:
-        raise _elsewhere(name, pool, dev)
-    return pool.data_ptr()
-
-
-_FP8 = (torch.uint8, torch.float8_e4m3fn)
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-
-
-def _kv_pools(fp8, k_pages, v_pages, scales, dim, dev):
-    """Addresses of the pools (keys, values, their scales) and their strides."""
-    kv, page, head = _blocks("k_pages", k_pages, _FP8 if fp8 else _BF16, (PAGE_POSITIONS, dim), dev)
-    where = (kv,) if v_pages is None else (kv, _alike("v_pages", v_pages, k_pages, dev))
-    if not fp8:
-        return where, (page, head)
-    kscale = scales[0]
-    at, *strides = _blocks("kscale", kscale, _F32, (PAGE_POSITIONS,), dev)
-    if kscale.shape[:2] != k_pages.shape[:2]:
-        raise ValueError("kscale must be of the keys' pages and heads")
-    if v_pages is None:
-        return where + (at,), (page, head, *strides)
-    return where + (at, _alike("vscale", scales[1], kscale, dev)), (page, head, *strides)
-
-
-def _num_pages(num_pages, pool):
-    """Pages of a pool, of which a call may take the first ``num_pages``."""
-    if num_pages is None:
-        return pool.shape[0]
-    if num_pages > pool.shape[0]:
-        raise ValueError(f"the pool holds {pool.shape[0]} pages, not {num_pages}")
-    return num_pages
+def _done(name, status, check) -> int:
+    """The status of a call, raised where it is an error and ``check``."""
+    if check and status != IDX_OK:
+        raise IdxError(status, f"{name}: {_STATUS_TEXT.get(status) or idx_status_string(status)}")
+    return status
 
 
 def idx_plan_batch(cached, added, free_pages, page_table, slots=None, positions=None, row_table=None, seqlens=None,
@@ -859,40 +794,9 @@ def idx_plan_batch(cached, added, free_pages, page_table, slots=None, positions=
     length 0), ``starts`` int64 [requests + 1] each request's first row, ``taken``
     int64 [1] the pages asked for.  Those that are None are not written.
     """
-    dev, requests = cached.get_device(), cached.numel()
-    have = _flat("cached", cached, torch.int32, requests, dev)
-    more = _flat("added", added, torch.int32, requests, dev)
-    num_free = free_pages.numel()
-    free = _flat("free_pages", free_pages, torch.int32, num_free, dev)
-    table, tables, width, step = _grid("page_table", page_table, dev)
-    if tables != requests:
-        raise ValueError(f"page_table holds {tables} tables for {requests} requests")
-    first = slots if slots is not None else positions if positions is not None else row_table if row_table is not None else seqlens
-    n = 0 if first is None else first.numel()
-    rows = (None if slots is None else _flat("slots", slots, torch.int64, n, dev),
-            None if positions is None else _flat("positions", positions, torch.int64, n, dev),
-            None if row_table is None else _flat("row_table", row_table, torch.int32, n, dev),
-            None if seqlens is None else _flat("seqlens", seqlens, torch.int32, n, dev),
-            None if starts is None else _flat("starts", starts, torch.int64, requests + 1, dev),
-            None if taken is None else _flat("taken", taken, torch.int64, 1, dev))
-    return _launch(_lib.idx_plan_batch, dev, stream, check, have, more, requests, free, num_free, table, width,
-                   step if requests > 1 else width, n, *rows)
-
-
-def _store_kv(fn, fp8, keys, values, slots, k_pages, v_pages, scales, num_pages, stream, check):
-    k_step, dev = _rows("keys", keys, 3), keys.get_device()
-    v_step, shape = _rows("values", values, 3), keys.shape
-    n, heads, dim = shape
-    if values.shape != shape:
-        raise ValueError(f"values must be {list(shape)}, got {list(values.shape)}")
-    if values.get_device() != dev:
-        raise _elsewhere("values", values, dev)
-    at = _flat("slots", slots, torch.int64, n, dev)
-    where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
-    if k_pages.shape[1] != heads:
-        raise ValueError(f"k_pages must have {heads} heads, got {k_pages.shape[1]}")
-    return _launch(fn, dev, stream, check, keys.data_ptr(), values.data_ptr(), at, n, heads, dim, k_step, v_step, *where,
-                   _num_pages(num_pages, k_pages), *strides)
+    status = _binding.plan_batch(cached, added, free_pages, page_table, slots, positions, row_table, seqlens, starts, taken,
+                                 _handle(stream))
+    return status and _done("idx_plan_batch", status, check)
 
 
 def idx_store_kv_fp8(keys, values, slots, k_pages, v_pages, kscale, vscale, *, num_pages=None, stream=None,
@@ -906,30 +810,14 @@ def idx_store_kv_fp8(keys, values, slots, k_pages, v_pages, kscale, vscale, *, n
     kv_heads, 64] likewise.  ``slots`` int64 [n] (64*page + position; out of range skips
     the token).
     """
-    return _store_kv(_lib.idx_store_kv_fp8, True, keys, values, slots, k_pages, v_pages, (kscale, vscale), num_pages,
-                     stream, check)
+    status = _binding.store_kv(True, keys, values, slots, k_pages, v_pages, kscale, vscale, num_pages, _handle(stream))
+    return status and _done("idx_store_kv_fp8", status, check)
 
 
 def idx_store_kv_bf16(keys, values, slots, k_pages, v_pages, *, num_pages=None, stream=None, check=True) -> int:
     """bf16 counterpart of :func:`idx_store_kv_fp8`: a copy."""
-    return _store_kv(_lib.idx_store_kv_bf16, False, keys, values, slots, k_pages, v_pages, (), num_pages, stream, check)
-
-
-def _page_bounds(fn, fp8, k_pages, kscale, page_table, seqlens, bounds, first, row_table, num_pages, stream, check):
-    dev = seqlens.get_device()
-    rows = seqlens.numel()
-    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
-    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
-    shape, near = k_pages.shape, bounds.shape
-    dim = shape[-1]
-    where, strides = _kv_pools(fp8, k_pages, None, (kscale,), dim, dev)
-    heads, pages = shape[1], _num_pages(num_pages, k_pages)
-    if len(near) != 4 or near[0] < pages or near[1:] != (heads, 2, dim):
-        raise ValueError(f"bounds must be [{pages}, {heads}, 2, {dim}], got {list(near)}")
-    to = _flat("bounds", bounds, torch.bfloat16, bounds.numel(), dev)
-    begin = None if first is None else _flat("first", first, torch.int32, rows, dev)
-    return _launch(fn, dev, stream, check, *where, table, which, tables, begin, lengths, to, rows, heads, dim, width, pages,
-                   *strides, step)
+    status = _binding.store_kv(False, keys, values, slots, k_pages, v_pages, None, None, num_pages, _handle(stream))
+    return status and _done("idx_store_kv_bf16", status, check)
 
 
 def idx_page_bounds_fp8(k_pages, kscale, page_table, seqlens, bounds, *, first=None, row_table=None, num_pages=None,
@@ -941,15 +829,17 @@ def idx_page_bounds_fp8(k_pages, kscale, page_table, seqlens, bounds, *, first=N
     Pools as in :func:`idx_store_kv_fp8`, ``page_table`` int32 [tables, width]: one for
     all rows, one per row, or row b's at ``row_table[b]``.
     """
-    return _page_bounds(_lib.idx_page_bounds_fp8, True, k_pages, kscale, page_table, seqlens, bounds, first, row_table,
-                        num_pages, stream, check)
+    status = _binding.page_bounds(True, k_pages, kscale, page_table, seqlens, bounds, first, row_table, num_pages,
+                                  _handle(stream))
+    return status and _done("idx_page_bounds_fp8", status, check)
 
 
 def idx_page_bounds_bf16(k_pages, page_table, seqlens, bounds, *, first=None, row_table=None, num_pages=None, stream=None,
                          check=True) -> int:
     """bf16 counterpart of :func:`idx_page_bounds_fp8`."""
-    return _page_bounds(_lib.idx_page_bounds_bf16, False, k_pages, None, page_table, seqlens, bounds, first, row_table,
-                        num_pages, stream, check)
+    status = _binding.page_bounds(False, k_pages, None, page_table, seqlens, bounds, first, row_table, num_pages,
+                                  _handle(stream))
+    return status and _done("idx_page_bounds_bf16", status, check)
 
 
 def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *, first_pages=0, last_pages=0,
@@ -963,67 +853,15 @@ def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *,
     ``scores.flatten(0, 1)`` and ``page_counts.flatten()`` are what
     :func:`idx_topk_logits` selects pages from (score rows a multiple of 4 apart).
     """
-    dev, shape, near = q.get_device(), q.shape, bounds.shape
-    if len(shape) != 3 or len(near) != 4 or near[2] != 2 or near[3] != shape[2]:
-        raise ValueError(f"q must be [rows, heads, D] and bounds [pages, kv_heads, 2, D], got {list(shape)} and {list(near)}")
-    rows, heads, dim = shape
-    pages, kv_heads = near[:2]
-    from_q = _flat("q", q, torch.bfloat16, rows * heads * dim, dev)
-    at = _flat("bounds", bounds, torch.bfloat16, bounds.numel(), dev)
-    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
-    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
-    if scores.dtype is not torch.float32:
-        raise ValueError(f"scores must be torch.float32, got {scores.dtype}")
-    if scores.shape != (rows, kv_heads, width):
-        raise ValueError(f"scores must be {[rows, kv_heads, width]}, got {list(scores.shape)}")
-    if scores.get_device() != dev:
-        raise _elsewhere("scores", scores, dev)
-    row, head, unit = scores.stride()
-    apart = head if kv_heads > 1 else row if rows > 1 else width
-    if (unit != 1 and width > 1) or (rows > 1 and kv_heads > 1 and row != kv_heads * head):
-        raise ValueError("scores must be unit-stride along its last dim, its rows evenly apart")
-    counts = None if page_counts is None else _flat("page_counts", page_counts, torch.int32, rows * kv_heads, dev)
-    return _launch(_lib.idx_page_scores, dev, stream, check, from_q, at, table, which, tables, lengths, scores.data_ptr(),
-                   counts, rows, heads, kv_heads, dim, width, pages, step, apart, first_pages, last_pages)
+    status = _binding.page_scores(q, bounds, page_table, seqlens, scores, page_counts, first_pages, last_pages, row_table,
+                                  _handle(stream))
+    return status and _done("idx_page_scores", status, check)
 
 
 def idx_kv_attention_workspace(rows, num_heads, kv_heads, head_dim, table_width, k=None) -> int:
     """Bytes of workspace that a call of :func:`idx_kv_attention_fp8` or its counterpart
     of these sizes needs on the current device (``k`` None: no selection)."""
     return _lib.idx_kv_attention_workspace(rows, num_heads, kv_heads, head_dim, table_width, -1 if k is None else k)
-
-
-def _kv_attention(fn, fp8, q, k_pages, v_pages, scales, page_table, page_idx, seqlens, out, lse, scale, num_pages, sinks,
-                  row_table, workspace, stream, check):
-    dev, shape = q.get_device(), q.shape
-    if len(shape) != 3 or out.shape != shape:
-        raise ValueError(f"q and out must be [rows, heads, D], got {list(shape)} and {list(out.shape)}")
-    rows, heads, dim = shape
-    size = rows * heads * dim
-    from_q = _flat("q", q, torch.bfloat16, size, dev)
-    to = _flat("out", out, torch.bfloat16, size, dev)
-    where, strides = _kv_pools(fp8, k_pages, v_pages, scales, dim, dev)
-    kv_heads = k_pages.shape[1]
-    table, which, tables, width, step = _table(page_table, rows, row_table, dev)
-    lengths = _flat("seqlens", seqlens, torch.int32, rows, dev)
-    idx = sink = log = None
-    k = -1
-    if page_idx is not None:
-        k = page_idx.shape[-1]
-        idx = _flat("page_idx", page_idx, torch.int32, rows * kv_heads * k, dev)
-    if sinks is not None:
-        sink = _flat("sinks", sinks, torch.float32, heads, dev)
-    if lse is not None:
-        log = _flat("lse", lse, torch.float32, rows * heads, dev)
-    if workspace is None:
-        workspace = _workspace(_lib.idx_kv_attention_workspace, (rows, heads, kv_heads, dim, width, k), dev, stream)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    elif workspace.get_device() != dev:
-        raise _elsewhere("workspace", workspace, dev)
-    space, nbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    return _launch(fn, dev, stream, check, from_q, *where, table, which, tables, idx, lengths, sink, to, log, rows, heads,
-                   kv_heads, dim, width, _num_pages(num_pages, k_pages), *strides, step, k, scale, space, nbytes)
 
 
 def idx_kv_attention_fp8(q, k_pages, v_pages, kscale, vscale, page_table, page_idx, seqlens, out, lse=None, *, scale,
@@ -1040,15 +878,17 @@ def idx_kv_attention_fp8(q, k_pages, v_pages, kscale, vscale, page_table, page_i
     :func:`idx_kv_attention_workspace` bytes, of this call's own while it runs; None takes
     one from torch's allocator.
     """
-    return _kv_attention(_lib.idx_kv_attention_fp8, True, q, k_pages, v_pages, (kscale, vscale), page_table, page_idx,
-                         seqlens, out, lse, scale, num_pages, sinks, row_table, workspace, stream, check)
+    status = _binding.kv_attention(True, q, k_pages, v_pages, kscale, vscale, page_table, page_idx, seqlens, out, lse, scale,
+                                   sinks, row_table, workspace, num_pages, _handle(stream), stream)
+    return status and _done("idx_kv_attention_fp8", status, check)
 
 
 def idx_kv_attention_bf16(q, k_pages, v_pages, page_table, page_idx, seqlens, out, lse=None, *, scale, sinks=None,
                           row_table=None, workspace=None, num_pages=None, stream=None, check=True) -> int:
     """bf16 counterpart of :func:`idx_kv_attention_fp8`."""
-    return _kv_attention(_lib.idx_kv_attention_bf16, False, q, k_pages, v_pages, (), page_table, page_idx, seqlens, out, lse,
-                         scale, num_pages, sinks, row_table, workspace, stream, check)
+    status = _binding.kv_attention(False, q, k_pages, v_pages, None, None, page_table, page_idx, seqlens, out, lse, scale,
+                                   sinks, row_table, workspace, num_pages, _handle(stream), stream)
+    return status and _done("idx_kv_attention_bf16", status, check)
 
 
 __all__ = [

@@ -135,7 +135,7 @@ ATTEND8 = ("q k v ks vs pt rt tables idx sl sinks out lse rows heads kvheads dim
            "space bytes stream")
 ATTEND16 = "q k v pt rt tables idx sl sinks out lse rows heads kvheads dim width pages kvp kvh pts topk scale space bytes stream"
 ATTEND = dict(q=16, k=16, v=16, ks=4, vs=4, pt=4, rt=4, tables=1, idx=4, sl=4, sinks=4, out=16, lse=4, rows=1, heads=8, kvheads=2,
-              dim=128, width=8, pages=1, kvp=65536, kvh=16384, ksp=512, ksh=256, pts=2, topk=4, scale=0.1, space=None, bytes=0,
+              dim=128, width=512, pages=1, kvp=65536, kvh=16384, ksp=512, ksh=256, pts=512, topk=512, scale=0.1, space=None, bytes=0,
               stream=None)
 
 
