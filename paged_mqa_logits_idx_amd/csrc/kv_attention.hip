@@ -44,7 +44,10 @@ namespace {
 constexpr float kLazy = 8.0f;     // base-2 logits that a tile's maximum exceeds its reference by where that moves
 constexpr float kNone = -3e38f;   // a reference before the first
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kMinShare = 2;  // pages of a workgroup's share, at least
+
+struct Cut {
+  int32_t share, by_unit;
+};
 
 struct Attend {
   const uint8_t* q;     // bf16 [rows][heads][D]
@@ -56,13 +59,15 @@ struct Attend {
   const float* sinks;   // [heads] or NULL
   uint8_t* out;         // bf16 [rows][heads][D]
   float* lse;           // [rows][heads] or NULL
-  int32_t* prefix;      // [rows + 1]: pages of the rows before, of one unit each (balanced)
+  Cut* cut;
+  int32_t* prefix;      // [rows + 1]: pages (by unit: pieces) of the rows before, of one unit each
   f32x2* ml;            // references and sums of the pieces: [2 * shares][16 * HW]
   f32x4* part;          // their outputs
   KvStrides s;
   uint32_t pages_lim;
   int32_t rows, heads, kv_heads, group, blocks, width, k;
   int32_t shares;       // workgroups with a share; 0: a unit each
+  int32_t least, slack, most_pieces;  // pages of a share; see cut_of
   float scale2;         // scale * log2(e)
 };
 
@@ -138,9 +143,25 @@ __device__ __forceinline__ int32_t pages_of(const Attend& a, int32_t L) {
   return a.k >= 0 ? min(a.k, c) : c;
 }
 
-// The pages of a workgroup's share.
-__device__ __forceinline__ int32_t share_pages(int32_t total, int32_t shares) {
-  return max((int32_t)(((uint32_t)total + (uint32_t)shares - 1) / (uint32_t)shares), kMinShare);
+// How the units' pages (`total` of all units) are cut: into shares of the same number
+// of pages, whatever units they are of, or each unit by itself into pieces of at
+// most that many, one a workgroup.  The latter has workgroups to spare for the units'
+// last pieces and larger shares for it, but no workgroup with two pieces, which cost
+// 3 us each; it is taken where the shares are no more than `slack` larger, and some
+// share would end inside a unit (`uneven`).  A unit is
+// not cut into more than 32 * HW pieces by far: joining them costs more than a
+// larger share (one row of 8 units of 128 pages: 64 pieces each 14.8 us, 32 pieces
+// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).
+template <class F>
+__device__ __forceinline__ Cut cut_of(const Attend& a, int32_t total, F uneven) {
+  const auto up = [](uint32_t x, uint32_t by) { return (int32_t)((x + by - 1) / by); };
+  const int32_t units = a.rows * a.kv_heads * a.blocks;
+  Cut c = {max(up((uint32_t)total, (uint32_t)a.shares), max(a.least, up((uint32_t)total, (uint32_t)(units * a.most_pieces)))), 0};
+  if (a.rows <= 64 && 2 * units <= a.shares) {
+    const int32_t more = max(c.share, up((uint32_t)total, (uint32_t)(a.shares - units)));
+    if (more - c.share <= a.slack && uneven(c.share)) c = {more, 1};
+  }
+  return c;
 }
 
 template <int KEY, int DIM, int HW>
@@ -153,10 +174,10 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
   const int wave = uniform(threadIdx.x >> 6), hw = wave % HW, group = wave / HW;
   const int32_t per_row = a.kv_heads * a.blocks;
 
-  // The workgroup's share: pages [at, end) of the units' in order, from page
-  // `page0` of unit `unit` of row `b`.
+  // The workgroup's pages: of units in order, `end` of them, from page `page0` of unit
+  // `unit` of row `b`.
   int64_t b;
-  int32_t unit, page0 = 0, count, at = 0, end, L;
+  int32_t unit, page0 = 0, count, end, L;
   int32_t early_j = 0, early_page = 0;  // of a unit's first 64 pages, looked up before the row's length is there
   if (a.shares == 0) {
     b = blockIdx.x / (uint32_t)per_row;
@@ -168,75 +189,97 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
     early_page = (uint32_t)early_j < (uint32_t)a.width && ok ? tab[early_j] : -1;
     L = length_of(a, b);
     count = end = pages_of(a, L);
-  } else {
-    const auto share_of = [&](int32_t total) {
-      const int32_t share = share_pages(total, a.shares);
-      at = (int32_t)min((int64_t)blockIdx.x * share, (int64_t)total);
-      end = min(at + share, total);
+  } else if (a.rows <= 64) {  // every wave by itself, a lane a row
+    const auto scan = [&](int32_t v) {
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int32_t u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+      }
+      return v;
     };
-    if (a.rows <= 64) {  // every wave by itself, a lane a row
-      const int32_t mine = lane < a.rows ? length_of(a, lane) : 0, own = pages_of(a, mine);
-      int32_t upto = own;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int32_t v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
-      }
-      if (blockIdx.x == 0 && wave == 0) {
-        if (lane < a.rows) a.prefix[lane] = upto - own;
-        if (lane == 63) a.prefix[a.rows] = upto;
-      }
-      share_of(__builtin_amdgcn_readlane(upto, 63) * per_row);
-      if (at >= end) return;
-      const int row = __builtin_ctzll(__ballot(upto * per_row > at));
-      b = row;
-      count = __builtin_amdgcn_readlane(own, row);
-      L = __builtin_amdgcn_readlane(mine, row);
-      page0 = at - (__builtin_amdgcn_readlane(upto, row) - count) * per_row;
-    } else {
-      const int32_t per = (a.rows + kThreads - 1) / kThreads;
-      const int32_t r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
-      int32_t own = 0;
-      for (int32_t r = r0; r < r1; ++r) own += pages_of(a, length_of(a, r));
-      int32_t upto = own;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const int32_t v = __shfl_up(upto, d);
-        if (lane >= d) upto += v;
-      }
-      if (lane == 63) sh.sums[wave] = upto;
-      __syncthreads();
-      int32_t total = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) upto += sh.sums[w];
-        total += sh.sums[w];
-      }
-      if (blockIdx.x == 0) {
-        int32_t p = upto - own;
-        for (int32_t r = r0; r < r1; ++r) {
-          a.prefix[r] = p;
-          p += pages_of(a, length_of(a, r));
-        }
-        if (threadIdx.x == 0) a.prefix[a.rows] = total;
-      }
-      share_of(total * per_row);
-      if (at >= end) return;
-      if (at < upto * per_row && at >= (upto - own) * per_row) {
-        int32_t p = (upto - own) * per_row, r = r0, c = pages_of(a, length_of(a, r));
-        while (at >= p + c * per_row) {
-          p += c * per_row;
-          c = pages_of(a, length_of(a, ++r));
-        }
-        sh.start[0] = r;
-        sh.start[1] = at - p;
-      }
-      __syncthreads();
-      b = uniform(sh.start[0]);
-      page0 = uniform(sh.start[1]);
-      L = uniform(length_of(a, b));
-      count = pages_of(a, L);
+    const int32_t mine = lane < a.rows ? length_of(a, lane) : 0, own = pages_of(a, mine);
+    int32_t each = own, upto = scan(own);  // what a unit of the lane's row counts for, and the rows before it with it
+    const Cut cut = cut_of(a, __builtin_amdgcn_readlane(upto, 63) * per_row, [&](int32_t share) {
+      return __ballot((uint32_t)own % (uint32_t)share != 0) != 0;
+    });
+    if (cut.by_unit) {
+      each = (own + cut.share - 1) / cut.share;
+      upto = scan(each);
     }
+    if (blockIdx.x == 0 && wave == 0) {
+      if (lane < a.rows) a.prefix[lane] = upto - each;
+      if (lane == 63) a.prefix[a.rows] = upto;
+      if (lane == 0) *a.cut = cut;
+    }
+    const int32_t total = __builtin_amdgcn_readlane(upto, 63) * per_row;
+    const int64_t first = cut.by_unit ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * cut.share;
+    if (first >= total) return;
+    const int row = __builtin_ctzll(__ballot(upto * per_row > (int32_t)first));
+    b = row;
+    L = __builtin_amdgcn_readlane(mine, row);
+    count = __builtin_amdgcn_readlane(own, row);
+    const int32_t n_each = __builtin_amdgcn_readlane(each, row);
+    const int32_t at = (int32_t)first - (__builtin_amdgcn_readlane(upto, row) - n_each) * per_row;
+    unit = at / n_each;
+    page0 = at - unit * n_each;
+    if (cut.by_unit) {
+      const int32_t piece = page0;
+      page0 = (int32_t)((int64_t)piece * count / n_each);
+      end = (int32_t)((int64_t)(piece + 1) * count / n_each) - page0;
+    } else {
+      end = min(cut.share, total - (int32_t)first);
+    }
+  } else {
+    const int32_t per = (a.rows + kThreads - 1) / kThreads;
+    const int32_t r0 = min((int)threadIdx.x * per, a.rows), r1 = min(r0 + per, a.rows);
+    int32_t own = 0;
+    for (int32_t r = r0; r < r1; ++r) own += pages_of(a, length_of(a, r));
+    int32_t upto = own;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int32_t v = __shfl_up(upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 63) sh.sums[wave] = upto;
+    __syncthreads();
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) upto += sh.sums[w];
+      total += sh.sums[w];
+    }
+    const Cut cut = cut_of(a, total * per_row, [](int32_t) { return false; });
+    if (blockIdx.x == 0) {
+      int32_t p = upto - own;
+      for (int32_t r = r0; r < r1; ++r) {
+        a.prefix[r] = p;
+        p += pages_of(a, length_of(a, r));
+      }
+      if (threadIdx.x == 0) {
+        a.prefix[a.rows] = total;
+        *a.cut = cut;
+      }
+    }
+    total *= per_row;
+    const int64_t first = (int64_t)blockIdx.x * cut.share;
+    if (first >= total) return;
+    end = min(cut.share, total - (int32_t)first);
+    const int32_t at = (int32_t)first;
+    if (at < upto * per_row && at >= (upto - own) * per_row) {
+      int32_t p = (upto - own) * per_row, r = r0, c = pages_of(a, length_of(a, r));
+      while (at >= p + c * per_row) {
+        p += c * per_row;
+        c = pages_of(a, length_of(a, ++r));
+      }
+      sh.start[0] = r;
+      sh.start[1] = at - p;
+    }
+    __syncthreads();
+    b = uniform(sh.start[0]);
+    page0 = uniform(sh.start[1]);
+    L = uniform(length_of(a, b));
+    count = pages_of(a, L);
     unit = page0 / count;
     page0 -= unit * count;
   }
@@ -257,7 +300,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
 
   int32_t slot = 0;  // of a piece that is not whole: the share's first, or its last
   while (true) {
-    const int32_t pages = a.shares == 0 ? count : min(count - page0, end - at);
+    const int32_t pages = min(count - page0, end);
     const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
     const int32_t head0 = h * a.group + 16 * (hb * HW + hw);        // the wave's first, of the row's
     const int32_t heads = min(16, a.group - 16 * (hb * HW + hw));    // (may be less than one)
@@ -555,8 +598,8 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
     barrier();  // (LDS is the next piece's)
     if (a.shares == 0) return;
     slot = 1;
-    at += pages;
-    if (at >= end) return;
+    end -= pages;
+    if (end <= 0) return;
     page0 = 0;
     if (++unit == per_row) {
       unit = 0;
@@ -583,10 +626,11 @@ __global__ __launch_bounds__(kThreads) void kv_join_kernel(Attend a) {
   const int32_t per_row = a.kv_heads * a.blocks;
   const int32_t b = (int32_t)(blockIdx.x / (uint32_t)per_row), unit = (int32_t)(blockIdx.x - (uint32_t)b * (uint32_t)per_row);
   const int32_t h = unit / a.blocks, hb = unit - h * a.blocks;
-  const int32_t before = a.prefix[b], count = a.prefix[b + 1] - before;
-  const int32_t share = share_pages(a.prefix[a.rows] * per_row, a.shares);
-  const int32_t s = before * per_row + unit * count;  // the unit's pages: s .. s + count
-  const int32_t w0 = s / share, w1 = count > 0 ? (s + count - 1) / share : w0 - 1;
+  const Cut cut = *a.cut;
+  const int32_t before = a.prefix[b], each = a.prefix[b + 1] - before;
+  const int32_t s = before * per_row + unit * each;  // the unit's pages or pieces: s .. s + each
+  const int32_t share = cut.by_unit ? 1 : cut.share;
+  const int32_t w0 = s / share, w1 = each > 0 ? (s + each - 1) / share : w0 - 1;
   if (w0 == w1) return;  // whole
   for (int block = FEW ? (int)blockIdx.y : (int)blockIdx.y * kWaves + wave; block < HW * kParts;
        block += FEW ? HW * kParts : (int)gridDim.y * kWaves) {
@@ -665,6 +709,7 @@ constexpr int64_t kMaxHeads = 8000000;  // of a call's rows together: a launch h
 
 struct Split {
   int hw, blocks, shares;  // waves of 16 heads of a unit, blocks of them a group, workgroups (0: a unit each)
+  int least, slack;
   int64_t bytes;
 };
 
@@ -689,7 +734,7 @@ int per_cu(int key, int32_t head_dim, int hw) {
 
 // From the scalar arguments alone (the lengths are on the device).
 Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
-  Split s = {1, 1, 0, 0};
+  Split s = {1, 1, 0, 0, 0, 0};
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
   while (s.hw < kWaves && 16 * s.hw < group) s.hw *= 2;
@@ -697,13 +742,25 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   const int64_t units = (int64_t)rows * kv_heads * s.blocks;
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
   const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.hw) * device_cu_count();
-  if (units > 4 * workgroups || units * most > INT32_MAX / 2 || most <= kMinShare) return s;
+  if (units > 4 * workgroups || units * most > INT32_MAX / 2) return s;
+  // A unit of few pages is done by its workgroup before a second kernel could join its
+  // pieces: 8 units of 4, 8 and 16 pages of 32 KB take 6.3, 8.4 and 12.3 us whole, 8.1,
+  // 8.2 and 8.8 cut; 64 units 6.6, 8.5 and 14.2, and 11.2, 11.8 and 15.4; 8 units of
+  // 64 heads and 2, 4 and 8 pages 8.2, 11.8 and 19.2, and 9.5, 12.3 and 12.9.  So are units
+  // that fill the device, unless rows may be far longer than others: 512 units of
+  // up to 16, 32 and 128 pages (a quarter of it the least) 36, 71 and 257 us, cut 45, 77
+  // and 248.
+  if (most * s.hw <= 8 || (2 * units >= workgroups && most <= 32)) return s;
+  // Selections are mostly of one size: whole units, where the last round of workgroups
+  // is full, nearly half full, or short (43008 bytes are 4 us of a workgroup's).
   const int64_t last = units % workgroups, page_bytes = (int64_t)2 * kPage * head_dim * (key == kFp8 ? 1 : 2);
   if (k >= 0 && (last == 0 || (2 * workgroups - 5 * last) * most * page_bytes < 5 * workgroups * 43008)) return s;
-  const int64_t want = (units * most + kMinShare - 1) / kMinShare;
+  s.least = s.hw == 4 ? 1 : 2;
+  s.slack = (int)(65536 / page_bytes);
+  const int64_t want = (units * most + s.least - 1) / s.least + units;  // (a unit's last piece may be short)
   s.shares = (int)(want < workgroups ? want : workgroups);
   if (s.shares < 1) s.shares = 1;
-  s.bytes = padded(4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.hw * 8) +
+  s.bytes = padded(8 + 4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.hw * 8) +
             2 * (int64_t)s.shares * s.hw * head_dim * 64;
   return s;
 }
@@ -765,8 +822,9 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   a.out = static_cast<uint8_t*>(out);
   a.lse = lse;
   uint8_t* space = static_cast<uint8_t*>(workspace);
-  a.prefix = reinterpret_cast<int32_t*>(space);
-  a.ml = reinterpret_cast<f32x2*>(space + padded(4 * ((int64_t)rows + 1)));
+  a.cut = reinterpret_cast<Cut*>(space);
+  a.prefix = reinterpret_cast<int32_t*>(space + 8);
+  a.ml = reinterpret_cast<f32x2*>(space + padded(8 + 4 * ((int64_t)rows + 1)));
   a.part = reinterpret_cast<f32x4*>(reinterpret_cast<uint8_t*>(a.ml) + padded(2 * (int64_t)split.shares * 16 * split.hw * 8));
   a.s = s;
   a.pages_lim = pages_limit(num_pages);
@@ -778,6 +836,9 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   a.width = table_width;
   a.k = k;
   a.shares = split.shares;
+  a.least = split.least;
+  a.slack = split.slack;
+  a.most_pieces = 32 * split.hw;
   a.scale2 = scale * kLog2e;
   (void)hipGetLastError();  // start from a clean error state
   if (head_dim == 64) launch_for<KEY, 64>(a, split, stream);
