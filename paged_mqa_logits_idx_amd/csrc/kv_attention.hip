@@ -68,6 +68,7 @@ struct Attend {
   int32_t rows, heads, kv_heads, group, blocks, width, k;
   int32_t shares;       // workgroups with a share; 0: a unit each
   int32_t least, slack, most_pieces;  // pages of a share; see cut_of
+  int32_t once;         // whether keys and values pass the caches by
   float scale2;         // scale * log2(e)
 };
 
@@ -90,8 +91,13 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 // (s_nop: a scalar that a vector instruction has written, as base's halves are, can be
 // read by a memory instruction five states on; the compiler counts them for its own
 // instructions, not for those in assembly.)
+// ONCE: of what is not read again soon, the first to leave the caches.
+template <bool ONCE>
 __device__ __forceinline__ void dma16_from(int64_t base, uint32_t off, uint32_t dst) {
-  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1 nt" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
+  else
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
 }
 
 template <int KEY, int DIM, int HW>
@@ -369,11 +375,15 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
       }
       const uint32_t to = lds_tile + (2 * place + kWhich) * F::kBytes + hw * (F::kBytes / HW);
       const uint32_t from = here(kWhich == 0 ? from_k : from_v);
+      const auto bring = [&](auto once) {
 #pragma unroll
-      for (int i = 0; i < F::kDmas; ++i) {
-        const int key = kWhich == 0 ? F::key_k(kRowsPerDma * i) : F::key_v(kRowsPerDma * i);
-        dma16_from(base, (from ^ (16 * key)) + 1024 * i, to + 1024 * i);
-      }
+        for (int i = 0; i < F::kDmas; ++i) {
+          const int key = kWhich == 0 ? F::key_k(kRowsPerDma * i) : F::key_v(kRowsPerDma * i);
+          dma16_from<decltype(once)::value>(base, (from ^ (16 * key)) + 1024 * i, to + 1024 * i);
+        }
+      };
+      if (a.once) bring(std::true_type{});
+      else bring(std::false_type{});
     };
     constexpr std::integral_constant<int, 0> kKeys{};
     constexpr std::integral_constant<int, 1> kVals{};
@@ -710,6 +720,7 @@ constexpr int64_t kMaxHeads = 8000000;  // of a call's rows together: a launch h
 struct Split {
   int hw, blocks, shares;  // waves of 16 heads of a unit, blocks of them a group, workgroups (0: a unit each)
   int least, slack;
+  bool once;
   int64_t bytes;
 };
 
@@ -734,7 +745,7 @@ int per_cu(int key, int32_t head_dim, int hw) {
 
 // From the scalar arguments alone (the lengths are on the device).
 Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
-  Split s = {1, 1, 0, 0, 0, 0};
+  Split s = {1, 1, 0, 0, 0, false, 0};
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
   while (s.hw < kWaves && 16 * s.hw < group) s.hw *= 2;
@@ -742,6 +753,14 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   const int64_t units = (int64_t)rows * kv_heads * s.blocks;
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
   const int64_t workgroups = (int64_t)per_cu(key, head_dim, s.hw) * device_cu_count();
+  const int64_t page_bytes = (int64_t)2 * kPage * head_dim * (key == kFp8 ? 1 : 2);
+  // Keys and values of a call that may read 256 MiB or more, the size of the last cache,
+  // would leave it before they are read again, and pass it by: 64 rows of 8 heads and 32
+  // selected pages of e4m3 (279 MB) 59 -> 52 us, all of up to 512 pages of bf16 (5.4 GB)
+  // 1025 -> 945, 64 rows of 2 heads with 32 queries each (335 MB) 75 -> 64.  But 33 rows of 8
+  // heads of 64 and 17 pages (39 MB, three such in turn) 13.1 -> 14.8, 32 rows of one head
+  // with 64 queries (84 MB) 30.5 -> 36.7.
+  s.once = s.blocks == 1 && units * most * page_bytes >= (int64_t)1 << 28;
   if (units > 4 * workgroups || units * most > INT32_MAX / 2) return s;
   // A unit of few pages is done by its workgroup before a second kernel could join its
   // pieces: 8 units of 4, 8 and 16 pages of 32 KB take 6.3, 8.4 and 12.3 us whole, 8.1,
@@ -753,7 +772,7 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   if (most * s.hw <= 8 || (2 * units >= workgroups && most <= 32)) return s;
   // Selections are mostly of one size: whole units, where the last round of workgroups
   // is full, nearly half full, or short (43008 bytes are 4 us of a workgroup's).
-  const int64_t last = units % workgroups, page_bytes = (int64_t)2 * kPage * head_dim * (key == kFp8 ? 1 : 2);
+  const int64_t last = units % workgroups;
   if (k >= 0 && (last == 0 || (2 * workgroups - 5 * last) * most * page_bytes < 5 * workgroups * 43008)) return s;
   s.least = s.hw == 4 ? 1 : 2;
   s.slack = (int)(65536 / page_bytes);
@@ -838,6 +857,7 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   a.shares = split.shares;
   a.least = split.least;
   a.slack = split.slack;
+  a.once = split.once;
   a.most_pieces = 32 * split.hw;
   a.scale2 = scale * kLog2e;
   (void)hipGetLastError();  // start from a clean error state

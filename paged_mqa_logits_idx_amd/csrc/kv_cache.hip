@@ -138,6 +138,13 @@ __global__ __launch_bounds__(THREADS) void plan_kernel(Plan p) {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
+// 16 bytes; ONCE: not read again soon, the first to leave the caches.
+template <bool ONCE>
+__device__ __forceinline__ u32x4 get(const uint8_t* from) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from));
+  return *reinterpret_cast<const u32x4*>(from);
+}
+
 struct Store {
   const uint8_t* x[2];  // keys, values (bf16)
   uint8_t* kv[2];
@@ -176,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void store_kv_kernel(Store p) {
         slot[u] = p.slots[t];
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-          raw[u][w] = *reinterpret_cast<const u32x4*>(p.x[w] + t * p.x_stride[w] + ((int64_t)head[u] * kDim + 8 * sub) * 2);
+          raw[u][w] = get<FAR>(p.x[w] + t * p.x_stride[w] + ((int64_t)head[u] * kDim + 8 * sub) * 2);
       }
     }
 #pragma unroll
@@ -246,6 +253,7 @@ __device__ __forceinline__ float fold_apart(float v, F f) {
 template <int KEY, int DIM>
 __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
   constexpr int kPer = KEY == kFp8 ? 16 : 8;  // values of a lane
+  constexpr int kRowBytes = KEY == kFp8 ? DIM : 2 * DIM;
   constexpr int LP = DIM / kPer, kLoads = LP, kStep = 64 / LP;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t b = blockIdx.x / p.side, first = ((int64_t)blockIdx.y * p.side + blockIdx.x % p.side) * kWaves + wave;
@@ -255,6 +263,10 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
   const int64_t j0 = p.first ? max(p.first[b], 0) / kPage : 0, j1 = (L + kPage - 1) / kPage;
   if (!table_ok || j0 >= j1) return;
   const int64_t items = (j1 - j0) * p.heads;
+  // (blocks pass the caches by where all rows, were they like this one, had 64 MiB or
+  // more: four prompts, 199 MB, 46.9 -> 42.7 us; but a decode step of 64 rows, 3.5 MB, 5.15
+  // -> 5.3)
+  const bool once = items * (kPage * kRowBytes) >= ((int64_t)1 << 26) / (gridDim.x / p.side);
   for (int64_t item = first; item < items; item += (int64_t)gridDim.y * p.side * kWaves) {
     const int64_t over = items <= UINT32_MAX ? (uint32_t)item / (uint32_t)p.heads : item / p.heads;
     const int64_t j = j0 + over, h = item - over * p.heads;
@@ -265,10 +277,22 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
     const float* scales = reinterpret_cast<const float*>(p.ks + (int64_t)page * p.s.ks_page + h * p.s.ks_head);
     u32x4 raw[kLoads];
     float scale[kLoads];
+    if constexpr (KEY == kFp8) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      raw[i] = *reinterpret_cast<const u32x4*>(block + 1024 * i + 16 * lane);
-      if constexpr (KEY == kFp8) scale[i] = scales[kStep * i + lane / LP];
+      for (int i = 0; i < kLoads; ++i) scale[i] = scales[kStep * i + lane / LP];
+    }
+    if (once) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = get<true>(block + 1024 * i + 16 * lane);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = get<false>(block + 1024 * i + 16 * lane);
+    }
+    if (live < kPage) {  // positions past the row's end: no numbers, which have no part
+      const uint32_t nan = KEY == kFp8 ? 0x7f7f7f7fu : 0x7fc07fc0u;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if (kStep * i + lane / LP >= live) raw[i] = (u32x4){nan, nan, nan, nan};
     }
     float lo[kPer], hi[kPer];
 #pragma unroll
@@ -286,12 +310,10 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
       } else {
         bf16x8_to_float(raw[i], v);
       }
-      const bool dead = kStep * i + lane / LP >= live;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        const float x = dead ? __builtin_nanf("") : v[e];
-        lo[e] = fminf(lo[e], x);
-        hi[e] = fmaxf(hi[e], x);
+        lo[e] = fminf(lo[e], v[e]);
+        hi[e] = fmaxf(hi[e], v[e]);
       }
     }
 #pragma unroll
