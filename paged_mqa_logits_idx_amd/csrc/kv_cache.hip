@@ -352,14 +352,19 @@ struct Scores {
 // max(q lo, q hi) is q hi where q is positive and q lo where it is negative, so the
 // sum is a product of [min(q, 0), max(q, 0)] with [lo, hi]: bf16 matrix instructions
 // with exact products and float32 sums.  A row's tiles are 16 pages of a head, heads
-// first, whose bounds stand side by side; a wave takes one.  A lane loads 16 bytes of a
-// page each as the B operand, against 16 query heads at a time, and then has 4 heads
-// of a page.
+// first, whose bounds stand side by side; a wave takes one: its bounds, whole rows, to
+// LDS by DMA, from there as the B operand against 16 query heads at a time; a lane then
+// has 4 heads of a page.
+__device__ const u32x4 kZeroBounds[4 * 256 / 16] = {};  // of pages that are none
+
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
-  constexpr int kSteps = DIM / 32;
+  constexpr int kSteps = DIM / 32, kRowBytes = 4 * DIM, kChunks = kRowBytes / 16, kRowsPerDma = 1024 / kRowBytes;
+  // chunk c (16 bytes) of row r stands at place c ^ r: 16 lanes read one chunk of 16 rows
+  __shared__ __attribute__((aligned(1024))) uint8_t rows[kWaves][16 * kRowBytes];
   const int lane = threadIdx.x & 63, n = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_u8*)&rows[wave][0];
   const int32_t group = p.heads / p.kv_heads;
   const int64_t units = (int64_t)p.rows * p.blocks;
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
@@ -382,13 +387,20 @@ __global__ __launch_bounds__(kThreads) void page_scores_kernel(Scores p) {
     if (j - n < count) {
       queries(0);
       const bool ok = (uint32_t)page < p.pages_lim && j < count;
+      const uint64_t row_at = (uint64_t)(ok ? p.bounds + ((int64_t)page * p.kv_heads + h) * kRowBytes : reinterpret_cast<const uint8_t*>(kZeroBounds));
+#pragma unroll
+      for (int i = 0; i < 16 / kRowsPerDma; ++i) {
+        const int r = kRowsPerDma * i + lane / kChunks;
+        const uint64_t at_r = (uint64_t)(uint32_t)__shfl((int)(row_at >> 32), r) << 32 | (uint32_t)__shfl((int)row_at, r);
+        dma16(reinterpret_cast<const uint8_t*>(at_r) + 16 * ((lane % kChunks) ^ r), lds + 1024 * i);
+      }
+      wait_vm<0>();
       bf16x8 side[2][kSteps];
-      const uint8_t* from = p.bounds + (((int64_t)(ok ? page : 0) * p.kv_heads + h) * 2 * DIM + 8 * quad) * 2;
 #pragma unroll
       for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-          side[w][s] = ok ? *reinterpret_cast<const bf16x8*>(from + (w * DIM + 32 * s) * 2) : (bf16x8)((__bf16)0.0f);
+          side[w][s] = *reinterpret_cast<const bf16x8*>(&rows[wave][n * kRowBytes + 16 * ((w * (DIM / 8) + 4 * s + quad) ^ n)]);
       for (int32_t i = 0;;) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
