@@ -391,26 +391,37 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
     f32x4 x[kSubs];        // of a tile's positions 16 * s + 4 * quad .. and head n: scores, then base-2 logits
     f32x4 ks[kSubs], vs[kSubs];
     bf16x8 w[kSubs / 2];   // probabilities
+    // (All reads of a tile's keys, or of 32 positions' values, are asked for before the
+    // first product: left to itself the compiler waits for each where it is used.)
     auto score = [&](int place) {
       const uint32_t from = here(lane_k + place * 2 * F::kBytes);
+      u32x4 raw[F::kChunks / 4][kSubs];
 #pragma unroll
-      for (int s = 0; s < kSubs; ++s) {
-        if constexpr (KEY == kFp8) {
+      for (int c = 0; c < F::kChunks / 4; ++c)
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) raw[c][s] = *(lds_u32x4*)(uintptr_t)((from ^ (64 * c)) + 16 * s * kRowBytes);
+      if constexpr (KEY == kFp8) {
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) {
           ks[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][0][16 * s + 4 * quad]);
           vs[s] = *reinterpret_cast<const f32x4*>(&sh.scale[wave][place][1][16 * s + 4 * quad]);
         }
-        x[s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int c = 0; c < F::kChunks / 4; ++c) {
-          const u32x4 raw = *(lds_u32x4*)(uintptr_t)((from ^ (64 * c)) + 16 * s * kRowBytes);
+      for (int s = 0; s < kSubs; ++s) x[s] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < F::kChunks / 4; ++c)
+#pragma unroll
+        for (int s = 0; s < kSubs; ++s) {
+          const u32x4 k = raw[c][s];
           if constexpr (KEY == kFp8) {
-            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(raw.x, raw.y), q[2 * c], x[s], 0, 0, 0);
-            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(raw.z, raw.w), q[2 * c + 1], x[s], 0, 0, 0);
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(k.x, k.y), q[2 * c], x[s], 0, 0, 0);
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8x8_to_bf16x8(k.z, k.w), q[2 * c + 1], x[s], 0, 0, 0);
           } else {
-            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, raw), q[c], x[s], 0, 0, 0);
+            x[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k), q[c], x[s], 0, 0, 0);
           }
         }
-      }
     };
     auto weigh = [&](int32_t left) {
 #pragma unroll
@@ -457,18 +468,26 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
       const uint32_t from = here(lane_v + place * 2 * F::kBytes);
 #pragma unroll
       for (int i = 0; i < kSubs / 2; ++i) {
+        v4s u[kParts][2];  // (e4m3: one of 8 codes)
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          if constexpr (KEY == kFp8) {
+            u[p][0] = __builtin_bit_cast(v4s, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(uintptr_t)((from ^ (16 * p)) + 32 * i * kRowBytes)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              u[p][e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)((from ^ (32 * p)) + (32 * i + 16 * e) * kRowBytes));
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
           bf16x8 v;
           if constexpr (KEY == kFp8) {
-            const v2i c = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(uintptr_t)((from ^ (16 * p)) + 32 * i * kRowBytes));
-            v = fp8x8_to_bf16x8((uint32_t)c.x, (uint32_t)c.y);
+            const u32x2 c = __builtin_bit_cast(u32x2, u[p][0]);
+            v = fp8x8_to_bf16x8(c.x, c.y);
           } else {
-            v4s u[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              u[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(uintptr_t)((from ^ (32 * p)) + (32 * i + 16 * e) * kRowBytes));
-            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u[0], u[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u[p][0], u[p][1], 0, 1, 2, 3, 4, 5, 6, 7));
           }
           acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[i], acc[p], 0, 0, 0);
         }
