@@ -67,7 +67,7 @@ struct Attend {
   uint32_t pages_lim;
   int32_t rows, heads, kv_heads, group, blocks, width, k;
   int32_t shares;       // workgroups with a share; 0: a unit each
-  int32_t least, slack, most_pieces;  // pages of a share; see cut_of
+  int32_t least, slack, few, most_pieces;  // pages of a share; see cut_of
   int32_t once;         // whether keys and values pass the caches by
   float scale2;         // scale * log2(e)
 };
@@ -157,12 +157,20 @@ __device__ __forceinline__ int32_t pages_of(const Attend& a, int32_t L) {
 // share would end inside a unit (`uneven`).  A unit is
 // not cut into more than 32 * HW pieces by far: joining them costs more than a
 // larger share (one row of 8 units of 128 pages: 64 pieces each 14.8 us, 32 pieces
-// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).
+// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).  Pieces of 64 heads are as many
+// bytes as a page of their keys and values: shares of up to `few` pages are made
+// by half the workgroups (8 rows of up to 64 and 128 pages 16.6 and 18.1 us by all, 13.9
+// and 16.7 by half; 32 rows 21.6 and 27.1, and 20.8 and 29.4).
 template <class F>
 __device__ __forceinline__ Cut cut_of(const Attend& a, int32_t total, F uneven) {
   const auto up = [](uint32_t x, uint32_t by) { return (int32_t)((x + by - 1) / by); };
   const int32_t units = a.rows * a.kv_heads * a.blocks;
-  Cut c = {max(up((uint32_t)total, (uint32_t)a.shares), max(a.least, up((uint32_t)total, (uint32_t)(units * a.most_pieces)))), 0};
+  int32_t share = up((uint32_t)total, (uint32_t)a.shares);
+  if (a.few > 0) {
+    const int32_t twice = up((uint32_t)total, (uint32_t)(a.shares / 2));
+    if (twice <= a.few) share = twice;
+  }
+  Cut c = {max(share, max(a.least, up((uint32_t)total, (uint32_t)(units * a.most_pieces)))), 0};
   if (a.rows <= 64 && 2 * units <= a.shares) {
     const int32_t more = max(c.share, up((uint32_t)total, (uint32_t)(a.shares - units)));
     if (more - c.share <= a.slack && uneven(c.share)) c = {more, 1};
@@ -749,7 +757,7 @@ constexpr int64_t kMaxHeads = 8000000;  // of a call's rows together: a launch h
 
 struct Split {
   int hw, blocks, shares;  // waves of 16 heads of a unit, blocks of them a group, workgroups (0: a unit each)
-  int least, slack;
+  int least, slack, few;
   bool once;
   int64_t bytes;
 };
@@ -775,7 +783,7 @@ int per_cu(int key, int32_t head_dim, int hw) {
 
 // From the scalar arguments alone (the lengths are on the device).
 Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32_t head_dim, int32_t table_width, int32_t k) {
-  Split s = {1, 1, 0, 0, 0, false, 0};
+  Split s = {1, 1, 0, 0, 0, 0, false, 0};
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
   while (s.hw < kWaves && 16 * s.hw < group) s.hw *= 2;
@@ -808,7 +816,7 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   s.slack = (int)(65536 / page_bytes);
   const int64_t want = (units * most + s.least - 1) / s.least + units;  // (a unit's last piece may be short)
   s.shares = (int)(want < workgroups ? want : workgroups);
-  if (s.shares < 1) s.shares = 1;
+  if (s.hw == kWaves && s.shares > device_cu_count()) s.few = (int)(196608 / page_bytes);
   s.bytes = padded(8 + 4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.hw * 8) +
             2 * (int64_t)s.shares * s.hw * head_dim * 64;
   return s;
@@ -819,7 +827,11 @@ void launch(const Attend& a, const Split& split, hipStream_t stream) {
   const uint32_t units = (uint32_t)((int64_t)a.rows * a.kv_heads * a.blocks);
   kv_attention_kernel<KEY, DIM, HW><<<dim3(split.shares ? (uint32_t)split.shares : units), dim3(kThreads), 0, stream>>>(a);
   if (split.shares == 0) return;
-  if (split.shares >= 8 * (int64_t)units) kv_join_kernel<DIM, HW, true><<<dim3(units, HW * DIM / 16), dim3(kThreads), 0, stream>>>(a);
+  // Pieces are shared among waves where a unit may have 16, or 8 and few blocks in all (32
+  // units of 32 blocks, 8 pieces each: 14.4 us so, the attention with it, 12.4 otherwise; one
+  // unit of them 9.2 and 9.5).
+  const int64_t blocks = (int64_t)units * HW * DIM / 16;
+  if (split.shares >= (blocks <= 512 ? 8 : 16) * (int64_t)units) kv_join_kernel<DIM, HW, true><<<dim3(units, HW * DIM / 16), dim3(kThreads), 0, stream>>>(a);
   else {
     uint32_t y = 512 / units;
     if (y > HW * DIM / 16 / kWaves) y = HW * DIM / 16 / kWaves;
@@ -887,6 +899,7 @@ int kv_attention(const void* q, const void* k_pages, const void* v_pages, const 
   a.shares = split.shares;
   a.least = split.least;
   a.slack = split.slack;
+  a.few = split.few;
   a.once = split.once;
   a.most_pieces = 32 * split.hw;
   a.scale2 = scale * kLog2e;
