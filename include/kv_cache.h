@@ -151,10 +151,10 @@ int idx_page_bounds_bf16(const void* k_pages, const int32_t* page_table, const i
  *                     -inf                                                                j >= C_b
  *
  * with C_b = ceil(L_b / 64) live pages, L_b as above, g = page_table_b[j], lo and hi
- * the bounds of idx_page_bounds; +inf for the first first_pages and the last
- * last_pages of the live ones, which so are selected first.  Group h is the heads
+ * the bounds of idx_page_bounds (lo <= hi); +inf for the first first_pages and the
+ * last last_pages of the live ones, which so are selected first.  Group h is the heads
  * h*G .. h*G + G - 1, G = num_heads / kv_heads.  Sums are float32; a NaN among q or
- * the bounds makes the score NaN.  A page id outside [0, num_pages), or a table index
+ * the bounds makes the score NaN, an infinity may.  A page id outside [0, num_pages), or a table index
  * outside [0, num_tables), scores NaN (a page of the first or last ones +inf).
  * page_counts[b][h] = C_b: scores and counts are what idx_topk_logits takes (rows *
  * kv_heads rows of table_width columns), and what it selects is the page_idx of

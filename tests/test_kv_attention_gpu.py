@@ -387,3 +387,98 @@ def test_a_run_of_them_together(lib):
         assert (want_live == live).all() and np.allclose(f64(scores), want_scores, rtol=1e-5, atol=1e-4)
         want = ref.attention(f64(q), key_values, value_values, table.cpu().numpy(), picks, lens.cpu().numpy(), dim ** -0.5, pages)
         assert_near_attention(out, lse, want, dim, k * PAGE)
+
+
+@pytest.mark.parametrize("seed", range(36))
+def test_random_shapes(lib, seed):
+    """Sizes across the ways of dividing a call: whole units, shares, units by themselves, few and many rows."""
+    rng = np.random.default_rng(seed)
+    dim = int(rng.choice([64, 128, 256]))
+    kv_heads = int(rng.choice([1, 1, 2, 3, 8]))
+    group = int(rng.choice([1, 3, 8, 16, 17, 30, 33, 64, 100, 128]))
+    rows = int(rng.choice([1, 2, 7, 40, 64, 65, 100, 150]))
+    width = int(rng.choice([1, 3, 9, 20, 33, 70]))
+    while rows * kv_heads * width * dim > 1_500_000 or rows * kv_heads * group > 6000:
+        rows, width = max(1, rows // 2), max(1, width * 2 // 3)
+    lengths = (rng.random(rows) ** 2 * (64 * width + 1)).astype(int)
+    lengths[rng.integers(rows)] = 64 * width
+    if rows > 3:
+        lengths[rng.integers(rows)] = 0
+    k = None if rng.random() < 0.6 else int(rng.integers(0, width + 3))
+    Case(seed, lengths.tolist(), kv_heads * group, kv_heads, dim, width, bool(rng.random() < 0.5), k=k, sinks=bool(rng.random() < 0.5),
+         layout=str(rng.choice(["fused", "heads", "apart"]))).check(lib)
+
+
+@pytest.mark.parametrize("rows,width,heads,kv_heads", [(65, 40, 8, 2), (100, 60, 2, 1), (200, 35, 3, 3), (130, 70, 64, 1)])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_many_rows_shared_out(lib, rows, width, heads, kv_heads, fp8):
+    """More rows than lanes, cut into shares; some empty, one far longer than the others."""
+    rng = np.random.default_rng(rows)
+    lengths = np.where(rng.random(rows) < 0.2, 0, rng.integers(1, 500, rows))
+    lengths[rows // 2] = 64 * width
+    assert lib.idx_kv_attention_workspace(rows, heads, kv_heads, 64, width) > 0
+    Case(rows, lengths.tolist(), heads, kv_heads, 64, width, fp8, sinks=True).check(lib)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30])
+def test_scales(lib, scale):
+    """Nothing, turned round, next to nothing."""
+    Case(41, LENGTHS, 8, 2, 128, 10, True, scale=scale).check(lib)
+    Case(42, LENGTHS, 40, 1, 64, 10, False, scale=scale, sinks=True).check(lib)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_far_pages(lib, fp8):
+    """Pages 2 GiB apart, heads in any order: offsets past 32 bits; stored, bounded and attended to."""
+    gen = torch.Generator().manual_seed(50)
+    pages, kv_heads, dim, apart = 4, 2, 128, 1 << 31
+    size = 1 if fp8 else 2
+    block = 64 * dim * size
+    flat = torch.zeros(3 * apart + 8 * block, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn if fp8 else BF16)
+    strides = (apart // size, 4 * block // size, dim, 1)
+    k = flat.as_strided((pages, kv_heads, 64, dim), strides)
+    v = flat.as_strided((pages, kv_heads, 64, dim), strides, 2 * block // size)
+    scales = tuple(torch.zeros((pages, kv_heads, 64), device="cuda") for _ in range(2)) if fp8 else ()
+    n = 200
+    x = torch.randn((n, 2, kv_heads, dim), generator=gen).to(BF16).cuda()
+    table = torch.tensor([[3, 1, 2, 0]], dtype=I32, device="cuda")
+    at = torch.arange(n, device="cuda")
+    slots = table[0].long()[at // 64] * 64 + at % 64
+    store, bound, attend = ((lib.idx_store_kv_fp8, lib.idx_page_bounds_fp8, lib.idx_kv_attention_fp8) if fp8 else
+                            (lib.idx_store_kv_bf16, lib.idx_page_bounds_bf16, lib.idx_kv_attention_bf16))
+    store(x[:, 0], x[:, 1], slots, k, v, *scales)
+    near = torch.zeros((pages, kv_heads, 2, dim), dtype=BF16, device="cuda")
+    lengths = i32([n])
+    bound(k, *scales[:1], table, lengths, near)
+    q = torch.randn((1, 8, dim), generator=gen).to(BF16).cuda()
+    out, lse = torch.empty_like(q), torch.empty((1, 8), device="cuda")
+    attend(q, k, v, *scales, table, None, lengths, out, lse, scale=0.1)
+    torch.cuda.synchronize()
+    keys, values = (values_of(p.contiguous(), s) for p, s in ((k, scales[0] if fp8 else None), (v, scales[1] if fp8 else None)))
+    got = keys[slots.cpu().numpy() // 64, :, slots.cpu().numpy() % 64]
+    want = f64(x[:, 0])
+    assert (got == want).all() if not fp8 else (np.abs(got - want) <= np.abs(want) * 2.0 ** -4 * 1.01 + 0.01).all()
+    limits = ref.bounds(keys, table.cpu().numpy(), [0], [n], np.zeros((pages, kv_heads, 2, dim)), pages)
+    assert (np.abs(f64(near) - limits) <= np.abs(limits) * 2.0 ** -7).all()
+    assert_near_attention(out, lse, ref.attention(f64(q), keys, values, table.cpu().numpy(), None, [n], 0.1, pages), dim, n)
+
+
+def test_heads_are_pools_of_the_other_operators(lib):
+    """A head of the keys is a pool that idx_load_slots_fp8 reads and idx_norm_rope_store_fp8 writes."""
+    gen = torch.Generator().manual_seed(51)
+    pages, kv_heads, dim = 5, 3, 128
+    k, v, (ks, vs) = make_pools(gen, pages, kv_heads, dim, True, "fused")
+    slots = torch.randperm(pages * 64, generator=gen)[:100].cuda()
+    stride = dict(num_pages=pages, kv_page_stride=k.stride(0), kscale_page_stride=4 * ks.stride(0))
+    for h in range(kv_heads):
+        x = torch.randn((100, dim), generator=gen).to(BF16).cuda()
+        at, scale_at = k.data_ptr() + h * k.stride(1), ks.data_ptr() + 4 * h * ks.stride(1)
+        lib.idx_norm_rope_store_fp8(x, None, None, slots, at, scale_at, norm=False, **stride)
+        other, _, (other_scale, _) = make_pools(torch.Generator().manual_seed(0), pages, 1, dim, True, "apart")
+        lib.idx_store_kv_fp8(x[:, None], x[:, None], slots, other, other.clone(), other_scale, other_scale.clone())
+        page, pos = slots // 64, slots % 64
+        assert torch.equal(k.view(torch.uint8)[page, h, pos], other.view(torch.uint8)[page, 0, pos])
+        back = torch.empty((100, dim), dtype=BF16, device="cuda")
+        lib.idx_load_slots_fp8(at, scale_at, slots, back, **stride)
+        want = k.view(torch.uint8)[page, h, pos].view(torch.float8_e4m3fn).float() * ks[page, h, pos][:, None]
+        assert torch.equal(back, want.to(BF16))

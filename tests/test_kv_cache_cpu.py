@@ -270,3 +270,19 @@ def test_binding_refusals_scores(kw, text):
     a.update(kw)
     with pytest.raises(ValueError, match=text):
         b.idx_page_scores(**a)
+
+
+def test_binding_takes_tensors_alone():
+    """What is no tensor, or too few of them, is refused by name."""
+    import paged_mqa_logits_idx_amd as b
+
+    with pytest.raises(ValueError, match="q must be a tensor"):
+        attend(q=[1.0])
+    with pytest.raises(ValueError, match="page_table must be a tensor"):
+        attend(page_table=None)
+    with pytest.raises(TypeError):
+        attend(scale="half")
+    with pytest.raises(TypeError):
+        attend(num_pages=1.5)
+    with pytest.raises(TypeError, match="arguments"):
+        b._binding.plan_batch(1)
