@@ -128,6 +128,7 @@ int idx_store_kv_bf16(const void* keys, const void* values, const int64_t* slots
  *   first      int32 [rows], 4-byte aligned, or NULL: 0 for all (a negative one too).
  *   seqlens    int32 [rows], 4-byte aligned.
  *   bounds     bf16 [num_pages][kv_heads][2][head_dim], 16-byte aligned.
+ *   rows * ceil(kv_heads / 4) less than 2^24.
  */
 int idx_page_bounds_fp8(const void* k_pages, const float* kscale, const int32_t* page_table,
                         const int32_t* row_table, int32_t num_tables, const int32_t* first,
@@ -166,7 +167,8 @@ int idx_page_bounds_bf16(const void* k_pages, const int32_t* page_table, const i
  *                (elements, >= table_width); 4-byte aligned.  Every element below
  *                table_width is written.
  *   page_counts  int32 [rows][kv_heads], 4-byte aligned, or NULL.
- *   num_heads    a multiple of kv_heads, at most 128 * kv_heads.
+ *   num_heads    a multiple of kv_heads, at most 128 * kv_heads; 0 returns IDX_OK with
+ *                no launch.
  *   first_pages, last_pages   >= 0.
  */
 int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table, const int32_t* row_table,

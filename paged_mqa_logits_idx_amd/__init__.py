@@ -3,8 +3,9 @@
 Argument marshalling only: every step of the computation runs in the library's
 HIP kernels (the marshalling of the newer functions is compiled, csrc/binding.cpp).
 The functions carry the C-ABI names and argument order; they
-accept torch device tensors (or raw device addresses as ints) and pass their
-addresses and sizes through ctypes.  torch supplies device memory and streams.
+accept torch device tensors (or raw device addresses as ints, but for the
+compiled ones) and pass their addresses and sizes through ctypes.  torch supplies
+device memory and streams.
 
 The library must be built in-tree first (``python paged_mqa_logits_idx_amd/_build.py``
 or ``__graft_entry__.build()``); importing this module without it raises.
@@ -771,10 +772,6 @@ _binding.bind(_make_workspace, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_
     "idx_page_scores", "idx_kv_attention_fp8", "idx_kv_attention_bf16", "idx_kv_attention_workspace")))
 
 
-def _handle(stream) -> int | None:
-    return None if stream is None else _stream_handle(stream, None)
-
-
 def _done(name, status, check) -> int:
     """The status of a call, raised where it is an error and ``check``."""
     if check and status != IDX_OK:
@@ -795,7 +792,7 @@ def idx_plan_batch(cached, added, free_pages, page_table, slots=None, positions=
     int64 [1] the pages asked for.  Those that are None are not written.
     """
     status = _binding.plan_batch(cached, added, free_pages, page_table, slots, positions, row_table, seqlens, starts, taken,
-                                 _handle(stream))
+                                 stream)
     return status and _done("idx_plan_batch", status, check)
 
 
@@ -810,13 +807,13 @@ def idx_store_kv_fp8(keys, values, slots, k_pages, v_pages, kscale, vscale, *, n
     kv_heads, 64] likewise.  ``slots`` int64 [n] (64*page + position; out of range skips
     the token).
     """
-    status = _binding.store_kv(True, keys, values, slots, k_pages, v_pages, kscale, vscale, num_pages, _handle(stream))
+    status = _binding.store_kv(True, keys, values, slots, k_pages, v_pages, kscale, vscale, num_pages, stream)
     return status and _done("idx_store_kv_fp8", status, check)
 
 
 def idx_store_kv_bf16(keys, values, slots, k_pages, v_pages, *, num_pages=None, stream=None, check=True) -> int:
     """bf16 counterpart of :func:`idx_store_kv_fp8`: a copy."""
-    status = _binding.store_kv(False, keys, values, slots, k_pages, v_pages, None, None, num_pages, _handle(stream))
+    status = _binding.store_kv(False, keys, values, slots, k_pages, v_pages, None, None, num_pages, stream)
     return status and _done("idx_store_kv_bf16", status, check)
 
 
@@ -830,7 +827,7 @@ def idx_page_bounds_fp8(k_pages, kscale, page_table, seqlens, bounds, *, first=N
     all rows, one per row, or row b's at ``row_table[b]``.
     """
     status = _binding.page_bounds(True, k_pages, kscale, page_table, seqlens, bounds, first, row_table, num_pages,
-                                  _handle(stream))
+                                  stream)
     return status and _done("idx_page_bounds_fp8", status, check)
 
 
@@ -838,7 +835,7 @@ def idx_page_bounds_bf16(k_pages, page_table, seqlens, bounds, *, first=None, ro
                          check=True) -> int:
     """bf16 counterpart of :func:`idx_page_bounds_fp8`."""
     status = _binding.page_bounds(False, k_pages, None, page_table, seqlens, bounds, first, row_table, num_pages,
-                                  _handle(stream))
+                                  stream)
     return status and _done("idx_page_bounds_bf16", status, check)
 
 
@@ -854,7 +851,7 @@ def idx_page_scores(q, bounds, page_table, seqlens, scores, page_counts=None, *,
     :func:`idx_topk_logits` selects pages from (score rows a multiple of 4 apart).
     """
     status = _binding.page_scores(q, bounds, page_table, seqlens, scores, page_counts, first_pages, last_pages, row_table,
-                                  _handle(stream))
+                                  stream)
     return status and _done("idx_page_scores", status, check)
 
 
@@ -879,7 +876,7 @@ def idx_kv_attention_fp8(q, k_pages, v_pages, kscale, vscale, page_table, page_i
     one from torch's allocator.
     """
     status = _binding.kv_attention(True, q, k_pages, v_pages, kscale, vscale, page_table, page_idx, seqlens, out, lse, scale,
-                                   sinks, row_table, workspace, num_pages, _handle(stream), stream)
+                                   sinks, row_table, workspace, num_pages, stream)
     return status and _done("idx_kv_attention_fp8", status, check)
 
 
@@ -887,7 +884,7 @@ def idx_kv_attention_bf16(q, k_pages, v_pages, page_table, page_idx, seqlens, ou
                           row_table=None, workspace=None, num_pages=None, stream=None, check=True) -> int:
     """bf16 counterpart of :func:`idx_kv_attention_fp8`."""
     status = _binding.kv_attention(False, q, k_pages, v_pages, None, None, page_table, page_idx, seqlens, out, lse, scale,
-                                   sinks, row_table, workspace, num_pages, _handle(stream), stream)
+                                   sinks, row_table, workspace, num_pages, stream)
     return status and _done("idx_kv_attention_bf16", status, check)
 
 

@@ -218,18 +218,33 @@ int64_t pages_taken(PyObject* num_pages, int64_t pages) {
   return n;
 }
 
+// The handle of a torch stream, which must be of the arguments' device, or of a number.
+hipStream_t handle_of(PyObject* stream, const Place& place) {
+  PyObject* number = nullptr;
+  if (PyObject_HasAttrString(stream, "cuda_stream")) {
+    PyObject* index = PyObject_GetAttrString(stream, "device_index");
+    if (!index) throw Refused();
+    const int64_t device = PyLong_AsLongLong(index);
+    Py_DECREF(index);
+    if (device == -1 && PyErr_Occurred()) throw Refused();
+    if (device != place.device.index()) refuse("stream is on cuda:%lld, the tensors on %s", (long long)device, place.device.str().c_str());
+    number = PyObject_GetAttrString(stream, "cuda_stream");
+  } else {
+    number = PyNumber_Long(stream);
+  }
+  if (!number) throw Refused();
+  void* handle = PyLong_AsVoidPtr(number);
+  Py_DECREF(number);
+  if (PyErr_Occurred()) throw Refused();
+  return static_cast<hipStream_t>(handle);
+}
+
 // Calls f(stream) on the arguments' device, whatever the current one is.
 template <class F>
 PyObject* launch(const Place& place, PyObject* stream, F f) {
   if (!place.device.is_cuda()) refuse("tensors passed to the indexer library must be device tensors");
   const c10::DeviceGuard guard(place.device);
-  hipStream_t handle;
-  if (stream == Py_None) {
-    handle = c10::hip::getCurrentHIPStream(place.device.index()).stream();
-  } else {
-    handle = reinterpret_cast<hipStream_t>(PyLong_AsVoidPtr(stream));
-    if (PyErr_Occurred()) throw Refused();
-  }
+  const hipStream_t handle = stream == Py_None ? c10::hip::getCurrentHIPStream(place.device.index()).stream() : handle_of(stream, place);
   return PyLong_FromLong(f(handle));
 }
 
@@ -362,7 +377,7 @@ PyObject* page_scores(PyObject*, PyObject* const* x, Py_ssize_t n) {
 }
 
 PyObject* kv_attention(PyObject*, PyObject* const* x, Py_ssize_t n) {
-  return guarded(n, 18, [&] {
+  return guarded(n, 17, [&] {
     const bool fp8 = x[0] == Py_True;
     const at::Tensor &q = tensor("q", x[1]), &out = tensor("out", x[9]);
     if (q.dim() != 3 || out.sizes() != q.sizes())
@@ -399,7 +414,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* x, Py_ssize_t n) {
         if (need > 0 && x[16] == Py_None) {
           workspace = at::empty({need}, at::TensorOptions(at::kByte).device(place.device));
         } else if (need > 0) {
-          PyObject* made = PyObject_CallFunction(make_workspace, "LO", (long long)need, x[17]);
+          PyObject* made = PyObject_CallFunction(make_workspace, "LO", (long long)need, x[16]);
           if (!made) throw Refused();
           workspace = THPVariable_Unpack(made);
           Py_DECREF(made);

@@ -155,6 +155,13 @@ __device__ __forceinline__ u32x4 get(const uint8_t* from) {
   return *reinterpret_cast<const u32x4*>(from);
 }
 
+// The same values; a signalling NaN, which least and largest would answer with, is a
+// quiet one, which they pass over.
+__device__ __forceinline__ void quiet(float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __builtin_canonicalizef(v[e]);
+}
+
 struct Store {
   const uint8_t* x[2];  // keys, values (bf16)
   uint8_t* kv[2];
@@ -210,7 +217,10 @@ __global__ __launch_bounds__(kThreads) void store_kv_kernel(Store p) {
         } else {
           float v[8], scale;
           bf16x8_to_float(raw[u][w], v);
-          const u32x2 codes = quantise<LPV>(v, 1.0f, ok, scale, [&](float (&f)[8]) { bf16x8_to_float(raw[u][w], f); });
+          const u32x2 codes = quantise<LPV>(v, 1.0f, ok, scale, [&](float (&f)[8]) {
+            bf16x8_to_float(raw[u][w], f);
+            quiet(f);
+          });
           if (ok) {
             put<FAR>(codes, p.kv[w] + at + i * kDim + 8 * sub);
             if (sub == 0) *reinterpret_cast<float*>(p.ks[w] + page * p.s.ks_page + head[u] * p.s.ks_head + 4 * i) = scale;
@@ -314,6 +324,7 @@ __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
         }
       } else {
         bf16x8_to_float(raw[i], v);
+        quiet(v);
       }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
@@ -518,6 +529,8 @@ int page_bounds(const void* k_pages, const float* kscale, const int32_t* page_ta
   if (!head_dim_ok(head_dim)) return IDX_ERR_UNSUPPORTED;
   int st = validate_rows(rows, kv_heads, table_width, num_tables, page_table_row_stride);
   if (st == IDX_OK) st = validate_kv_strides(KEY, kv_heads, head_dim, num_pages, s);
+  const int64_t side = ((int64_t)kv_heads + kWaves - 1) / kWaves;
+  if (st == IDX_OK && rows * side >= ((int64_t)1 << 32) / kThreads) st = IDX_ERR_SHAPE;  // (a launch has less than 2^32 threads)
   if (st != IDX_OK || rows == 0 || kv_heads == 0 || table_width == 0) return st;
   if (!page_table || !seqlens || !bounds) return IDX_ERR_NULL;
   st = validate_kv_pointers(KEY, kv_heads, k_pages, kscale, s);
@@ -538,7 +551,7 @@ int page_bounds(const void* k_pages, const float* kscale, const int32_t* page_ta
   (void)hipGetLastError();
   // The workgroups of one page of a row, then those of the next row: what the rows have
   // of a decode step so is all dies', and neighbours read neighbouring blocks.
-  p.side = (uint32_t)((kv_heads + kWaves - 1) / kWaves);
+  p.side = (uint32_t)side;
   int64_t y = table_width;
   const int64_t cap = (16 * (int64_t)device_cu_count() + (int64_t)rows * p.side - 1) / ((int64_t)rows * p.side);
   if (y > cap) y = cap;

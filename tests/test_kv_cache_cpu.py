@@ -113,6 +113,12 @@ def test_bounds_validation(raw, kw, status):
     assert call(raw, "idx_page_bounds_bf16", BOUNDS16, BOUNDS, **kw) == status
 
 
+@pytest.mark.parametrize("rows,heads", [((1 << 24), 1), (1 << 22, 16), (1 << 30, 1)])
+def test_bounds_of_more_rows_than_a_launch_has(raw, rows, heads):
+    assert call(raw, "idx_page_bounds_fp8", BOUNDS8, BOUNDS, rows=rows, heads=heads) == SHAPE
+    assert call(raw, "idx_page_bounds_bf16", BOUNDS16, BOUNDS, rows=rows, heads=heads) == SHAPE
+
+
 SCORES_ORDER = "q near pt rt tables sl out counts rows heads kvheads dim width pages pts stride first last stream"
 SCORES = dict(q=16, near=16, pt=4, rt=4, tables=1, sl=4, out=4, counts=4, rows=1, heads=8, kvheads=2, dim=128, width=2, pages=1,
               pts=2, stride=4, first=0, last=0, stream=None)

@@ -175,6 +175,25 @@ def test_store_values_that_are_no_numbers(lib):
     assert k.view(torch.uint8)[0, 0, 4, 0] == 0x80
 
 
+@pytest.mark.parametrize("bits", [0x7F81, 0xFF81, 0x7FBF, 0x7FC0, 0xFFFF])
+def test_store_nan_of_any_bits(lib, bits):
+    """Wherever it stands in a vector, and whatever its bits, a NaN has no part in the amount."""
+    x = torch.randn((64, 1, 64), generator=torch.Generator().manual_seed(9)).to(BF16)
+    whole = x.clone()
+    for t in range(64):
+        x.view(torch.int16)[t, 0, t] = bits - 0x10000 if bits >= 0x8000 else bits
+        whole[t, 0, t] = 0
+    amax = whole.float().abs().amax(-1)[:, 0]
+    k, v, (ks, vs) = make_pools(torch.Generator().manual_seed(0), 1, 1, 64, True, "apart")
+    lib.idx_store_kv_fp8(x.cuda(), whole.cuda(), torch.arange(64).cuda(), k, v, ks, vs)
+    assert torch.equal(ks.cpu()[0, 0], amax / 448) and torch.equal(vs.cpu()[0, 0], amax / 448)
+    codes, others = k.view(torch.uint8).cpu()[0, 0], v.view(torch.uint8).cpu()[0, 0]
+    at = torch.arange(64)
+    assert (codes[at, at] == (0xFE if bits >= 0x8000 else 0x7E)).all()
+    codes[at, at] = others[at, at]
+    assert torch.equal(codes, others)  # (both ways round the quotient correctly)
+
+
 # --- bounds
 
 
@@ -246,6 +265,18 @@ def test_bounds_values_that_are_no_numbers(lib):
         k[:, :, 40:, 30:] = float("nan")
         k[:, 0, :, 1] = float("inf")
     bounds_case(lib, torch.Generator().manual_seed(5), [40, 64 + 20, 3], None, 2, 64, False, 2, spoil=spoil)
+
+
+def test_bounds_signalling_nan(lib):
+    """Every bit pattern of a NaN, of either sign, is one."""
+    def spoil(k):
+        bits = k.view(torch.int16)
+        bits[:, 0, 3, ::2] = 0x7F81
+        bits[:, 0, 4, ::3] = 0xFF81 - 0x10000
+        bits[:, 1, :, 5] = 0x7FBF
+        bits[:, 1, 7, :] = 0xFFC0 - 0x10000
+        bits[:, :, 60:, 1:9] = 0x7F81  # past the end of a row's last page
+    bounds_case(lib, torch.Generator().manual_seed(6), [40, 64 + 20, 3], None, 2, 64, False, 2, spoil=spoil)
 
 
 # --- scores
@@ -360,6 +391,20 @@ def test_scores_bound_every_key(lib):
 
 
 # --- together, on another stream, in a graph
+
+
+def test_stream_of_another_device(lib):
+    """A stream of another device than the tensors' is refused."""
+    class Elsewhere:
+        cuda_stream, device_index = 0, 1
+
+    s = torch.zeros(1, dtype=I64, device="cuda")
+    lens = torch.zeros(1, dtype=I32, device="cuda")
+    table = torch.zeros((1, 1), dtype=I32, device="cuda")
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        lib.idx_plan_batch(lens, lens, lens, table, s, stream=Elsewhere())
+    with pytest.raises(TypeError):
+        lib.idx_plan_batch(lens, lens, lens, table, s, stream="elsewhere".split())
 
 
 def test_on_another_stream_and_in_a_graph(lib):
