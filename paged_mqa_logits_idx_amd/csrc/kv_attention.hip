@@ -168,10 +168,10 @@ __device__ __forceinline__ int32_t pages_of(const Attend& a, int32_t L) {
 // share would end inside a unit (`uneven`).  A unit is
 // not cut into more than 32 * HW pieces by far: joining them costs more than a
 // larger share (one row of 8 units of 128 pages: 64 pieces each 14.8 us, 32 pieces
-// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).  Pieces of 64 heads are as many
-// bytes as a page of their keys and values: shares of up to `few` pages are made
-// by half the workgroups (8 rows of up to 64 and 128 pages 16.6 and 18.1 us by all, 13.9
-// and 16.7 by half; 32 rows 21.6 and 27.1, and 20.8 and 29.4).
+// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).  Pieces of 64 heads are about as many
+// bytes as a page of their keys and values: shares of up to `few` (6) pages are made
+// by half the workgroups (bf16, 8 rows of up to 64 and 128 pages 17.0 and 18.4 us by all, 14.3
+// and 17.1 by half; 64 rows of 64 pages in e4m3, shares of 5 and 10 pages, 26.8 and 30.4).
 template <class F>
 __device__ __forceinline__ Cut cut_of(const Attend& a, int32_t total, F uneven) {
   const auto up = [](uint32_t x, uint32_t by) { return (int32_t)((x + by - 1) / by); };
@@ -827,7 +827,7 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   s.slack = (int)(65536 / page_bytes);
   const int64_t want = (units * most + s.least - 1) / s.least + units;  // (a unit's last piece may be short)
   s.shares = (int)(want < workgroups ? want : workgroups);
-  if (s.hw == kWaves && s.shares > device_cu_count()) s.few = (int)(196608 / page_bytes);
+  if (s.hw == kWaves && s.shares > device_cu_count()) s.few = 6;
   s.bytes = padded(8 + 4 * ((int64_t)rows + 1)) + padded(2 * (int64_t)s.shares * 16 * s.hw * 8) +
             2 * (int64_t)s.shares * s.hw * head_dim * 64;
   return s;
