@@ -42,7 +42,7 @@
 // the matrix units have 5 and 7 %.  One row of 8192 positions, 34 MB, takes 13.2: 6 of memory,
 // the way to the first keys (length, page id, keys one after the other) and a second
 // kernel, 2.5 and a launch.  64 heads of one key head, 64 rows of up to 8192 bf16
-// positions, 168 MB, 50 us: the pieces' outputs are a fifth of what is moved, and joining
+// positions, 168 MB, 42 to 48 us: the pieces' outputs are a fifth of what is moved, and joining
 // them 8 us.  64 positions of one row 5 us, a launch and three trips to memory: code is
 // kept short where it runs once, since the first run of each line waits for it (an end
 // unrolled by heads, of 10 KB, cost a call of 64 heads 12 us).
