@@ -451,3 +451,35 @@ def test_far_positions_keep_what_float64_leaves(lib, halves, power):
     off = np.concatenate([off, off], -1) if halves else np.repeat(off, 2, -1)
     # (assert_near_bf16 takes F32 of `size`)
     assert_near_bf16(out, y, size * (1 + off[:, None] / F32))
+
+
+@pytest.mark.parametrize("bits", [0x7F81, 0xFF81, 0x7FBF, 0x7FC0, 0xFFFF])
+@pytest.mark.parametrize("dim", [128, 512])
+@pytest.mark.parametrize("opts", [None, {}, {"halves": True}, {"leading": True}])
+def test_store_nan_of_any_bits(lib, dim, opts, bits):
+    """Without a norm, and where no rotation touches it: a NaN has no part in the
+    amount, whatever its bits and wherever it stands, and becomes +-448; the other
+    values are stored as without it.  (The largest value of each vector stands
+    before the NaN, among the 8 that a lane has.)"""
+    rng = np.random.default_rng(dim)
+    rope = 0 if opts is None else 64
+    first = 64 if opts and opts.get("leading") else 0  # of the values that are not rotated
+    at = torch.arange(first, first + dim - rope)
+    n, pages = len(at), -(-dim // PAGE)
+    x = torch.from_numpy(rng.standard_normal((n, dim))).to(torch.bfloat16)
+    t = torch.arange(n)
+    x[t, at // 8 * 8] = 10.0
+    whole = x.clone()
+    whole[t, at] = 0.0
+    x.view(torch.int16)[t, at] = bits - 0x10000 if bits >= 0x8000 else bits
+    freq = inv_freq(32).cuda() if rope else None
+    positions = torch.from_numpy(rng.integers(0, 1 << 20, n)).cuda() if rope else None
+    slots = torch.from_numpy(rng.permutation(pages * PAGE)[:n])
+    call = dict(norm=False, **(opts or {}))
+    codes, scales = stored_bytes(lib, x.cuda(), positions, freq, None, slots.cuda(), pages, dim, **call)
+    others, want = stored_bytes(lib, whole.cuda(), positions, freq, None, slots.cuda(), pages, dim, **call)
+    assert np.array_equal(scales, want)
+    s, i = slots.numpy(), at.numpy()
+    assert (codes[s, i] == (0xFE if bits >= 0x8000 else 0x7E)).all()
+    codes[s, i] = others[s, i]
+    assert np.array_equal(codes, others)
