@@ -8,7 +8,8 @@ compiled ones) and pass their addresses and sizes through ctypes.  torch supplie
 device memory and streams.
 
 The library must be built in-tree first (``python paged_mqa_logits_idx_amd/_build.py``
-or ``__graft_entry__.build()``); importing this module without it raises.
+or ``__graft_entry__.build()``); importing this module without it raises.  Where the
+compiled marshalling does not load, the functions that use it raise when called.
 """
 from __future__ import annotations
 
@@ -17,11 +18,23 @@ from pathlib import Path
 
 import torch  # loads the HIP runtime the library binds to (same soname)
 
+
+class _Missing:
+    """In the place of the compiled marshalling where it does not load (not built, or
+    built for another Python or torch): its calls say so, the others do without it."""
+
+    def __init__(self, error):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError(f"{Path(__file__).resolve().parent / '_binding.so'}: {self._error}; build it first "
+                          "(python paged_mqa_logits_idx_amd/_build.py)") from self._error
+
+
 try:
     from . import _binding  # compiled with the library
 except ImportError as e:
-    raise ImportError(f"{Path(__file__).resolve().parent / '_binding.so'}: {e}; build it first "
-                      "(python paged_mqa_logits_idx_amd/_build.py)") from e
+    _binding = _Missing(e)
 
 LIB_PATH = Path(__file__).resolve().parent / "libidx_paged_mqa.so"
 
@@ -767,9 +780,10 @@ def _make_workspace(nbytes, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-_binding.bind(_make_workspace, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
-    "idx_plan_batch", "idx_store_kv_fp8", "idx_store_kv_bf16", "idx_page_bounds_fp8", "idx_page_bounds_bf16",
-    "idx_page_scores", "idx_kv_attention_fp8", "idx_kv_attention_bf16", "idx_kv_attention_workspace")))
+if not isinstance(_binding, _Missing):
+    _binding.bind(_make_workspace, *(ctypes.cast(getattr(_lib, name), ctypes.c_void_p).value for name in (
+        "idx_plan_batch", "idx_store_kv_fp8", "idx_store_kv_bf16", "idx_page_bounds_fp8", "idx_page_bounds_bf16",
+        "idx_page_scores", "idx_kv_attention_fp8", "idx_kv_attention_bf16", "idx_kv_attention_workspace")))
 
 
 def _done(name, status, check) -> int:

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import re
 import subprocess
+import sys
 from pathlib import Path
 
 import pytest
@@ -292,3 +293,34 @@ def test_binding_takes_tensors_alone():
         attend(num_pages=1.5)
     with pytest.raises(TypeError, match="arguments"):
         b._binding.plan_batch(1)
+
+
+def test_other_operators_without_the_compiled_marshalling():
+    """The indexer's and the latent cache's calls do not need _binding.so; those that do
+    say so when they are called."""
+    code = """
+import sys
+sys.modules["paged_mqa_logits_idx_amd._binding"] = None  # as if it were not built
+import torch
+import paged_mqa_logits_idx_amd as b
+assert b.idx_abi_version() > 0 and b.idx_kv_attention_workspace(0, 8, 2, 128, 8) == 0
+try:
+    b.idx_topk_logits(torch.zeros((1, 8)), torch.zeros((1,), dtype=torch.int64), torch.zeros((1, 2), dtype=torch.int32))
+except ValueError as e:
+    assert "lens" in str(e) or "int32" in str(e), e
+else:
+    raise AssertionError("a wrong type went through")
+z = torch.zeros((1, 1), dtype=torch.int32)
+for call in (lambda: b.idx_plan_batch(z[0], z[0], z[0], z), lambda: b.idx_store_kv_bf16(z, z, z, z, z),
+             lambda: b.idx_page_bounds_bf16(z, z, z, z), lambda: b.idx_page_scores(z, z, z, z, z),
+             lambda: b.idx_kv_attention_bf16(z, z, z, z, None, z, z, scale=1.0)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_binding.so" in str(e) and "build" in str(e), e
+    else:
+        raise AssertionError("went on without it")
+print("fine")
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert done.returncode == 0 and done.stdout.strip().endswith("fine"), done.stderr
