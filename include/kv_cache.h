@@ -196,8 +196,9 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
  * in the result, whatever they hold.  A page of S_bh whose id lies outside [0,
  * num_pages), or whose row's table index lies outside [0, num_tables), is not read:
  * it makes out and lse of the group's heads NaN.  Scores, sums and outputs are
- * float32 until the one rounding of out; the probability of a position (times the
- * value's e4m3 scale) is rounded to bf16 for its product with v_p.
+ * float32 until the one rounding of out, scores times log2(e) (beyond +-2.35e38 they
+ * are infinite); the probability of a position (times the value's e4m3 scale) is
+ * rounded to bf16 for its product with v_p.
  *
  *   q          bf16 [rows][num_heads][head_dim], contiguous, 16-byte aligned.
  *   page_table, row_table, num_tables, page_table_row_stride

@@ -53,7 +53,7 @@
 namespace {
 
 constexpr float kLazy = 8.0f;     // base-2 logits that a tile's maximum exceeds its reference by where that moves
-constexpr float kNone = -3e38f;   // a reference before the first
+constexpr float kNone = -3.4028234663852886e38f;  // a reference before the first: no logit is less but -infinity
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 struct Cut {

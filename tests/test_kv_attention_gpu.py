@@ -482,3 +482,47 @@ def test_heads_are_pools_of_the_other_operators(lib):
         lib.idx_load_slots_fp8(at, scale_at, slots, back, **stride)
         want = k.view(torch.uint8)[page, h, pos].view(torch.float8_e4m3fn).float() * ks[page, h, pos][:, None]
         assert torch.equal(back, want.to(BF16))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("heads,width,sinks", [(2, 2, False), (2, 60, True), (40, 2, False), (40, 60, False), (128, 60, False)])
+def test_scores_at_the_low_end(lib, fp8, heads, width, sinks):
+    """Logits next to float32's lowest value are numbers as others: positions of the same
+    logit share the weight, a larger one has it all.  (A product of one value of q and one
+    of k: -1.3125 * 2^127 with the scale, and log2(e) times that, -1.8935 * 2^127, in base
+    2; float32 ends at -2 * 2^127.)"""
+    n = 64 * width - 7
+    c = Case(60, [n, n, 0], heads, 2, 64, width, fp8, scale=0.75, sinks=sinks)
+    x = -1.3125 * 2.0 ** 127
+    c.q.zero_()
+    c.q[..., 5] = -1.75 * 2.0 ** 64
+    if fp8:
+        c.k.view(torch.uint8).zero_()
+        c.k.view(torch.uint8)[..., 5] = 0x38  # 1.0
+        c.scales[0].fill_(2.0 ** 63)
+    else:
+        c.k.zero_()
+        c.k[..., 5] = 2.0 ** 63
+    if sinks:
+        c.sinks.fill_(-float("inf"))
+    c.run(lib)
+    keys = f64(c.v) if not fp8 else values_of(c.v, c.scales[1])
+    for b in range(2):
+        pages = [int(j) for j in c.table[b]]
+        v = np.concatenate([keys[p] for p in pages], 1)[:, :n]  # [kv heads, n, dim]
+        mean, size = v.mean(1).repeat(heads // 2, 0), np.abs(v).mean(1).repeat(heads // 2, 0)
+        # float32 sums of n products (of probabilities 1 and, in e4m3, scales rounded to
+        # bf16, 2^-8 of each), one rounding of the result to bf16
+        err = size * ((2.0 ** -8 if fp8 else 0) + (n + 8) * 2.0 ** -24) + np.abs(mean) * 2.0 ** -8
+        assert (np.abs(f64(c.out[b]) - mean) <= err).all()
+        assert np.abs(f64(c.lse[b]) / x - 1).max() <= 2.0 ** -21
+    assert (c.out[2] == 0).all() and torch.isneginf(c.lse[2]).all()
+    page, at = int(c.table[1, width - 1]), 11  # a smaller amount: the largest logit of row 1
+    if fp8:
+        c.scales[0][page, :, at] *= 0.9375
+    else:
+        c.k[page, :, at, 5] *= 0.9375
+    c.run(lib)
+    want = keys[page, :, at].repeat(heads // 2, 0)
+    assert (np.abs(f64(c.out[1]) - want) <= np.abs(want) * (2.0 ** -7 if fp8 else 0)).all()
+    assert np.abs(f64(c.lse[1]) / (0.9375 * x) - 1).max() <= 2.0 ** -21
