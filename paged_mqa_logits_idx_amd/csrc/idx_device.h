@@ -209,7 +209,8 @@ struct Closing {
   float by, half, lse;
 };
 __device__ __forceinline__ Closing close_sum(float m, float z, float sink) {
-  const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : top;
+  // (finite, so that a sink of infinity leaves nothing but itself, not a NaN)
+  const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.0f : fminf(top, 3.4028234663852886e38f);
   Closing c;
   c.half = __builtin_amdgcn_exp2f(0.5f * (m - ref));
   const float total = z * c.half * c.half + __builtin_amdgcn_exp2f(sink - ref);

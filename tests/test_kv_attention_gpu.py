@@ -526,3 +526,18 @@ def test_scores_at_the_low_end(lib, fp8, heads, width, sinks):
     want = keys[page, :, at].repeat(heads // 2, 0)
     assert (np.abs(f64(c.out[1]) - want) <= np.abs(want) * (2.0 ** -7 if fp8 else 0)).all()
     assert np.abs(f64(c.lse[1]) / (0.9375 * x) - 1).max() <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("lengths,width,k", [([100, 0, 300], 5, None), ([100, 0, 5000], 80, None), ([300, 0, 5000], 80, 3)])
+def test_sink_of_infinity(lib, fp8, lengths, width, k):
+    """exp(x) / inf = 0: nothing is left of the positions, and ln z is infinite; the
+    other heads have the bits that they have without it."""
+    c = Case(61, lengths, 8, 2, 64, width, fp8, k=k, sinks=True)
+    c.run(lib)
+    plain, plain_lse = c.out.clone(), c.lse.clone()
+    c.sinks[5] = float("inf")
+    c.run(lib)
+    assert (c.out[:, 5] == 0).all() and torch.isposinf(c.lse[:, 5]).all()
+    others = [0, 1, 2, 3, 4, 6, 7]
+    assert torch.equal(c.out[:, others], plain[:, others]) and torch.equal(c.lse[:, others], plain_lse[:, others])

@@ -591,3 +591,26 @@ def test_no_numbers_stay_where_they_are(lib, fp8, rows):
     assert out[none].isnan().all() and lse[none].isnan().all()
     assert torch.equal(out[~none].view(torch.int16), plain[~none].view(torch.int16))
     assert torch.equal(lse[~none].view(torch.int32), plain_lse[~none].view(torch.int32))
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("rows,k", [(2, None), (2, 40), (530, None)])
+def test_sink_of_infinity(lib, fp8, rows, k):
+    """exp(x) / inf = 0: nothing is left of the positions, and ln z is infinite; the
+    other heads have the bits that they have without it."""
+    rng = np.random.default_rng(8)
+    heads, width = 6, 4
+    cache = Cache(rng, 9, fp8)
+    table = np.stack([rng.permutation(8)[:width] for _ in range(rows)]).astype(np.int32)
+    lengths = rng.integers(1, width * PAGE + 1, rows)
+    lengths[1] = 0
+    selected = None if k is None else torch.from_numpy(np.stack([some(rng, int(n), k, k) for n in lengths]))
+    q = queries(rng, rows, heads)
+    sinks = torch.from_numpy(rng.standard_normal(heads).astype(np.float32))
+    args = (cache, q, torch.from_numpy(table), selected, torch.from_numpy(lengths.astype(np.int32)))
+    plain, plain_lse = call(lib, *args, sinks=sinks)
+    sinks[4] = float("inf")
+    out, lse = call(lib, *args, sinks=sinks)
+    assert (out[:, 4] == 0).all() and torch.isposinf(lse[:, 4]).all()
+    others = [0, 1, 2, 3, 5]
+    assert torch.equal(out[:, others], plain[:, others]) and torch.equal(lse[:, others], plain_lse[:, others])
