@@ -541,3 +541,70 @@ def test_sink_of_infinity(lib, fp8, lengths, width, k):
     assert (c.out[:, 5] == 0).all() and torch.isposinf(c.lse[:, 5]).all()
     others = [0, 1, 2, 3, 4, 6, 7]
     assert torch.equal(c.out[:, others], plain[:, others]) and torch.equal(c.lse[:, others], plain_lse[:, others])
+
+
+def few_long_rows(rows, pages, width):
+    """Rows of up to two pages, and some of up to `pages`."""
+    lengths = [(37 * b) % 129 for b in range(rows)]
+    for i, p in enumerate(pages):
+        lengths[(i * rows) // len(pages) + 1] = 64 * p - 13 * i
+    return lengths
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("rows,group,kv_heads,dim", [(260, 1, 8, 128), (260, 20, 8, 64), (260, 40, 8, 64), (260, 3, 8, 256), (131, 100, 8, 64)])
+def test_whole_units_of_many_pages(lib, rows, group, kv_heads, dim, fp8):
+    """More units than are cut, some of more pages than the 64 that are looked up
+    early: all pages, and lists with entries to skip and pages outside the pool on
+    both sides of the 64th."""
+    width = 200
+    lengths = few_long_rows(rows, [64, 65, 129, 200, 66], width)
+    assert lib.idx_kv_attention_workspace(rows, kv_heads * group, kv_heads, dim, width) == 0
+    Case(70, lengths, kv_heads * group, kv_heads, dim, width, fp8, tables=1, sinks=True).check(lib)
+    Case(71, lengths, kv_heads * group, kv_heads, dim, width, fp8, tables=1, bad=[(0, 65, -1), (0, 199, 1 << 20)]).check(lib)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("rows,group,kv_heads,dim", [(260, 2, 8, 128), (260, 33, 8, 64), (64, 8, 8, 128)])
+def test_whole_units_of_long_lists(lib, rows, group, kv_heads, dim, fp8):
+    width, k = 150, 140
+    lengths = few_long_rows(rows, [150, 64, 141, 149, 100], width)
+    rng = np.random.default_rng(rows)
+    picks = np.full((rows, kv_heads, k), -1)
+    for b, n in enumerate(lengths):
+        count = -(-n // PAGE)
+        for h in range(kv_heads):
+            some = np.sort(rng.permutation(count)[:k])
+            picks[b, h, : len(some)] = some
+    long = int(np.argmax(lengths))
+    for at in (3, 63, 64, 65, 127, 128, 139):  # to be skipped
+        picks[long, at % kv_heads, at] = rng.choice([-1, -9, width, 2 ** 31 - 1])
+    c = Case(72, lengths, kv_heads * group, kv_heads, dim, width, fp8, tables=1, selected=picks, sinks=True)
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert lib.idx_kv_attention_workspace(rows, kv_heads * group, kv_heads, dim, width, k) == 0
+    c.check(lib)
+    picks[long, 1, 2], picks[long, 2, 100] = 70, 71  # pages that are outside the pool
+    Case(73, lengths, kv_heads * group, kv_heads, dim, width, fp8, tables=1, selected=picks, bad=[(0, 70, 1 << 20), (0, 71, -5)]).check(lib)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("group,dim", [(1, 64), (8, 128), (16, 256), (32, 128), (20, 64), (64, 64), (64, 128), (50, 256)])
+def test_past_the_caches(lib, group, dim, fp8):
+    """Calls whose tables may name 256 MiB and more, few and many pages to a row, cut
+    and whole."""
+    kv_heads, rows = 2, 9
+    page_bytes = 2 * PAGE * dim * (1 if fp8 else 2)
+    width = -(-(1 << 28) // (rows * kv_heads * page_bytes))
+    lengths = [1, 64 * 40 - 7, 0, 640, 65, 3000, 64, 31, 2000]
+    gen_width = 48  # the pool has pages for these columns; the others of the table are never live
+    for k in (None, 30):
+        c = Case(80 + group, lengths, kv_heads * group, kv_heads, dim, gen_width, fp8, tables=1, k=k, sinks=True)
+        wide = torch.full((1, width), -1, dtype=I32, device="cuda")
+        wide[:, :gen_width] = c.table
+        c.table = wide
+        if k is not None:
+            wider = torch.full((rows, kv_heads, width), -1, dtype=I32, device="cuda")
+            wider[..., :k] = c.selected
+            c.selected = wider
+        assert rows * kv_heads * width * page_bytes >= 1 << 28
+        c.check(lib)

@@ -467,3 +467,120 @@ def test_on_another_stream_and_in_a_graph(lib):
         assert (eager["lens"].cpu() == eager["cached"].cpu() + 1).all()
         advance(eager)
         advance(static)
+
+
+# --- more work than a launch has workgroups: every loop goes round again
+
+
+def cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("requests,n,each", [(1000, 140000, 13000), (2000, 600000, 600)])
+def test_plan_of_more_rows_than_its_grid(lib, requests, n, each):
+    """Rows, and for long prompts new pages, past those of the first round."""
+    threads = 256 if requests <= 1024 else 1024
+    round_ = 2 * cus() * threads
+    rng = np.random.default_rng(requests)
+    added = rng.integers(each // 2, each + 1, requests)
+    cached = rng.integers(0, 200, requests)
+    width = -(-(each + 200) // PAGE) + 1
+    pages = int((-(-(cached + added) // PAGE) - -(-cached // PAGE)).sum())
+    assert round_ < n <= added.sum() and (threads > 256 or pages > round_)
+    plan_case(lib, cached, added, pages - 5, width, n)
+
+
+def test_plan_of_pages_alone(lib):
+    """More new pages than the threads of the one workgroup that hands them out."""
+    requests, width = 300, 40
+    added = np.full(requests, 64 * width - 3)
+    cached = np.arange(requests) % 3
+    free = np.random.default_rng(3).permutation(requests * width).astype(np.int32)
+    table = torch.full((requests, width), -7, dtype=I32, device="cuda")
+    lib.idx_plan_batch(i32(cached), i32(added), i32(free), table)
+    want = ref.plan(cached, added, free, np.full((requests, width), -7), 0)
+    assert want[6] > 1024 and (table.cpu().numpy() == want[0]).all()
+
+
+@pytest.mark.parametrize("fp8,dim,heads", [(True, 64, 4), (True, 128, 8), (True, 256, 2), (False, 64, 4), (False, 128, 8), (False, 256, 2)])
+@pytest.mark.parametrize("size", ["below", "at", "round"])
+def test_store_of_many_tokens(lib, fp8, dim, heads, size):
+    """Just below and just at the 16 MiB of outputs that pass the caches by, and more
+    vectors than one round of the grid takes."""
+    far = -(-(1 << 24) // (2 * dim if fp8 else 4 * dim))        # vectors
+    round_ = 16 * cus() * 2 * 4 * (64 // (dim // 8))
+    vectors = {"below": far - heads, "at": far, "round": round_ + 5 * heads}[size]
+    n = vectors // heads
+    assert n * heads == vectors and (vectors >= far) == (size != "below") and (vectors > round_) == (size == "round")
+    gen = torch.Generator(device="cuda").manual_seed(dim + heads)
+    pages = -(-n // PAGE) + 2
+    if fp8:
+        k, v = (torch.full((pages, heads, PAGE, dim), 0x3A, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+        scales = tuple(torch.full((pages, heads, PAGE), -3.0, device="cuda") for _ in range(2))
+    else:
+        k, v = (torch.full((pages, heads, PAGE, dim), 77.0, dtype=BF16, device="cuda") for _ in range(2))
+        scales = ()
+    x = (torch.randn((n, 2, heads, dim), generator=gen, device="cuda") * (torch.rand((n, 2, heads, 1), generator=gen, device="cuda") * 4)).to(BF16)
+    slots = torch.randperm(pages * PAGE, generator=gen, device="cuda")[:n]
+    slots[1], slots[n - 2] = -1, pages * PAGE
+    (lib.idx_store_kv_fp8 if fp8 else lib.idx_store_kv_bf16)(x[:, 0], x[:, 1], slots, k, v, *scales)
+    kept = (slots >= 0) & (slots < pages * PAGE)
+    page, at = slots[kept] // PAGE, slots[kept] % PAGE
+    rest = torch.ones((pages, PAGE), dtype=torch.bool, device="cuda")
+    rest[page, at] = False
+    rest = rest[:, None].expand(pages, heads, PAGE)
+    for i, pool in enumerate((k, v)):
+        want = x[kept, i]
+        if not fp8:
+            assert torch.equal(pool[page, :, at], want) and (pool[rest] == 77).all()
+            continue
+        assert_near_fp8(pool.view(torch.uint8)[page, :, at].reshape(-1, dim).cpu().numpy(), scales[i][page, :, at].reshape(-1).cpu().numpy(),
+                        f64(want).reshape(-1, dim), np.zeros((want.shape[0] * heads, dim)))
+        assert (pool.view(torch.uint8)[rest] == 0x3A).all() and (scales[i][rest] == -3).all()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("heads,dim", [(4, 64), (3, 128), (5, 256)])
+def test_bounds_of_more_pages_than_a_grid(lib, fp8, heads, dim):
+    """So many rows that each has one column of workgroups, which go along its pages:
+    rows of three tables, pages outside the pool among them."""
+    rows, width = 16 * cus() // -(-heads // 4) + 200, 7
+    assert rows * -(-heads // 4) >= 16 * cus() and width * heads > 4 * -(-heads // 4)
+    rng = np.random.default_rng(heads)
+    which = rng.integers(-1, 4, rows)
+    lengths = np.choose(np.clip(which, 0, 2), [64 * width, 64 * width - 40, 130])  # (rows of a table agree)
+    first = rng.integers(0, 130, rows)
+    first[:6] = 0
+    which[:6] = [0, 1, 2, 0, 1, 2]
+    lengths[:6] = [64 * width, 64 * width - 40, 130] * 2
+    bounds_case(lib, torch.Generator().manual_seed(heads), lengths, first, heads, dim, fp8, width, row_table=which)
+
+
+def test_scores_of_more_units_than_a_grid(lib):
+    """Units past the 2^20 of a round, whose bounds come to the LDS places of earlier ones."""
+    rows, heads, kv_heads, dim, width, pages = 64, 16, 8, 64, 16 * 9000, 50
+    blocks = -(-(-(-width // 16) * kv_heads) // 4)
+    assert rows * blocks > 1 << 20
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn((rows, heads, dim), generator=gen, device="cuda").to(BF16)
+    near = torch.randn((pages, kv_heads, 2, dim), generator=gen, device="cuda").sort(2).values.to(BF16)
+    table = torch.randint(0, pages + 1, (1, width), generator=gen, device="cuda").to(I32)  # (one id outside the pool)
+    lengths = torch.full((rows,), 64 * width, dtype=I32, device="cuda")
+    lengths[::3] -= 64 * 777 + 5
+    out = torch.full((rows, kv_heads, width), -5.0, device="cuda")
+    counts = torch.full((rows, kv_heads), -5, dtype=I32, device="cuda")
+    lib.idx_page_scores(q, near, table, lengths, out, counts, last_pages=1)
+    x = q.double().reshape(rows, kv_heads, 1, heads // kv_heads, dim)
+    lo, hi = (near[:, :, i].double().transpose(0, 1)[None, :, :, None] for i in range(2))  # [1, kv heads, pages, 1, dim]
+    best = torch.maximum(x * lo, x * hi)
+    want = torch.cat((best.sum(-1).amax(-1), torch.full((rows, kv_heads, 1), float("nan"), device="cuda")), 2)
+    err = (dim + 2) * 2.0 ** -24 * torch.cat((best.abs().sum(-1).amax(-1), torch.zeros((rows, kv_heads, 1), device="cuda")), 2)
+    at = table[0].long()
+    j = torch.arange(width, device="cuda")
+    for b in range(rows):
+        live = -(-int(lengths[b]) // PAGE)
+        assert (counts[b] == live).all()
+        assert torch.isneginf(out[b, :, live:]).all() and torch.isposinf(out[b, :, live - 1]).all()
+        inside = (j < live - 1) & (at < pages)
+        assert ((out[b].double() - want[b][:, at]).abs() <= err[b][:, at])[:, inside].all(), b
+        assert out[b][:, (j < live - 1) & (at == pages)].isnan().all()
