@@ -197,8 +197,9 @@ int idx_page_scores(const void* q, const void* bounds, const int32_t* page_table
  * num_pages), or whose row's table index lies outside [0, num_tables), is not read:
  * it makes out and lse of the group's heads NaN.  Scores, sums and outputs are
  * float32 until the one rounding of out, scores times log2(e) (beyond +-2.35e38 they
- * are infinite); the probability of a position (times the value's e4m3 scale) is
- * rounded to bf16 for its product with v_p.
+ * are infinite); the probability of a position (times the value's e4m3 scale) enters
+ * its product with v_p rounded to 16 bits (two bf16) where at most 16 query heads
+ * share a key head, to bf16 where more do.
  *
  *   q          bf16 [rows][num_heads][head_dim], contiguous, 16-byte aligned.
  *   page_table, row_table, num_tables, page_table_row_stride

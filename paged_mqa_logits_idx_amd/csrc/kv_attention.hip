@@ -28,9 +28,15 @@
 //   outputs  O^T += V^T P^T:  the lane's positions of two such blocks are its 8
 //            k-values, so P stays in registers; V^T comes out of LDS through the
 //            transposing reads in the same order.
-// Rounding: scores, exponentials, sums and outputs are float32; the products take
-// bf16 operands, which rounds the probability (times the value's e4m3 scale) once, by
-// 2^-8 of itself at most.  The denominator sums the unrounded probabilities.
+// Rounding: scores, exponentials, sums and outputs are float32, the denominator sums
+// unrounded probabilities; the products take bf16 operands.  Up to 16 heads (HW 1),
+// which memory bounds, a probability (times the value's e4m3 scale) goes in as bf16
+// and again as bf16 of what that leaves: 16 bits of it, for 0 to 2 % of the time (64
+// rows of up to 32768 positions bf16 823 -> 822 us, e4m3 453 -> 456; 32 selected pages
+// of each 82.2 -> 82.5 and 51.4 -> 52.3; one row of 64 positions 5.1 -> 5.3 and 5.8 ->
+// 6.1).  With more heads the waves' chains of products bound it, and it goes in
+// once, off by 2^-8 of itself at most: 64 rows of 64 heads of one key head and up to
+// 8192 positions would take 44.5 us for 42.6, in e4m3 42.1 for 37.8.
 //
 // Running maximum: a head's reference moves, and sums and outputs are rescaled,
 // only where a tile's maximum exceeds it by more than kLazy: probabilities reach 2^8
@@ -130,6 +136,7 @@ struct Form {
   static constexpr int kSteps = DIM / 32;   // of the scores' sums
   static constexpr int kParts = DIM / 16;   // blocks of 16 values
   static constexpr int kSubs = kTile / 16;  // blocks of 16 positions
+  static constexpr bool kFine = HW == 1;    // probabilities of 16 bits
 
   // Chunk c (16 bytes) of position r stands at place c ^ key(r) of its LDS row, so
   // that what 16 lanes (keys: one chunk of 16 positions) or 32 (values: one or two
@@ -409,7 +416,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
 
     f32x4 x[kSubs];        // of a tile's positions 16 * s + 4 * quad .. and head n: scores, then base-2 logits
     f32x4 ks[kSubs], vs[kSubs];
-    bf16x8 w[kSubs / 2];   // probabilities
+    bf16x8 w[kSubs / 2], rest[F::kFine ? kSubs / 2 : 1];  // probabilities, and what bf16 leaves of them
     // (All reads of a tile's keys, or of 32 positions' values, are asked for before the
     // first product: left to itself the compiler waits for each where it is used.)
     auto score = [&](int place) {
@@ -476,7 +483,9 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
         for (int e = 0; e < 4; ++e) {
           const float p = __builtin_amdgcn_exp2f(x[s][e] - ref);
           sum += p;
-          w[s / 2][4 * (s & 1) + e] = (__bf16)(KEY == kFp8 ? p * vs[s][e] : p);
+          const float y = KEY == kFp8 ? p * vs[s][e] : p;
+          w[s / 2][4 * (s & 1) + e] = (__bf16)y;
+          if constexpr (F::kFine) rest[s / 2][4 * (s & 1) + e] = (__bf16)(y - (float)(__bf16)y);
         }
     };
     auto add = [&](int place, int32_t left) {
@@ -509,6 +518,7 @@ __global__ __launch_bounds__(kThreads, (Form<KEY, DIM, HW>::kPerCu)) void kv_att
             v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(u[p][0], u[p][1], 0, 1, 2, 3, 4, 5, 6, 7));
           }
           acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, w[i], acc[p], 0, 0, 0);
+          if constexpr (F::kFine) acc[p] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, rest[i], acc[p], 0, 0, 0);
         }
       }
     };

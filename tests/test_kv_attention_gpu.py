@@ -608,3 +608,21 @@ def test_past_the_caches(lib, group, dim, fp8):
             c.selected = wider
         assert rows * kv_heads * width * page_bytes >= 1 << 28
         c.check(lib)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("heads,kv_heads,dim,k", [(64, 8, 128, None), (16, 1, 64, None), (3, 3, 256, None), (40, 8, 64, 17), (32, 2, 128, 5)])
+def test_probabilities_keep_16_bits(lib, heads, kv_heads, dim, k, fp8):
+    """Up to 16 query heads a key head: a probability p goes into its product with the
+    values as bf16(p) and bf16 of what that leaves, r = p - bf16(p), which float32 holds:
+    |r| <= 2^-8 p, and off by 2^-8 |r| at most, 2^-16 p.  The rest as in
+    assert_near_attention."""
+    c = Case(90 + dim, [640, 1200, 64, 1000, 70, 1280], heads, kv_heads, dim, 20, fp8, k=k, sinks=True)
+    c.run(lib)
+    torch.cuda.synchronize()
+    y, log, size, far = c.want()
+    one = far * (dim + 8) * 2.0 ** -24 + 2.0 ** -22
+    total = ((PAGE * k if k else 1280) / 4 + 64) * 2.0 ** -24
+    err = size * (2.0 ** -16 + 2 * one + total)[..., None] * (1 + 2.0 ** -7) + np.abs(y) * 2.0 ** -8 + 2.0 ** -133
+    d = np.abs(f64(c.out) - y)
+    assert (d <= err).all(), f"{(d > err).sum()} of {d.size} off, {(d / err).max():.2f} times as far"
