@@ -44,8 +44,8 @@
 //
 // What bounds it.  Long rows: memory.  64 rows of 8 heads of 128 (64 query heads) and
 // up to 32768 bf16 positions, 5.4 GB, take 820 to 945 us (the cards differ), 5.7 to 6.6
-// TB/s; 32 selected e4m3 pages of each, 279 MB, 47.5 us, 5.9 TB/s; of the SIMDs' cycles
-// the matrix units have 5 and 7 %.  One row of 8192 positions, 34 MB, takes 13.2: 6 of memory,
+// TB/s; 32 selected e4m3 pages of each, 279 MB, 48 us, 5.8 TB/s; of the SIMDs' cycles
+// the matrix units have 7 and 10 %.  One row of 8192 positions, 34 MB, takes 13.3: 6 of memory,
 // the way to the first keys (length, page id, keys one after the other) and a second
 // kernel, 2.5 and a launch.  64 heads of one key head, 64 rows of up to 8192 bf16
 // positions, 168 MB, 42 to 48 us: the pieces' outputs are a fifth of what is moved, and joining
@@ -175,7 +175,9 @@ __device__ __forceinline__ int32_t pages_of(const Attend& a, int32_t L) {
 // share would end inside a unit (`uneven`).  A unit is
 // not cut into more than 32 * HW pieces by far: joining them costs more than a
 // larger share (one row of 8 units of 128 pages: 64 pieces each 14.8 us, 32 pieces
-// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).  Pieces of 64 heads are about as many
+// 13.7, 16 pieces 14.1; of 256 pages 19.8, 19.6 and 18.4).  Rows of more than a wave's lanes
+// are not cut by units: 64 rows of 2 heads and 1024 bf16 positions take 18.8 us, 65 20.6, in
+// e4m3 15.3 and 18.3.  Pieces of 64 heads are about as many
 // bytes as a page of their keys and values: shares of up to `few` (6) pages are made
 // by half the workgroups (bf16, 8 rows of up to 64 and 128 pages 17.0 and 18.4 us by all, 14.3
 // and 17.1 by half; 64 rows of 64 pages in e4m3, shares of 5 and 10 pages, 26.8 and 30.4).
@@ -808,6 +810,8 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   if (rows == 0 || num_heads == 0) return s;
   const int32_t group = num_heads / kv_heads;
   while (s.hw < kWaves && 16 * s.hw < group) s.hw *= 2;
+  // (Two blocks read keys and values twice: 64 rows of one key head and up to 8192 bf16
+  // positions take 43 us with 64 query heads and 68 with 128, in e4m3 38 and 57.)
   s.blocks = (group + 16 * s.hw - 1) / (16 * s.hw);
   const int64_t units = (int64_t)rows * kv_heads * s.blocks;
   const int64_t most = k >= 0 && k < table_width ? k : table_width;  // pages of a unit
@@ -818,8 +822,14 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   // selected pages of e4m3 (279 MB) 59 -> 52 us, all of up to 512 pages of bf16 (5.4 GB)
   // 1025 -> 945, 64 rows of 2 heads with 32 queries each (335 MB) 75 -> 64.  But 33 rows of 8
   // heads of 64 and 17 pages (39 MB, three such in turn) 13.1 -> 14.8, 32 rows of one head
-  // with 64 queries (84 MB) 30.5 -> 36.7.
+  // with 64 queries (84 MB) 30.5 -> 36.7.  (What the tables may name decides, since the lengths
+  // are on the device: 8 rows of 8 heads and 1920 positions in tables of 4097 columns 21.5 ->
+  // 21.0 in bf16, 31 MB, but 17.4 -> 18.0 in e4m3, 16 MB.)
   s.once = s.blocks == 1 && units * most * page_bytes >= (int64_t)1 << 28;
+  // More units than four rounds of workgroups: whole.  Rows of like lengths gain by it: 300
+  // rows of 8 heads and 512 bf16 positions each 103 us, cut 119, of up to 512 and 2048 (a
+  // quarter of it the least) 73 and 250, cut 98 and 282.  One row of 32768 among 299 of 512
+  // loses: 346, cut 143.
   if (units > 4 * workgroups || units * most > INT32_MAX / 2) return s;
   // A unit of few pages is done by its workgroup before a second kernel could join its
   // pieces: 8 units of 4, 8 and 16 pages of 32 KB take 6.3, 8.4 and 12.3 us whole, 8.1,
@@ -827,10 +837,16 @@ Split split_of(int key, int32_t rows, int32_t num_heads, int32_t kv_heads, int32
   // 64 heads and 2, 4 and 8 pages 8.2, 11.8 and 19.2, and 9.5, 12.3 and 12.9.  So are units
   // that fill the device, unless rows may be far longer than others: 512 units of
   // up to 16, 32 and 128 pages (a quarter of it the least) 36, 71 and 257 us, cut 45, 77
-  // and 248.
+  // and 248.  (By the table's width: 64 rows of 8 heads and 256 positions take 17.0 us in tables
+  // of 4 columns, whole, and 17.9 in tables of 4097, cut; in e4m3 11.8 and 14.8.)
   if (most * s.hw <= 8 || (2 * units >= workgroups && most <= 32)) return s;
   // Selections are mostly of one size: whole units, where the last round of workgroups
-  // is full, nearly half full, or short (43008 bytes are 4 us of a workgroup's).
+  // is full, nearly half full, or short (43008 bytes are 4 us of a workgroup's).  Rows of 8
+  // heads in bf16, on 512 workgroups: 64, 30 and 48 rows of 32 pages 99, 55.5 and 76 us, cut
+  // 101, 63 and 81; cut, 4 rows of 32 and 10 of 64 15.4 and 40.5, whole 22.6 and 48.4.  It errs
+  // for 20 rows of 32 (cut 46.5, whole 41.5), where the last round is just over half full (33
+  // rows of 32 and 128 69 and 241, cut 63 and 190) and for lists of a few long rows among
+  // short ones (all of 32768 positions in 4 rows and of 1024 in 60 329, cut 136).
   const int64_t last = units % workgroups;
   if (k >= 0 && (last == 0 || (2 * workgroups - 5 * last) * most * page_bytes < 5 * workgroups * 43008)) return s;
   s.least = s.hw == 4 ? 1 : 2;

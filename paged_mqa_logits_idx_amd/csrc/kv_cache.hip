@@ -45,7 +45,8 @@ __device__ __forceinline__ Request request_of(const Plan& p, int32_t cached, int
 // the runs, then a walk along one; a new page's likewise.  Lengths of up to 4 requests
 // a thread are held in LDS for the walks (1024 requests and 65536 tokens 6.4 -> 5.4 us).
 // A launch and three trips to memory (lengths, the page, the store) are its time: 64
-// requests of one token 2.8 us.
+// requests of one token 2.8 us.  The grid goes by the rows: pages alone (n 0) are one
+// workgroup's, the 65536 of 1024 prompts of 4096 tokens 181 us, with their slots 42.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void plan_kernel(Plan p) {
   __shared__ int64_t tokens[THREADS + 1], pages[THREADS + 1];
@@ -172,8 +173,9 @@ constexpr int kStoreSteps = 2;
 // A vector of D values is D/8 lanes' (16 bytes of bf16 each); a wave takes
 // kStoreSteps groups of 64*8/D neighbouring vectors of the keys and the same of
 // the values, all loads under way at once.  Bound by memory: 32768 tokens of 8 bf16
-// heads of 128, keys and values, 268 MB, take 51.8 us, 5.2 TB/s (with one step 52.5, with four
-// 51.3; but 64 tokens to e4m3 3.5, 3.0 and 4.6).
+// heads of 128, keys and values, 268 MB, take 51.5 us, 5.2 TB/s, to e4m3, 204 MB, 42.6, 4.8
+// TB/s (with one step 52.8 and 43.8, with four 51.9 and 43.5; 4096 tokens 6.9 and 7.8, with one
+// 7.8 and 7.4, with four 6.6 and 8.3; 64 tokens 2.6 and 3.5, 2.4 and 2.9, 3.2 and 4.6).
 template <int KEY, int LPV, bool FAR>
 __global__ __launch_bounds__(kThreads) void store_kv_kernel(Store p) {
   constexpr int kDim = 8 * LPV, kVecs = 64 / LPV, kUnit = kStoreSteps * kVecs;
@@ -264,8 +266,9 @@ __device__ __forceinline__ float fold_apart(float v, F f) {
 // A wave takes a page of a head: a lane 16 bytes of a position, 1024 bytes of the
 // block a load, all of the block's loads under way at once; then the lanes that
 // have the same values of other positions.  Bound by memory: four prompts of up to
-// 32768 positions of 8 heads of 128 bf16 values, 199 MB, take 41.2 us, 4.8 TB/s (by columns
-// of 128 bytes, twice the waves, 42.5; of 64 bytes 61.6).
+// 32768 positions of 8 heads of 128 bf16 values, 199 MB, take 39.5 to 41.5 us, 4.8 to 5.0
+// TB/s (41.2 on the card on which columns of 128 bytes, twice the waves, took 42.5, of 64 bytes
+// 61.6); in e4m3, 106 MB, 32.2, 3.3 TB/s: twice the vector instructions a byte.
 template <int KEY, int DIM>
 __global__ __launch_bounds__(kThreads) void page_bounds_kernel(Bounds p) {
   constexpr int kPer = KEY == kFp8 ? 16 : 8;  // values of a lane
