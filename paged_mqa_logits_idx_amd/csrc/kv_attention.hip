@@ -31,10 +31,10 @@
 // Rounding: scores, exponentials, sums and outputs are float32, the denominator sums
 // unrounded probabilities; the products take bf16 operands.  Up to 16 heads (HW 1),
 // which memory bounds, a probability (times the value's e4m3 scale) goes in as bf16
-// and again as bf16 of what that leaves: 16 bits of it, for 0 to 2 % of the time (64
+// and again as bf16 of what that leaves: 16 bits of it, for 0 to 4 % of the time (64
 // rows of up to 32768 positions bf16 823 -> 822 us, e4m3 453 -> 456; 32 selected pages
-// of each 82.2 -> 82.5 and 51.4 -> 52.3; one row of 64 positions 5.1 -> 5.3 and 5.8 ->
-// 6.1).  With more heads the waves' chains of products bound it, and it goes in
+// of each 82.2 -> 82.5 and 51.4 -> 52.3; 33 rows of 17 e4m3 pages of heads of 64 13.4 ->
+// 14.0; one row of 64 positions 5.1 -> 5.3 and 5.8 -> 6.1).  With more heads the waves' chains of products bound it, and it goes in
 // once, off by 2^-8 of itself at most: 64 rows of 64 heads of one key head and up to
 // 8192 positions would take 44.5 us for 42.6, in e4m3 42.1 for 37.8.
 //
